@@ -401,6 +401,132 @@ sfr_status bsr_linear_bf16(const uint16_t* x, int64_t m, int64_t k, const int32_
                            const uint16_t* values, int64_t n, const uint16_t* bias, void* out, sfr_out_t out_dt,
                            void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The gated feed-forward block and its 8-bit and 4-bit forms.
+ *
+ *     h[m, j] = act(sum_k x[m, k] w[j, k]) * sum_k x[m, k] w[f + j, k]
+ *
+ * for bf16 x [m, k] and one weight w [2 f, k] whose first f rows are the gate
+ * projection and last f rows the up projection.  Activations saved for the
+ * backward pass, and weights for decoding, may be held in MX block formats
+ * (OCP Microscaling Formats v1.0: blocks of 32 values along a row share one
+ * power-of-two scale, a byte E8M0), which gfx950 converts in hardware.
+ *
+ * Unlike the FP8 entry points above, these carry NaN and infinities through as
+ * binary32 arithmetic does (an MX block that holds one decodes to NaN).
+ *
+ * Sizes: 0 <= m <= SFR_MAX_DIM; 0 < k, 2 f, n <= SFR_MAX_BLOCK_DIM; k % 32 == 0,
+ * f % 32 == 0, n % 16 == 0; a call whose output takes more than 2^24 tiles of
+ * 128 x 128 (64 x 64 up to 64 rows) is SFR_ERR_SHAPE.  Results do not depend on anything
+ * but the arguments: the order of every sum is fixed, no atomics.
+ * ---------------------------------------------------------------------------
+ */
+#define SFR_MAX_BLOCK_DIM ((int64_t)1 << 20)
+#define SFR_MX_BLOCK 32
+
+/* Element formats of the MX blocks.  E2M1 (4 bits: 0, .5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives) packs two values a byte, the even column in the low half. */
+typedef enum { SFR_MX_E4M3 = 0, SFR_MX_E5M2 = 1, SFR_MX_E2M1 = 2 } sfr_mx_t;
+
+/* Activation of the gated block: x s(x), the tanh form of GELU, max(x, 0). */
+typedef enum { SFR_ACT_SILU = 0, SFR_ACT_GELU_TANH = 1, SFR_ACT_RELU = 2 } sfr_act_t;
+
+/* How an activation is saved for the backward pass. */
+typedef enum { SFR_SAVE_NONE = 0, SFR_SAVE_BF16 = 1, SFR_SAVE_E4M3 = 2, SFR_SAVE_E5M2 = 3 } sfr_save_t;
+
+/*
+ * quantize_mx / dequantize_mx -- bf16 rows to MX blocks and back.
+ * For every block b of 32 columns of every row (fmax = 448, 57344 or 6):
+ *     amax        = max |x|                              (exact)
+ *     scale[r, b] = e + 127, e the smallest whole number >= -110 with
+ *                   amax <= fmax * 2^e                   (17 for a zero block)
+ *     q           = rne(x * 2^-e)                        (sign of zero kept; an
+ *                   element that would stand for 2^128 is the one below)
+ * A block with a NaN or an infinity gets scale 255 and zero codes.
+ * dequantize_mx writes q * 2^e, exactly (every such value is a bf16 number),
+ * and NaN for a block of scale 255.  Deterministic, bit-exact.
+ *
+ *   x, out  [rows, cols] bf16 bits.
+ *   q       [rows, cols] bytes, or [rows, cols / 2] for SFR_MX_E2M1.
+ *   scale   [rows, cols / 32] bytes.
+ * Sizes: 0 <= rows <= SFR_MAX_DIM, 0 < cols <= SFR_MAX_DIM, cols % 32 == 0.
+ * rows == 0 is a no-op.
+ */
+sfr_status quantize_mx(const uint16_t* x, int64_t rows, int64_t cols, sfr_mx_t dt, uint8_t* q, uint8_t* scale,
+                       void* stream);
+sfr_status dequantize_mx(const uint8_t* q, const uint8_t* scale, int64_t rows, int64_t cols, sfr_mx_t dt,
+                         uint16_t* out, void* stream);
+
+/*
+ * gated_linear_bf16 -- the gated block's forward pass in one launch: both
+ * projections accumulate in binary32, h is formed from the unrounded sums g, u
+ * and rounded once to bf16.  With a checkpoint, [g | u] is written as well:
+ * bf16 values, or MX blocks quantized from the binary32 sums by the rule of
+ * quantize_mx.
+ *
+ *   x        [m, k], w [2 f, k], h [m, f]: bf16 bits.
+ *   save     SFR_SAVE_NONE: gu and gu_scale are not used (NULL).
+ *   gu       [m, 2 f] bf16 bits (SFR_SAVE_BF16) or bytes (SFR_SAVE_E4M3 / _E5M2).
+ *   gu_scale [m, 2 f / 32] bytes for the 8-bit forms, else not used.
+ * m == 0 is a no-op.
+ */
+sfr_status gated_linear_bf16(const uint16_t* x, int64_t m, int64_t k, const uint16_t* w, int64_t f, sfr_act_t act,
+                             uint16_t* h, sfr_save_t save, void* gu, uint8_t* gu_scale, void* stream);
+
+/*
+ * gated_linear_bf16_backward -- its gradients, from the saved [g | u] and x:
+ *     dg = dh * u * act'(g),  du = dh * act(g)        (binary32, rounded to bf16)
+ *     dx[m, k] = sum_j dg[m, j] w[j, k] + du[m, j] w[f + j, k]
+ *     dw[j, k] = sum_m dg[m, j] x[m, k],  dw[f + j, k] = sum_m du[m, j] x[m, k]
+ * (binary32 sums, rounded once to bf16).  relu'(0) = 0.
+ *
+ *   dh        [m, f] bf16 bits.
+ *   gu, gu_scale, gu_save   as gated_linear_bf16 wrote them.
+ *   x, x_scale, x_save      [m, k]: bf16 bits (SFR_SAVE_BF16, x_scale not used)
+ *                           or quantize_mx's codes and scales.
+ *   dx [m, k], dw [2 f, k]  bf16 bits, written; either may be NULL (not computed;
+ *                           x is not read without dw, w not without dx).
+ *   workspace  device scratch of at least sfr_gated_backward_workspace_bytes(
+ *              m, k, f, x_save) bytes, overwritten; calls that may run at the
+ *              same time need distinct workspaces.
+ * m == 0 writes zeros to dw.  SFR_SAVE_NONE is SFR_ERR_DTYPE; a small
+ * workspace is SFR_ERR_SHAPE.
+ */
+sfr_status gated_linear_bf16_backward(const uint16_t* dh, int64_t m, int64_t k, int64_t f, sfr_act_t act,
+                                      const void* gu, const uint8_t* gu_scale, sfr_save_t gu_save, const void* x,
+                                      const uint8_t* x_scale, sfr_save_t x_save, const uint16_t* w, uint16_t* dx,
+                                      uint16_t* dw, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of gated_linear_bf16_backward; 0 for sizes it rejects. */
+int64_t sfr_gated_backward_workspace_bytes(int64_t m, int64_t k, int64_t f, sfr_save_t x_save);
+
+/*
+ * mxfp4_linear -- the linear layer for a 4-bit weight with one scale per 32
+ * values, as quantize_mx(SFR_MX_E2M1) writes it:
+ *     out[m, n] = sum_k x[m, k] wq[n, k] (+ bias[n])
+ * The weight's values are exact in bf16; sums are binary32, rounded once to
+ * bf16 or returned in binary32.
+ * mxfp4_gated_linear -- the gated block for such a weight [2 f, k]; h bf16.
+ *
+ *   x   [m, k] bf16 bits.
+ *   wq  [n, k / 2] (gated [2 f, k / 2]) bytes, ws [n, k / 32] bytes.
+ *   bias [n] bf16 bits or NULL;  out [m, n] bf16 bits or binary32;  h [m, f].
+ *   workspace  device scratch of at least sfr_mxfp4_workspace_bytes(m, n, k)
+ *              bytes (n = 2 f for the gated block; 0 for few rows, then it may be
+ *              NULL), overwritten; calls that may run at the same time need
+ *              distinct workspaces.
+ * m == 0 or n == 0 is a no-op; a small workspace is SFR_ERR_SHAPE.
+ */
+sfr_status mxfp4_linear(const uint16_t* x, int64_t m, int64_t k, const uint8_t* wq, const uint8_t* ws, int64_t n,
+                        const uint16_t* bias, void* out, sfr_out_t out_dt, void* workspace, int64_t workspace_bytes,
+                        void* stream);
+sfr_status mxfp4_gated_linear(const uint16_t* x, int64_t m, int64_t k, const uint8_t* wq, const uint8_t* ws, int64_t f,
+                              sfr_act_t act, uint16_t* h, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of mxfp4_linear and mxfp4_gated_linear; 0 for sizes they reject. */
+int64_t sfr_mxfp4_workspace_bytes(int64_t m, int64_t n, int64_t k);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* sfr_status_string(sfr_status s);
 

@@ -40,7 +40,9 @@ EXPORTED = ("quantize_rowwise_fp8", "quantize_tensorwise_fp8", "sfr_quantize_ten
             "sparse_fp8_rowwise_linear_dynamic", "sparse_fp8_rowwise_linear_dynamic_algo",
             "sparse_fp8_scaled_linear_algo", "sfr_linear_algo_count", "sfr_linear_algo_valid",
             "sfr_linear_algo_name", "sfr_linear_algo_supported", "sfr_linear_default_algo",
-            "bsr_count_bf16", "bsr_fill_bf16", "bsr_linear_bf16", "sfr_status_string", "sfr_format_version")
+            "bsr_count_bf16", "bsr_fill_bf16", "bsr_linear_bf16", "sfr_status_string", "sfr_format_version",
+            "quantize_mx", "dequantize_mx", "gated_linear_bf16", "gated_linear_bf16_backward",
+            "sfr_gated_backward_workspace_bytes", "mxfp4_linear", "mxfp4_gated_linear", "sfr_mxfp4_workspace_bytes")
 
 _FP8 = {torch.float8_e4m3fn: SFR_E4M3, torch.float8_e5m2: SFR_E5M2}
 _lib = None
@@ -86,6 +88,19 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.bsr_count_bf16.argtypes = [P, I64, I64, P, P]
     lib.bsr_fill_bf16.argtypes = [P, I64, I64, P, P, P, P]
     lib.bsr_linear_bf16.argtypes = [P, I64, I64, P, P, P, I64, P, P, I, P]
+    lib.quantize_mx.argtypes = [P, I64, I64, I, P, P, P]
+    lib.dequantize_mx.argtypes = [P, P, I64, I64, I, P, P]
+    lib.gated_linear_bf16.argtypes = [P, I64, I64, P, I64, I, P, I, P, P, P]
+    lib.gated_linear_bf16_backward.argtypes = [P, I64, I64, I64, I, P, P, I, P, P, I, P, P, P, P, I64, P]
+    lib.mxfp4_linear.argtypes = [P, I64, I64, P, P, I64, P, P, I, P, I64, P]
+    lib.mxfp4_gated_linear.argtypes = [P, I64, I64, P, P, I64, I, P, P, I64, P]
+    lib.sfr_gated_backward_workspace_bytes.argtypes = [I64, I64, I64, I]
+    lib.sfr_gated_backward_workspace_bytes.restype = I64
+    lib.sfr_mxfp4_workspace_bytes.argtypes = [I64, I64, I64]
+    lib.sfr_mxfp4_workspace_bytes.restype = I64
+    for fn in (lib.quantize_mx, lib.dequantize_mx, lib.gated_linear_bf16, lib.gated_linear_bf16_backward,
+               lib.mxfp4_linear, lib.mxfp4_gated_linear):
+        fn.restype = I
     for fn in (lib.quantize_rowwise_fp8, lib.compress_2to4_fp8, lib.prune_2to4_bf16, lib.sparse_fp8_rowwise_linear,
                lib.quantize_tensorwise_fp8, lib.sparse_fp8_scaled_linear, lib.sparse_fp8_rowwise_linear_dynamic,
                lib.sparse_fp8_rowwise_linear_dynamic_algo,
@@ -453,4 +468,269 @@ def bsr_linear(x: torch.Tensor, w: BsrWeight, bias: Optional[torch.Tensor] = Non
                                   w.values.data_ptr() if w.nnz else None, w.n,
                                   None if bias is None else bias.data_ptr(), out.data_ptr(), od, _stream(stream)),
            "bsr_linear_bf16")
+    return out
+
+
+# --------------------------------------------------------------------------
+# Gated feed-forward block, MX block formats, 4-bit weights
+# --------------------------------------------------------------------------
+MX_BLOCK = 32
+SFR_ACT = {"silu": 0, "gelu_tanh": 1, "relu": 2}
+_MX = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1, torch.float4_e2m1fn_x2: 2}
+_SAVE = {None: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 2, torch.float8_e5m2: 3}
+
+
+@dataclass
+class MxTensor:
+    """Rows of MX blocks: 32 values along a row share one power-of-two scale.
+
+    codes: float8_e4m3fn or float8_e5m2 [rows, cols], or float4_e2m1fn_x2
+    [rows, cols / 2] (two values a byte, the even column in the low half);
+    scale: float8_e8m0fnu [rows, cols / 32]."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+
+    @property
+    def shape(self):
+        r, c = self.codes.shape
+        return (r, 2 * c if self.codes.dtype == torch.float4_e2m1fn_x2 else c)
+
+
+@dataclass
+class GatedCheckpoint:
+    """What gated_linear_checkpointed keeps for gated_linear_backward: the
+    input x [m, k] and the projections gu = [g | u] [m, 2 f], each a bf16 tensor
+    or an 8-bit MxTensor, and the activation's name."""
+    x: object
+    gu: object
+    activation: str
+
+
+class _On:
+    """The device and stream of a call: its tensors' device current, and (with
+    an explicit stream) what the call allocates belonging to that stream."""
+
+    def __init__(self, t: torch.Tensor, stream):
+        self._device, self._stream = torch.cuda.device(t.device), stream
+        self._inner = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self._device.__enter__()
+        if self._inner is not None:
+            self._inner.__enter__()
+        return _stream(self._stream)
+
+    def __exit__(self, *exc):
+        if self._inner is not None:
+            self._inner.__exit__(*exc)
+        self._device.__exit__(*exc)
+
+
+def _together(first: torch.Tensor, *named):
+    """Every tensor contiguous and on the first one's GPU."""
+    for t, name in named:
+        _dev(t, name)
+        if t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, another device than {first.device}")
+
+
+def _bf16_2d(t: torch.Tensor, name: str):
+    _dev(t, name)
+    if t.dtype != torch.bfloat16 or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D bfloat16 tensor")
+
+
+def _mx_parts(t, name: str, kinds=None):
+    """(codes, scale, dtype) of an MxTensor, checked."""
+    if not isinstance(t, MxTensor):
+        raise ValueError(f"{name} must be an MxTensor")
+    if t.codes.dtype not in _MX or (kinds is not None and t.codes.dtype not in kinds):
+        raise ValueError(f"{name}: unsupported element type {t.codes.dtype}")
+    if t.codes.dim() != 2 or t.scale.dtype != torch.float8_e8m0fnu:
+        raise ValueError(f"{name}: codes must be 2-D and scale float8_e8m0fnu")
+    rows, cols = t.shape
+    if cols % MX_BLOCK != 0 or t.scale.shape != (rows, cols // MX_BLOCK):
+        raise ValueError(f"{name}: scale must have one entry per {MX_BLOCK} columns")
+    _together(t.codes, (t.codes, f"{name}.codes"), (t.scale, f"{name}.scale"))
+    return t.codes, t.scale, t.codes.dtype
+
+
+def _act_enum(name: str) -> int:
+    if name not in SFR_ACT:
+        raise ValueError(f"activation must be one of {sorted(SFR_ACT)}")
+    return SFR_ACT[name]
+
+
+def _out_like(out, shape, dtype, device, name="out"):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or not out.is_contiguous() or out.device != device:
+        raise ValueError(f"{name} has the wrong shape, dtype or device")
+    return out
+
+
+def quantize_mx(x: torch.Tensor, dtype=torch.float8_e4m3fn, stream=None) -> MxTensor:
+    """bf16 [rows, cols] -> MxTensor of float8_e4m3fn, float8_e5m2 or
+    float4_e2m1fn_x2 elements (cols a multiple of 32)."""
+    _bf16_2d(x, "x")
+    if dtype not in _MX:
+        raise ValueError(f"unsupported element type {dtype}")
+    rows, cols = x.shape
+    if cols == 0 or cols % MX_BLOCK != 0:
+        raise SfrError(2, "quantize_mx")
+    with _On(x, stream) as h:
+        codes = torch.empty((rows, cols // 2 if dtype == torch.float4_e2m1fn_x2 else cols), dtype=dtype,
+                            device=x.device)
+        scale = torch.empty((rows, cols // MX_BLOCK), dtype=torch.float8_e8m0fnu, device=x.device)
+        _check(load().quantize_mx(x.data_ptr(), rows, cols, _MX[dtype], codes.data_ptr(), scale.data_ptr(), h),
+               "quantize_mx")
+    return MxTensor(codes, scale)
+
+
+def dequantize_mx(t: MxTensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """MxTensor -> the bf16 values it stands for (exact)."""
+    codes, scale, dtype = _mx_parts(t, "t")
+    rows, cols = t.shape
+    with _On(codes, stream) as h:
+        out = _out_like(out, (rows, cols), torch.bfloat16, codes.device)
+        _check(load().dequantize_mx(codes.data_ptr(), scale.data_ptr(), rows, cols, _MX[dtype], out.data_ptr(), h),
+               "dequantize_mx")
+    return out
+
+
+def _gated_shapes(x: torch.Tensor, w: torch.Tensor):
+    _bf16_2d(x, "x")
+    _bf16_2d(w, "w")
+    _together(x, (w, "w"))
+    if w.shape[1] != x.shape[1] or w.shape[0] % 2 != 0:
+        raise ValueError("w must be [2 f, k] for x [m, k]")
+    return x.shape[0], x.shape[1], w.shape[0] // 2
+
+
+def gated_linear(x: torch.Tensor, w: torch.Tensor, activation: str = "silu", out: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """h [m, f] = act(x @ w[:f].T) * (x @ w[f:].T) for bf16 x [m, k], w [2 f, k]."""
+    m, k, f = _gated_shapes(x, w)
+    act = _act_enum(activation)
+    with _On(x, stream) as hs:
+        out = _out_like(out, (m, f), torch.bfloat16, x.device)
+        _check(load().gated_linear_bf16(x.data_ptr(), m, k, w.data_ptr(), f, act, out.data_ptr(), 0, None, None, hs),
+               "gated_linear")
+    return out
+
+
+def gated_linear_checkpointed(x: torch.Tensor, w: torch.Tensor, activation: str = "silu",
+                              checkpoint=torch.float8_e4m3fn, stream=None):
+    """(h, GatedCheckpoint): gated_linear, keeping for the backward pass x and
+    the projections in 8 bits (checkpoint float8_e4m3fn or float8_e5m2: MX
+    blocks), or x itself and the projections in bf16 (torch.bfloat16)."""
+    m, k, f = _gated_shapes(x, w)
+    act = _act_enum(activation)
+    if checkpoint is None or checkpoint not in _SAVE:
+        raise ValueError(f"unsupported checkpoint type {checkpoint}")
+    mx = checkpoint != torch.bfloat16
+    with _On(x, stream) as hs:
+        h = torch.empty((m, f), dtype=torch.bfloat16, device=x.device)
+        gu = torch.empty((m, 2 * f), dtype=checkpoint, device=x.device)
+        scale = torch.empty((m, 2 * f // MX_BLOCK), dtype=torch.float8_e8m0fnu, device=x.device) if mx else None
+        _check(load().gated_linear_bf16(x.data_ptr(), m, k, w.data_ptr(), f, act, h.data_ptr(), _SAVE[checkpoint],
+                                        gu.data_ptr(), scale.data_ptr() if mx else None, hs),
+               "gated_linear_checkpointed")
+    saved = GatedCheckpoint(quantize_mx(x, checkpoint, stream) if mx else x, MxTensor(gu, scale) if mx else gu,
+                            activation)
+    return h, saved
+
+
+def _saved_parts(t, name: str):
+    """(values or codes, scale or None, save enum, shape) of one saved activation."""
+    if isinstance(t, MxTensor):
+        codes, scale, dtype = _mx_parts(t, name, (torch.float8_e4m3fn, torch.float8_e5m2))
+        return codes, scale, _SAVE[dtype], t.shape
+    _bf16_2d(t, name)
+    return t, None, _SAVE[torch.bfloat16], tuple(t.shape)
+
+
+def gated_linear_backward(dh: torch.Tensor, w: torch.Tensor, saved: GatedCheckpoint, need_dx: bool = True,
+                          need_dw: bool = True, stream=None):
+    """(dx [m, k], dw [2 f, k]) in bf16 from dh [m, f], w and what
+    gated_linear_checkpointed kept; None in place of one that is not needed."""
+    _bf16_2d(dh, "dh")
+    _bf16_2d(w, "w")
+    x, xs, x_save, x_shape = _saved_parts(saved.x, "saved.x")
+    gu, gs, gu_save, gu_shape = _saved_parts(saved.gu, "saved.gu")
+    act = _act_enum(saved.activation)
+    _together(dh, (w, "w"), (x, "saved.x"), (gu, "saved.gu"))
+    m, f = dh.shape
+    k = w.shape[1]
+    if tuple(w.shape) != (2 * f, k) or tuple(x_shape) != (m, k) or tuple(gu_shape) != (m, 2 * f):
+        raise ValueError("operand shapes do not match")
+    lib = load()
+    with _On(dh, stream) as hs:
+        dx = torch.empty((m, k), dtype=torch.bfloat16, device=dh.device) if need_dx else None
+        dw = torch.empty((2 * f, k), dtype=torch.bfloat16, device=dh.device) if need_dw else None
+        nbytes = int(lib.sfr_gated_backward_workspace_bytes(m, k, f, x_save))
+        work = torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=dh.device)
+
+        def ptr(t):
+            return None if t is None else t.data_ptr()
+        _check(lib.gated_linear_bf16_backward(dh.data_ptr(), m, k, f, act, gu.data_ptr(), ptr(gs), gu_save,
+                                              x.data_ptr(), ptr(xs), x_save, w.data_ptr(), ptr(dx), ptr(dw),
+                                              work.data_ptr(), nbytes, hs), "gated_linear_backward")
+    return dx, dw
+
+
+def _mxfp4_weight(x: torch.Tensor, w: MxTensor):
+    _bf16_2d(x, "x")
+    codes, scale, _ = _mx_parts(w, "w", (torch.float4_e2m1fn_x2,))
+    _together(x, (codes, "w.codes"))
+    if w.shape[1] != x.shape[1]:
+        raise ValueError("operand shapes do not match")
+    return codes, scale
+
+
+def _mxfp4_workspace(lib, m: int, n: int, k: int, device):
+    nbytes = int(lib.sfr_mxfp4_workspace_bytes(m, n, k))
+    work = torch.empty((nbytes,), dtype=torch.uint8, device=device) if nbytes else None
+    return (work.data_ptr() if nbytes else None), nbytes, work
+
+
+def mxfp4_linear(x: torch.Tensor, w: MxTensor, bias: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
+                 out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """bf16 x [m, k] -> out [m, n] = x @ W.T (+ bias) for a 4-bit weight W [n, k]
+    with one scale per 32 values, from quantize_mx(w, torch.float4_e2m1fn_x2)."""
+    codes, scale = _mxfp4_weight(x, w)
+    m, k = x.shape
+    n = w.shape[0]
+    if bias is not None:
+        _together(x, (bias, "bias"))
+        if bias.dtype != torch.bfloat16 or bias.shape != (n,):
+            raise ValueError("bias must be bfloat16 [n]")
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out_dtype must be bfloat16 or float32")
+    od = {torch.bfloat16: SFR_OUT_BF16, torch.float32: SFR_OUT_F32}[out_dtype]
+    lib = load()
+    with _On(x, stream) as hs:
+        out = _out_like(out, (m, n), out_dtype, x.device)
+        ptr, nbytes, work = _mxfp4_workspace(lib, m, n, k, x.device)
+        _check(lib.mxfp4_linear(x.data_ptr(), m, k, codes.data_ptr(), scale.data_ptr(), n,
+                                None if bias is None else bias.data_ptr(), out.data_ptr(), od, ptr, nbytes, hs),
+               "mxfp4_linear")
+    return out
+
+
+def mxfp4_gated_linear(x: torch.Tensor, w: MxTensor, activation: str = "silu", out: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+    """gated_linear for a 4-bit weight [2 f, k] from quantize_mx(w, torch.float4_e2m1fn_x2)."""
+    codes, scale = _mxfp4_weight(x, w)
+    act = _act_enum(activation)
+    m, k = x.shape
+    if w.shape[0] % 2 != 0:
+        raise ValueError("w must be [2 f, k]")
+    f = w.shape[0] // 2
+    lib = load()
+    with _On(x, stream) as hs:
+        out = _out_like(out, (m, f), torch.bfloat16, x.device)
+        ptr, nbytes, work = _mxfp4_workspace(lib, m, 2 * f, k, x.device)
+        _check(lib.mxfp4_gated_linear(x.data_ptr(), m, k, codes.data_ptr(), scale.data_ptr(), f, act, out.data_ptr(),
+                                      ptr, nbytes, hs), "mxfp4_gated_linear")
     return out

@@ -13,6 +13,21 @@ bool scale_ok(int kind) { return kind == SFR_SCALE_ROW || kind == SFR_SCALE_TENS
 // Bound on rows * cols of any one tensor, keeping every grid within HIP's limits.
 constexpr int64_t kMaxElems = (int64_t)1 << 40;
 
+bool act_ok(int act) { return act == SFR_ACT_SILU || act == SFR_ACT_GELU_TANH || act == SFR_ACT_RELU; }
+bool out_ok(int dt) { return dt == SFR_OUT_BF16 || dt == SFR_OUT_F32; }
+bool save_ok(int s) { return s >= SFR_SAVE_NONE && s <= SFR_SAVE_E5M2; }
+bool save8(int s) { return s == SFR_SAVE_E4M3 || s == SFR_SAVE_E5M2; }
+bool block_dim(int64_t d, int64_t multiple) { return d > 0 && d <= SFR_MAX_BLOCK_DIM && d % multiple == 0; }
+// An output of the dense products: its tiles make one grid.
+bool dense_ok(int64_t rows, int64_t cols) {
+  const int64_t t = rows > 64 ? 128 : 64;
+  return ((rows + t - 1) / t) * ((cols + t - 1) / t) <= ((int64_t)1 << 24);
+}
+bool gated_shape(int64_t m, int64_t k, int64_t f) {
+  return m >= 0 && m <= SFR_MAX_DIM && block_dim(k, 32) && block_dim(2 * f, 64) && dense_ok(m, 2 * f) &&
+         dense_ok(m, k) && dense_ok(2 * f, k);
+}
+
 sfr_status launch_status(hipError_t e) { return e == hipSuccess ? SFR_OK : SFR_ERR_LAUNCH; }
 
 }  // namespace
@@ -202,6 +217,106 @@ sfr_status bsr_linear_bf16(const uint16_t* x, int64_t m, int64_t k, const int32_
     return SFR_ERR_ALIGN;
   return launch_status(sfr::launch_bsr_linear(x, m, k, crow, col, values, n, bias, out, (int)out_dt,
                                               static_cast<hipStream_t>(stream)));
+}
+
+sfr_status quantize_mx(const uint16_t* x, int64_t rows, int64_t cols, sfr_mx_t dt, uint8_t* q, uint8_t* scale,
+                       void* stream) {
+  if (dt < SFR_MX_E4M3 || dt > SFR_MX_E2M1) return SFR_ERR_DTYPE;
+  if (rows < 0 || rows > SFR_MAX_DIM || cols <= 0 || cols > SFR_MAX_DIM || cols % SFR_MX_BLOCK != 0 ||
+      rows * cols > kMaxElems)
+    return SFR_ERR_SHAPE;
+  if (rows == 0) return SFR_OK;
+  if (!x || !q || !scale) return SFR_ERR_NULL;
+  if (!aligned16(x) || !aligned16(q) || !aligned16(scale)) return SFR_ERR_ALIGN;
+  return launch_status(sfr::launch_quantize_mx(x, rows, cols, dt, q, scale, static_cast<hipStream_t>(stream)));
+}
+
+sfr_status dequantize_mx(const uint8_t* q, const uint8_t* scale, int64_t rows, int64_t cols, sfr_mx_t dt,
+                         uint16_t* out, void* stream) {
+  if (dt < SFR_MX_E4M3 || dt > SFR_MX_E2M1) return SFR_ERR_DTYPE;
+  if (rows < 0 || rows > SFR_MAX_DIM || cols <= 0 || cols > SFR_MAX_DIM || cols % SFR_MX_BLOCK != 0 ||
+      rows * cols > kMaxElems)
+    return SFR_ERR_SHAPE;
+  if (rows == 0) return SFR_OK;
+  if (!q || !scale || !out) return SFR_ERR_NULL;
+  if (!aligned16(q) || !aligned16(scale) || !aligned16(out)) return SFR_ERR_ALIGN;
+  return launch_status(sfr::launch_dequantize_mx(q, scale, rows, cols, dt, out, static_cast<hipStream_t>(stream)));
+}
+
+sfr_status gated_linear_bf16(const uint16_t* x, int64_t m, int64_t k, const uint16_t* w, int64_t f, sfr_act_t act,
+                             uint16_t* h, sfr_save_t save, void* gu, uint8_t* gu_scale, void* stream) {
+  if (!act_ok(act) || !save_ok(save)) return SFR_ERR_DTYPE;
+  if (!gated_shape(m, k, f)) return SFR_ERR_SHAPE;
+  if (m == 0) return SFR_OK;
+  if (!x || !w || !h || (save != SFR_SAVE_NONE && !gu) || (save8(save) && !gu_scale)) return SFR_ERR_NULL;
+  if (!aligned16(x) || !aligned16(w) || !aligned16(h) || (save != SFR_SAVE_NONE && !aligned16(gu)) ||
+      (save8(save) && !aligned16(gu_scale)))
+    return SFR_ERR_ALIGN;
+  const sfr::GatedArgs a{x, w, m, k, f, (int)act, h, (int)save, gu, gu_scale};
+  return launch_status(sfr::launch_gated(a, static_cast<hipStream_t>(stream)));
+}
+
+int64_t sfr_gated_backward_workspace_bytes(int64_t m, int64_t k, int64_t f, sfr_save_t x_save) {
+  if (!save_ok(x_save) || x_save == SFR_SAVE_NONE || !gated_shape(m, k, f)) return 0;
+  return sfr::gated_backward_workspace_bytes(m, k, f, save8(x_save));
+}
+
+sfr_status gated_linear_bf16_backward(const uint16_t* dh, int64_t m, int64_t k, int64_t f, sfr_act_t act,
+                                      const void* gu, const uint8_t* gu_scale, sfr_save_t gu_save, const void* x,
+                                      const uint8_t* x_scale, sfr_save_t x_save, const uint16_t* w, uint16_t* dx,
+                                      uint16_t* dw, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!act_ok(act) || !save_ok(gu_save) || gu_save == SFR_SAVE_NONE || !save_ok(x_save) || x_save == SFR_SAVE_NONE)
+    return SFR_ERR_DTYPE;
+  if (!gated_shape(m, k, f)) return SFR_ERR_SHAPE;
+  if (workspace_bytes < sfr::gated_backward_workspace_bytes(m, k, f, save8(x_save))) return SFR_ERR_SHAPE;
+  if (!dx && !dw) return SFR_OK;
+  if (m > 0 && (!dh || !gu || !workspace || (save8(gu_save) && !gu_scale) || (dx && !w) ||
+                (dw && (!x || (save8(x_save) && !x_scale)))))
+    return SFR_ERR_NULL;
+  if (!aligned16(dh) || !aligned16(gu) || !aligned16(workspace) || !aligned16(dx) || !aligned16(dw) ||
+      (save8(gu_save) && !aligned16(gu_scale)) || (dx && !aligned16(w)) ||
+      (dw && (!aligned16(x) || (save8(x_save) && !aligned16(x_scale)))))
+    return SFR_ERR_ALIGN;
+  const sfr::GatedBackwardArgs a{dh,          w,  m,       k,           f, (int)act, (int)gu_save, gu, gu_scale,
+                                 (int)x_save, x,  x_scale, dx,          dw};
+  return launch_status(sfr::launch_gated_backward(a, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int64_t sfr_mxfp4_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  if (m <= 0 || m > SFR_MAX_DIM || !block_dim(n, 16) || !block_dim(k, 32) || !dense_ok(m, n)) return 0;
+  return sfr::mxfp4_workspace_bytes(m, n, k);
+}
+
+sfr_status mxfp4_linear(const uint16_t* x, int64_t m, int64_t k, const uint8_t* wq, const uint8_t* ws, int64_t n,
+                        const uint16_t* bias, void* out, sfr_out_t out_dt, void* workspace, int64_t workspace_bytes,
+                        void* stream) {
+  if (!out_ok(out_dt)) return SFR_ERR_DTYPE;
+  if (m < 0 || m > SFR_MAX_DIM || (n != 0 && !block_dim(n, 16)) || !block_dim(k, 32) || !dense_ok(m, n))
+    return SFR_ERR_SHAPE;
+  if (m == 0 || n == 0) return SFR_OK;
+  const int64_t need = sfr::mxfp4_workspace_bytes(m, n, k);
+  if (workspace_bytes < need) return SFR_ERR_SHAPE;
+  if (!x || !wq || !ws || !out || (need > 0 && !workspace)) return SFR_ERR_NULL;
+  if (!aligned16(x) || !aligned16(wq) || !aligned16(ws) || !aligned16(out) || (bias && !aligned16(bias)) ||
+      (need > 0 && !aligned16(workspace)))
+    return SFR_ERR_ALIGN;
+  const sfr::StreamArgs a{x, wq, ws, m, k, n, false, 0, bias, out, (int)out_dt};
+  return launch_status(sfr::launch_mxfp4(a, workspace, static_cast<hipStream_t>(stream)));
+}
+
+sfr_status mxfp4_gated_linear(const uint16_t* x, int64_t m, int64_t k, const uint8_t* wq, const uint8_t* ws, int64_t f,
+                              sfr_act_t act, uint16_t* h, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!act_ok(act)) return SFR_ERR_DTYPE;
+  if (m < 0 || m > SFR_MAX_DIM || !block_dim(2 * f, 64) || !block_dim(k, 32) || !dense_ok(m, 2 * f))
+    return SFR_ERR_SHAPE;
+  if (m == 0) return SFR_OK;
+  const int64_t need = sfr::mxfp4_workspace_bytes(m, 2 * f, k);
+  if (workspace_bytes < need) return SFR_ERR_SHAPE;
+  if (!x || !wq || !ws || !h || (need > 0 && !workspace)) return SFR_ERR_NULL;
+  if (!aligned16(x) || !aligned16(wq) || !aligned16(ws) || !aligned16(h) || (need > 0 && !aligned16(workspace)))
+    return SFR_ERR_ALIGN;
+  const sfr::StreamArgs a{x, wq, ws, m, k, f, true, (int)act, nullptr, h, (int)SFR_OUT_BF16};
+  return launch_status(sfr::launch_mxfp4(a, workspace, static_cast<hipStream_t>(stream)));
 }
 
 const char* sfr_status_string(sfr_status s) {

@@ -76,4 +76,66 @@ hipError_t launch_bsr_linear(const uint16_t* x, int64_t m, int64_t k, const int3
                              const uint16_t* values, int64_t n, const uint16_t* bias, void* out, int out_fmt,
                              hipStream_t stream);
 
+// MX block formats (fmt: MX_E4M3, MX_E5M2, MX_E2M1); cols % 32 == 0.
+hipError_t launch_quantize_mx(const uint16_t* x, int64_t rows, int64_t cols, int fmt, uint8_t* q, uint8_t* scale,
+                              hipStream_t stream);
+hipError_t launch_dequantize_mx(const uint8_t* q, const uint8_t* scale, int64_t rows, int64_t cols, int fmt,
+                                uint16_t* out, hipStream_t stream);
+
+// How activations are saved for the backward pass.
+enum { GU_NONE = 0, GU_BF16 = 1, GU_E4M3 = 2, GU_E5M2 = 3 };
+
+struct GatedArgs {
+  const uint16_t *x, *w;  // [m, k]; [2 f, k]
+  int64_t m, k, f;
+  int act;
+  uint16_t* h;  // [m, f]
+  int gu_fmt;
+  void* gu;           // [m, 2 f]
+  uint8_t* gu_scale;  // [m, 2 f / 32]
+};
+hipError_t launch_gated(const GatedArgs& a, hipStream_t stream);
+hipError_t launch_gated_dense(const GatedArgs& a, hipStream_t stream);  // the matrix-core form, any m
+
+struct GatedBackwardArgs {
+  const uint16_t *dh, *w;
+  int64_t m, k, f;
+  int act;
+  int gu_fmt;
+  const void* gu;
+  const uint8_t* gu_scale;
+  int x_fmt;
+  const void* x;
+  const uint8_t* x_scale;
+  uint16_t *dx, *dw;  // either may be null
+};
+int64_t gated_backward_workspace_bytes(int64_t m, int64_t k, int64_t f, bool x_mx);
+hipError_t launch_gated_backward(const GatedBackwardArgs& a, void* workspace, hipStream_t stream);
+
+// Dense bf16 products: out[m, n] = x w^T (+ bias); dx = dgu w; dw = dgu^T x.
+hipError_t launch_dense_nt(const uint16_t* x, const uint16_t* w, int64_t m, int64_t n, int64_t k, const uint16_t* bias,
+                           void* out, int out_fmt, hipStream_t stream);
+hipError_t launch_dense_dx(const uint16_t* dgu, const uint16_t* w, int64_t m, int64_t k, int64_t f2, uint16_t* dx,
+                           hipStream_t stream);
+hipError_t launch_dense_dw(const uint16_t* dgu, const uint16_t* x, int64_t m, int64_t k, int64_t f2, uint16_t* dw,
+                           hipStream_t stream);
+
+// Products of few activation rows: a bf16 weight (w_scale null, gated only)
+// or a 4-bit one.  rows: n, or f when gated.
+struct StreamArgs {
+  const uint16_t* x;
+  const void* w;
+  const uint8_t* w_scale;
+  int64_t m, k, rows;
+  bool gated;
+  int act;
+  const uint16_t* bias;
+  void* out;
+  int out_fmt;
+};
+bool stream_rows(int64_t m);
+hipError_t launch_stream(const StreamArgs& a, hipStream_t stream);
+int64_t mxfp4_workspace_bytes(int64_t m, int64_t n, int64_t k);
+hipError_t launch_mxfp4(const StreamArgs& a, void* workspace, hipStream_t stream);
+
 }  // namespace sfr
