@@ -513,18 +513,17 @@ int64_t sfr_gated_backward_workspace_bytes(int64_t m, int64_t k, int64_t f, sfr_
  *   wq  [n, k / 2] (gated [2 f, k / 2]) bytes, ws [n, k / 32] bytes.
  *   bias [n] bf16 bits or NULL;  out [m, n] bf16 bits or binary32;  h [m, f].
  *   workspace  device scratch of at least sfr_mxfp4_workspace_bytes(m, n, k)
- *              bytes (n = 2 f for the gated block; 0 for few rows, then it may be
- *              NULL), overwritten; calls that may run at the same time need
- *              distinct workspaces.
+ *              bytes (0 for many sizes; then it may be NULL), overwritten; calls
+ *              that may run at the same time need distinct workspaces.
  * m == 0 or n == 0 is a no-op; a small workspace is SFR_ERR_SHAPE.
  */
 sfr_status mxfp4_linear(const uint16_t* x, int64_t m, int64_t k, const uint8_t* wq, const uint8_t* ws, int64_t n,
                         const uint16_t* bias, void* out, sfr_out_t out_dt, void* workspace, int64_t workspace_bytes,
                         void* stream);
 sfr_status mxfp4_gated_linear(const uint16_t* x, int64_t m, int64_t k, const uint8_t* wq, const uint8_t* ws, int64_t f,
-                              sfr_act_t act, uint16_t* h, void* workspace, int64_t workspace_bytes, void* stream);
+                              sfr_act_t act, uint16_t* h, void* stream);
 
-/* Workspace bytes of mxfp4_linear and mxfp4_gated_linear; 0 for sizes they reject. */
+/* Workspace bytes of mxfp4_linear; 0 for sizes it rejects. */
 int64_t sfr_mxfp4_workspace_bytes(int64_t m, int64_t n, int64_t k);
 
 /* Human-readable name of a status code (static string, never NULL). */

@@ -20,6 +20,7 @@ calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import Optional
@@ -93,7 +94,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.gated_linear_bf16.argtypes = [P, I64, I64, P, I64, I, P, I, P, P, P]
     lib.gated_linear_bf16_backward.argtypes = [P, I64, I64, I64, I, P, P, I, P, P, I, P, P, P, P, I64, P]
     lib.mxfp4_linear.argtypes = [P, I64, I64, P, P, I64, P, P, I, P, I64, P]
-    lib.mxfp4_gated_linear.argtypes = [P, I64, I64, P, P, I64, I, P, P, I64, P]
+    lib.mxfp4_gated_linear.argtypes = [P, I64, I64, P, P, I64, I, P, P]
     lib.sfr_gated_backward_workspace_bytes.argtypes = [I64, I64, I64, I]
     lib.sfr_gated_backward_workspace_bytes.restype = I64
     lib.sfr_mxfp4_workspace_bytes.argtypes = [I64, I64, I64]
@@ -477,7 +478,7 @@ def bsr_linear(x: torch.Tensor, w: BsrWeight, bias: Optional[torch.Tensor] = Non
 MX_BLOCK = 32
 SFR_ACT = {"silu": 0, "gelu_tanh": 1, "relu": 2}
 _MX = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1, torch.float4_e2m1fn_x2: 2}
-_SAVE = {None: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 2, torch.float8_e5m2: 3}
+_SAVE = {torch.bfloat16: 1, torch.float8_e4m3fn: 2, torch.float8_e5m2: 3}
 
 
 @dataclass
@@ -506,53 +507,60 @@ class GatedCheckpoint:
     activation: str
 
 
-class _On:
-    """The device and stream of a call: its tensors' device current, and (with
-    an explicit stream) what the call allocates belonging to that stream."""
-
-    def __init__(self, t: torch.Tensor, stream):
-        self._device, self._stream = torch.cuda.device(t.device), stream
-        self._inner = None if stream is None else torch.cuda.stream(stream)
-
-    def __enter__(self):
-        self._device.__enter__()
-        if self._inner is not None:
-            self._inner.__enter__()
-        return _stream(self._stream)
-
-    def __exit__(self, *exc):
-        if self._inner is not None:
-            self._inner.__exit__(*exc)
-        self._device.__exit__(*exc)
+def _current_raw_stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
 
 
-def _together(first: torch.Tensor, *named):
-    """Every tensor contiguous and on the first one's GPU."""
-    for t, name in named:
-        _dev(t, name)
-        if t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, another device than {first.device}")
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_raw_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _bf16_2d(t: torch.Tensor, name: str):
-    _dev(t, name)
-    if t.dtype != torch.bfloat16 or t.dim() != 2:
+def _placed(fn):
+    """Runs fn with its first argument's device current and, with an explicit
+    `stream`, with that stream current, so that what the call allocates belongs
+    to the stream its kernels run on.  Nothing is switched when both are so
+    already."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        t = first.codes if isinstance(first, MxTensor) else first
+        device = t.get_device()
+        if device < 0 or (stream is None and device == _current_device()):
+            return fn(first, *args, **kw)
+        with torch.cuda.device(device), torch.cuda.stream(stream):
+            return fn(first, *args, **kw)
+    return call
+
+
+def _gpu(t: torch.Tensor, name: str, device: int) -> int:
+    """t's address; t must be contiguous and on GPU `device`."""
+    d = t.get_device()
+    if d < 0:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if d != device:
+        raise ValueError(f"{name} is on GPU {d}, another device than GPU {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _bf16_2d(t: torch.Tensor, name: str, device: int) -> int:
+    if t.dtype is not torch.bfloat16 or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D bfloat16 tensor")
+    return _gpu(t, name, device)
 
 
-def _mx_parts(t, name: str, kinds=None):
-    """(codes, scale, dtype) of an MxTensor, checked."""
+def _mx_parts(t, name: str, device: int, kinds=_MX):
+    """(rows, cols, address of the codes, of the scales) of an MxTensor, checked."""
     if not isinstance(t, MxTensor):
         raise ValueError(f"{name} must be an MxTensor")
-    if t.codes.dtype not in _MX or (kinds is not None and t.codes.dtype not in kinds):
+    if t.codes.dtype not in kinds:
         raise ValueError(f"{name}: unsupported element type {t.codes.dtype}")
-    if t.codes.dim() != 2 or t.scale.dtype != torch.float8_e8m0fnu:
+    if t.codes.dim() != 2 or t.scale.dtype is not torch.float8_e8m0fnu:
         raise ValueError(f"{name}: codes must be 2-D and scale float8_e8m0fnu")
     rows, cols = t.shape
     if cols % MX_BLOCK != 0 or t.scale.shape != (rows, cols // MX_BLOCK):
         raise ValueError(f"{name}: scale must have one entry per {MX_BLOCK} columns")
-    _together(t.codes, (t.codes, f"{name}.codes"), (t.scale, f"{name}.scale"))
-    return t.codes, t.scale, t.codes.dtype
+    return rows, cols, _gpu(t.codes, f"{name}.codes", device), _gpu(t.scale, f"{name}.scale", device)
 
 
 def _act_enum(name: str) -> int:
@@ -561,176 +569,168 @@ def _act_enum(name: str) -> int:
     return SFR_ACT[name]
 
 
-def _out_like(out, shape, dtype, device, name="out"):
+def _output(out, rows: int, cols: int, dtype, like: torch.Tensor):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or not out.is_contiguous() or out.device != device:
-        raise ValueError(f"{name} has the wrong shape, dtype or device")
+        return like.new_empty((rows, cols), dtype=dtype)
+    if out.shape != (rows, cols) or out.dtype is not dtype or not out.is_contiguous() or out.device != like.device:
+        raise ValueError("out has the wrong shape, dtype or device")
     return out
 
 
-def quantize_mx(x: torch.Tensor, dtype=torch.float8_e4m3fn, stream=None) -> MxTensor:
+@_placed
+def quantize_mx(x: torch.Tensor, dtype=torch.float8_e4m3fn) -> MxTensor:
     """bf16 [rows, cols] -> MxTensor of float8_e4m3fn, float8_e5m2 or
     float4_e2m1fn_x2 elements (cols a multiple of 32)."""
-    _bf16_2d(x, "x")
     if dtype not in _MX:
         raise ValueError(f"unsupported element type {dtype}")
+    device = x.get_device()
+    px = _bf16_2d(x, "x", device)
     rows, cols = x.shape
     if cols == 0 or cols % MX_BLOCK != 0:
         raise SfrError(2, "quantize_mx")
-    with _On(x, stream) as h:
-        codes = torch.empty((rows, cols // 2 if dtype == torch.float4_e2m1fn_x2 else cols), dtype=dtype,
-                            device=x.device)
-        scale = torch.empty((rows, cols // MX_BLOCK), dtype=torch.float8_e8m0fnu, device=x.device)
-        _check(load().quantize_mx(x.data_ptr(), rows, cols, _MX[dtype], codes.data_ptr(), scale.data_ptr(), h),
-               "quantize_mx")
+    codes = x.new_empty((rows, cols // 2 if dtype is torch.float4_e2m1fn_x2 else cols), dtype=dtype)
+    scale = x.new_empty((rows, cols // MX_BLOCK), dtype=torch.float8_e8m0fnu)
+    _check(load().quantize_mx(px, rows, cols, _MX[dtype], codes.data_ptr(), scale.data_ptr(), _raw_stream(device)),
+           "quantize_mx")
     return MxTensor(codes, scale)
 
 
-def dequantize_mx(t: MxTensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+@_placed
+def dequantize_mx(t: MxTensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """MxTensor -> the bf16 values it stands for (exact)."""
-    codes, scale, dtype = _mx_parts(t, "t")
-    rows, cols = t.shape
-    with _On(codes, stream) as h:
-        out = _out_like(out, (rows, cols), torch.bfloat16, codes.device)
-        _check(load().dequantize_mx(codes.data_ptr(), scale.data_ptr(), rows, cols, _MX[dtype], out.data_ptr(), h),
-               "dequantize_mx")
+    device = t.codes.get_device()
+    rows, cols, pq, ps = _mx_parts(t, "t", device)
+    out = _output(out, rows, cols, torch.bfloat16, t.codes)
+    _check(load().dequantize_mx(pq, ps, rows, cols, _MX[t.codes.dtype], out.data_ptr(), _raw_stream(device)),
+           "dequantize_mx")
     return out
 
 
-def _gated_shapes(x: torch.Tensor, w: torch.Tensor):
-    _bf16_2d(x, "x")
-    _bf16_2d(w, "w")
-    _together(x, (w, "w"))
-    if w.shape[1] != x.shape[1] or w.shape[0] % 2 != 0:
+def _gated_operands(x: torch.Tensor, w: torch.Tensor):
+    device = x.get_device()
+    px, pw = _bf16_2d(x, "x", device), _bf16_2d(w, "w", device)
+    m, k = x.shape
+    f2, kw = w.shape
+    if kw != k or f2 % 2 != 0:
         raise ValueError("w must be [2 f, k] for x [m, k]")
-    return x.shape[0], x.shape[1], w.shape[0] // 2
+    return device, px, pw, m, k, f2 // 2
 
 
-def gated_linear(x: torch.Tensor, w: torch.Tensor, activation: str = "silu", out: Optional[torch.Tensor] = None,
-                 stream=None) -> torch.Tensor:
+@_placed
+def gated_linear(x: torch.Tensor, w: torch.Tensor, activation: str = "silu",
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """h [m, f] = act(x @ w[:f].T) * (x @ w[f:].T) for bf16 x [m, k], w [2 f, k]."""
-    m, k, f = _gated_shapes(x, w)
+    device, px, pw, m, k, f = _gated_operands(x, w)
     act = _act_enum(activation)
-    with _On(x, stream) as hs:
-        out = _out_like(out, (m, f), torch.bfloat16, x.device)
-        _check(load().gated_linear_bf16(x.data_ptr(), m, k, w.data_ptr(), f, act, out.data_ptr(), 0, None, None, hs),
-               "gated_linear")
+    out = _output(out, m, f, torch.bfloat16, x)
+    _check(load().gated_linear_bf16(px, m, k, pw, f, act, out.data_ptr(), 0, None, None, _raw_stream(device)),
+           "gated_linear")
     return out
 
 
+@_placed
 def gated_linear_checkpointed(x: torch.Tensor, w: torch.Tensor, activation: str = "silu",
-                              checkpoint=torch.float8_e4m3fn, stream=None):
+                              checkpoint=torch.float8_e4m3fn):
     """(h, GatedCheckpoint): gated_linear, keeping for the backward pass x and
     the projections in 8 bits (checkpoint float8_e4m3fn or float8_e5m2: MX
     blocks), or x itself and the projections in bf16 (torch.bfloat16)."""
-    m, k, f = _gated_shapes(x, w)
-    act = _act_enum(activation)
-    if checkpoint is None or checkpoint not in _SAVE:
+    if checkpoint not in _SAVE:
         raise ValueError(f"unsupported checkpoint type {checkpoint}")
-    mx = checkpoint != torch.bfloat16
-    with _On(x, stream) as hs:
-        h = torch.empty((m, f), dtype=torch.bfloat16, device=x.device)
-        gu = torch.empty((m, 2 * f), dtype=checkpoint, device=x.device)
-        scale = torch.empty((m, 2 * f // MX_BLOCK), dtype=torch.float8_e8m0fnu, device=x.device) if mx else None
-        _check(load().gated_linear_bf16(x.data_ptr(), m, k, w.data_ptr(), f, act, h.data_ptr(), _SAVE[checkpoint],
-                                        gu.data_ptr(), scale.data_ptr() if mx else None, hs),
-               "gated_linear_checkpointed")
-    saved = GatedCheckpoint(quantize_mx(x, checkpoint, stream) if mx else x, MxTensor(gu, scale) if mx else gu,
-                            activation)
-    return h, saved
+    device, px, pw, m, k, f = _gated_operands(x, w)
+    act = _act_enum(activation)
+    h = x.new_empty((m, f))
+    gu = x.new_empty((m, 2 * f), dtype=checkpoint)
+    scale = None if checkpoint is torch.bfloat16 else x.new_empty((m, 2 * f // MX_BLOCK), dtype=torch.float8_e8m0fnu)
+    _check(load().gated_linear_bf16(px, m, k, pw, f, act, h.data_ptr(), _SAVE[checkpoint], gu.data_ptr(),
+                                    None if scale is None else scale.data_ptr(), _raw_stream(device)),
+           "gated_linear_checkpointed")
+    if scale is None:
+        return h, GatedCheckpoint(x, gu, activation)
+    return h, GatedCheckpoint(quantize_mx(x, checkpoint), MxTensor(gu, scale), activation)
 
 
-def _saved_parts(t, name: str):
-    """(values or codes, scale or None, save enum, shape) of one saved activation."""
+def _saved_parts(t, name: str, device: int):
+    """(rows, cols, address, address of the scales or None, save enum) of one saved activation."""
     if isinstance(t, MxTensor):
-        codes, scale, dtype = _mx_parts(t, name, (torch.float8_e4m3fn, torch.float8_e5m2))
-        return codes, scale, _SAVE[dtype], t.shape
-    _bf16_2d(t, name)
-    return t, None, _SAVE[torch.bfloat16], tuple(t.shape)
+        return (*_mx_parts(t, name, device, _SAVE), _SAVE[t.codes.dtype])
+    p = _bf16_2d(t, name, device)
+    return (*t.shape, p, None, _SAVE[torch.bfloat16])
 
 
+@_placed
 def gated_linear_backward(dh: torch.Tensor, w: torch.Tensor, saved: GatedCheckpoint, need_dx: bool = True,
-                          need_dw: bool = True, stream=None):
+                          need_dw: bool = True):
     """(dx [m, k], dw [2 f, k]) in bf16 from dh [m, f], w and what
     gated_linear_checkpointed kept; None in place of one that is not needed."""
-    _bf16_2d(dh, "dh")
-    _bf16_2d(w, "w")
-    x, xs, x_save, x_shape = _saved_parts(saved.x, "saved.x")
-    gu, gs, gu_save, gu_shape = _saved_parts(saved.gu, "saved.gu")
+    device = dh.get_device()
+    pd, pw = _bf16_2d(dh, "dh", device), _bf16_2d(w, "w", device)
+    xm, xk, px, pxs, x_save = _saved_parts(saved.x, "saved.x", device)
+    gm, gf2, pg, pgs, g_save = _saved_parts(saved.gu, "saved.gu", device)
     act = _act_enum(saved.activation)
-    _together(dh, (w, "w"), (x, "saved.x"), (gu, "saved.gu"))
     m, f = dh.shape
     k = w.shape[1]
-    if tuple(w.shape) != (2 * f, k) or tuple(x_shape) != (m, k) or tuple(gu_shape) != (m, 2 * f):
+    if w.shape[0] != 2 * f or (xm, xk) != (m, k) or (gm, gf2) != (m, 2 * f):
         raise ValueError("operand shapes do not match")
     lib = load()
-    with _On(dh, stream) as hs:
-        dx = torch.empty((m, k), dtype=torch.bfloat16, device=dh.device) if need_dx else None
-        dw = torch.empty((2 * f, k), dtype=torch.bfloat16, device=dh.device) if need_dw else None
-        nbytes = int(lib.sfr_gated_backward_workspace_bytes(m, k, f, x_save))
-        work = torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=dh.device)
-
-        def ptr(t):
-            return None if t is None else t.data_ptr()
-        _check(lib.gated_linear_bf16_backward(dh.data_ptr(), m, k, f, act, gu.data_ptr(), ptr(gs), gu_save,
-                                              x.data_ptr(), ptr(xs), x_save, w.data_ptr(), ptr(dx), ptr(dw),
-                                              work.data_ptr(), nbytes, hs), "gated_linear_backward")
+    dx = dh.new_empty((m, k)) if need_dx else None
+    dw = dh.new_empty((2 * f, k)) if need_dw else None
+    nbytes = lib.sfr_gated_backward_workspace_bytes(m, k, f, x_save)
+    work = dh.new_empty((max(nbytes, 16),), dtype=torch.uint8)
+    _check(lib.gated_linear_bf16_backward(pd, m, k, f, act, pg, pgs, g_save, px, pxs, x_save, pw,
+                                          dx.data_ptr() if need_dx else None, dw.data_ptr() if need_dw else None,
+                                          work.data_ptr(), nbytes, _raw_stream(device)), "gated_linear_backward")
     return dx, dw
 
 
-def _mxfp4_weight(x: torch.Tensor, w: MxTensor):
-    _bf16_2d(x, "x")
-    codes, scale, _ = _mx_parts(w, "w", (torch.float4_e2m1fn_x2,))
-    _together(x, (codes, "w.codes"))
-    if w.shape[1] != x.shape[1]:
+_FP4 = (torch.float4_e2m1fn_x2,)
+
+
+@functools.lru_cache(maxsize=4096)
+def _mxfp4_workspace_bytes(m: int, n: int, k: int) -> int:
+    return load().sfr_mxfp4_workspace_bytes(m, n, k)
+
+
+def _mxfp4_operands(x: torch.Tensor, w: MxTensor):
+    device = x.get_device()
+    px = _bf16_2d(x, "x", device)
+    n, wk, pq, ps = _mx_parts(w, "w", device, _FP4)
+    m, k = x.shape
+    if wk != k:
         raise ValueError("operand shapes do not match")
-    return codes, scale
+    return device, px, pq, ps, m, n, k
 
 
-def _mxfp4_workspace(lib, m: int, n: int, k: int, device):
-    nbytes = int(lib.sfr_mxfp4_workspace_bytes(m, n, k))
-    work = torch.empty((nbytes,), dtype=torch.uint8, device=device) if nbytes else None
-    return (work.data_ptr() if nbytes else None), nbytes, work
-
-
+@_placed
 def mxfp4_linear(x: torch.Tensor, w: MxTensor, bias: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
-                 out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """bf16 x [m, k] -> out [m, n] = x @ W.T (+ bias) for a 4-bit weight W [n, k]
     with one scale per 32 values, from quantize_mx(w, torch.float4_e2m1fn_x2)."""
-    codes, scale = _mxfp4_weight(x, w)
-    m, k = x.shape
-    n = w.shape[0]
+    device, px, pq, ps, m, n, k = _mxfp4_operands(x, w)
+    pb = None
     if bias is not None:
-        _together(x, (bias, "bias"))
-        if bias.dtype != torch.bfloat16 or bias.shape != (n,):
+        pb = _gpu(bias, "bias", device)
+        if bias.dtype is not torch.bfloat16 or bias.shape != (n,):
             raise ValueError("bias must be bfloat16 [n]")
-    if out_dtype not in (torch.bfloat16, torch.float32):
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise ValueError("out_dtype must be bfloat16 or float32")
-    od = {torch.bfloat16: SFR_OUT_BF16, torch.float32: SFR_OUT_F32}[out_dtype]
-    lib = load()
-    with _On(x, stream) as hs:
-        out = _out_like(out, (m, n), out_dtype, x.device)
-        ptr, nbytes, work = _mxfp4_workspace(lib, m, n, k, x.device)
-        _check(lib.mxfp4_linear(x.data_ptr(), m, k, codes.data_ptr(), scale.data_ptr(), n,
-                                None if bias is None else bias.data_ptr(), out.data_ptr(), od, ptr, nbytes, hs),
-               "mxfp4_linear")
+    out = _output(out, m, n, out_dtype, x)
+    nbytes = _mxfp4_workspace_bytes(m, n, k)
+    work = x.new_empty((nbytes,), dtype=torch.uint8) if nbytes else None
+    _check(load().mxfp4_linear(px, m, k, pq, ps, n, pb, out.data_ptr(),
+                               SFR_OUT_BF16 if out_dtype is torch.bfloat16 else SFR_OUT_F32,
+                               work.data_ptr() if nbytes else None, nbytes, _raw_stream(device)), "mxfp4_linear")
     return out
 
 
-def mxfp4_gated_linear(x: torch.Tensor, w: MxTensor, activation: str = "silu", out: Optional[torch.Tensor] = None,
-                       stream=None) -> torch.Tensor:
+@_placed
+def mxfp4_gated_linear(x: torch.Tensor, w: MxTensor, activation: str = "silu",
+                       out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """gated_linear for a 4-bit weight [2 f, k] from quantize_mx(w, torch.float4_e2m1fn_x2)."""
-    codes, scale = _mxfp4_weight(x, w)
+    device, px, pq, ps, m, n, k = _mxfp4_operands(x, w)
     act = _act_enum(activation)
-    m, k = x.shape
-    if w.shape[0] % 2 != 0:
+    if n % 2 != 0:
         raise ValueError("w must be [2 f, k]")
-    f = w.shape[0] // 2
-    lib = load()
-    with _On(x, stream) as hs:
-        out = _out_like(out, (m, f), torch.bfloat16, x.device)
-        ptr, nbytes, work = _mxfp4_workspace(lib, m, 2 * f, k, x.device)
-        _check(lib.mxfp4_gated_linear(x.data_ptr(), m, k, codes.data_ptr(), scale.data_ptr(), f, act, out.data_ptr(),
-                                      ptr, nbytes, hs), "mxfp4_gated_linear")
+    out = _output(out, m, n // 2, torch.bfloat16, x)
+    _check(load().mxfp4_gated_linear(px, m, k, pq, ps, n // 2, act, out.data_ptr(), _raw_stream(device)),
+           "mxfp4_gated_linear")
     return out

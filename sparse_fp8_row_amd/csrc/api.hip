@@ -252,7 +252,7 @@ sfr_status gated_linear_bf16(const uint16_t* x, int64_t m, int64_t k, const uint
   if (!aligned16(x) || !aligned16(w) || !aligned16(h) || (save != SFR_SAVE_NONE && !aligned16(gu)) ||
       (save8(save) && !aligned16(gu_scale)))
     return SFR_ERR_ALIGN;
-  const sfr::GatedArgs a{x, w, m, k, f, (int)act, h, (int)save, gu, gu_scale};
+  const sfr::GatedArgs a{x, w, nullptr, m, k, f, (int)act, h, (int)save, gu, gu_scale};
   return launch_status(sfr::launch_gated(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -284,7 +284,7 @@ sfr_status gated_linear_bf16_backward(const uint16_t* dh, int64_t m, int64_t k, 
 
 int64_t sfr_mxfp4_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   if (m <= 0 || m > SFR_MAX_DIM || !block_dim(n, 16) || !block_dim(k, 32) || !dense_ok(m, n)) return 0;
-  return sfr::mxfp4_workspace_bytes(m, n, k);
+  return sfr::mxfp4_workspace_bytes(m, n, k, false);
 }
 
 sfr_status mxfp4_linear(const uint16_t* x, int64_t m, int64_t k, const uint8_t* wq, const uint8_t* ws, int64_t n,
@@ -294,7 +294,7 @@ sfr_status mxfp4_linear(const uint16_t* x, int64_t m, int64_t k, const uint8_t* 
   if (m < 0 || m > SFR_MAX_DIM || (n != 0 && !block_dim(n, 16)) || !block_dim(k, 32) || !dense_ok(m, n))
     return SFR_ERR_SHAPE;
   if (m == 0 || n == 0) return SFR_OK;
-  const int64_t need = sfr::mxfp4_workspace_bytes(m, n, k);
+  const int64_t need = sfr::mxfp4_workspace_bytes(m, n, k, false);
   if (workspace_bytes < need) return SFR_ERR_SHAPE;
   if (!x || !wq || !ws || !out || (need > 0 && !workspace)) return SFR_ERR_NULL;
   if (!aligned16(x) || !aligned16(wq) || !aligned16(ws) || !aligned16(out) || (bias && !aligned16(bias)) ||
@@ -305,18 +305,15 @@ sfr_status mxfp4_linear(const uint16_t* x, int64_t m, int64_t k, const uint8_t* 
 }
 
 sfr_status mxfp4_gated_linear(const uint16_t* x, int64_t m, int64_t k, const uint8_t* wq, const uint8_t* ws, int64_t f,
-                              sfr_act_t act, uint16_t* h, void* workspace, int64_t workspace_bytes, void* stream) {
+                              sfr_act_t act, uint16_t* h, void* stream) {
   if (!act_ok(act)) return SFR_ERR_DTYPE;
   if (m < 0 || m > SFR_MAX_DIM || !block_dim(2 * f, 64) || !block_dim(k, 32) || !dense_ok(m, 2 * f))
     return SFR_ERR_SHAPE;
   if (m == 0) return SFR_OK;
-  const int64_t need = sfr::mxfp4_workspace_bytes(m, 2 * f, k);
-  if (workspace_bytes < need) return SFR_ERR_SHAPE;
-  if (!x || !wq || !ws || !h || (need > 0 && !workspace)) return SFR_ERR_NULL;
-  if (!aligned16(x) || !aligned16(wq) || !aligned16(ws) || !aligned16(h) || (need > 0 && !aligned16(workspace)))
-    return SFR_ERR_ALIGN;
+  if (!x || !wq || !ws || !h) return SFR_ERR_NULL;
+  if (!aligned16(x) || !aligned16(wq) || !aligned16(ws) || !aligned16(h)) return SFR_ERR_ALIGN;
   const sfr::StreamArgs a{x, wq, ws, m, k, f, true, (int)act, nullptr, h, (int)SFR_OUT_BF16};
-  return launch_status(sfr::launch_mxfp4(a, workspace, static_cast<hipStream_t>(stream)));
+  return launch_status(sfr::launch_mxfp4(a, nullptr, static_cast<hipStream_t>(stream)));
 }
 
 const char* sfr_status_string(sfr_status s) {

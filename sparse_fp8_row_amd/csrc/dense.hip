@@ -15,6 +15,7 @@ enum { EPI_PLAIN = 0, EPI_GATED = 1 };
 
 struct DenseParams {
   const uint16_t *x, *w;
+  const uint8_t* w_scale;  // CODES: w holds the codes
   int64_t ldx, ldw;
   int64_t rows_m, rows_n;  // rows of X; rows of W (GATED: of one half)
   int64_t k;
@@ -26,6 +27,31 @@ struct DenseParams {
   GatedOut gated;
 };
 
+// Where this workgroup's outputs go: the output, or its slice's partial sums.
+__device__ __forceinline__ PlainOut plain_of(const DenseParams& p) {
+  PlainOut o = p.plain;
+  if (p.partial) {
+    o.out = p.partial + (int64_t)blockIdx.y * o.m * o.n;
+    o.bias = nullptr;
+    o.out_fmt = OUT_F32;
+  }
+  return o;
+}
+
+// The W operand's loader in the three forms.
+template <int LW, int BR, int NW, bool PAIR>
+struct WLoader {
+  Loader<LW, BR, NW, PAIR> rows;
+  __device__ __forceinline__ WLoader(const DenseParams& p, int64_t r0, int64_t k0, int wave, int lane)
+      : rows(p.w, p.ldw, r0, p.rows_n, k0, wave, lane) {}
+};
+template <int BR, int NW, bool PAIR>
+struct WLoader<CODES, BR, NW, PAIR> {
+  CodeLoader<BR, NW, PAIR> codes;
+  __device__ __forceinline__ WLoader(const DenseParams& p, int64_t r0, int64_t k0, int wave, int lane)
+      : codes(p.w, p.w_scale, p.k, r0, p.rows_n, k0, wave, lane) {}
+};
+
 // ---------------------------------------------------------------------------
 // Tiled kernel: BN x BM outputs per workgroup, WN x WM wavefronts of 64 (n) x
 // BM / WM (m), S stages of BK in LDS.
@@ -35,7 +61,9 @@ __global__ __launch_bounds__(64 * WN * WM) void dense_tile_kernel(DenseParams p)
   constexpr int NW = WN * WM, FM = BM / WM / 16, FN = 4;
   constexpr bool PAIR = EPI == EPI_GATED;
   constexpr int WB = BN * BK * 2, XB = BM * BK * 2, STAGE = WB + XB;
-  constexpr int LPS = BN / 8 / NW + BM / 8 / NW;  // loads per wavefront and stage
+  constexpr bool FP4 = LW == CODES;
+  // loads per wavefront and stage into LDS; of codes
+  constexpr int LPS = (FP4 ? 0 : BN / 8 / NW) + BM / 8 / NW, LPC = FP4 ? CodeLoader<BN, NW, PAIR>::LOADS : 0;
   static_assert(BN == WN * 64, "64 weight rows per wavefront");
   static_assert(NW * FM * 16 * 128 <= S * STAGE, "epilogue regions fit");
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
@@ -49,14 +77,21 @@ __global__ __launch_bounds__(64 * WN * WM) void dense_tile_kernel(DenseParams p)
   const int kdim = (int)min(p.k - k0, p.k_per_split);
   const int KT = (kdim + BK - 1) / BK;
 
-  Loader<LW, BN, NW, PAIR> lw(p.w, p.ldw, n0, p.rows_n, k0, p.k, wave, lane);
-  Loader<LX, BM, NW, false> lx(p.x, p.ldx, m0, p.rows_m, k0, p.k, wave, lane);
-  const Reader<LW, BN> rw(lane);
-  const Reader<LX, BM> rx(lane);
+  WLoader<LW, BN, NW, PAIR> lw(p, n0, k0, wave, lane);
+  Loader<LX, BM, NW, false> lx(p.x, p.ldx, m0, p.rows_m, k0, wave, lane);
+  const Reader<FP4 ? ROWS : LW, BN, FN> rw(wn * FN, lane);
+  const Reader<LX, BM, FM> rx(wm * FM, lane);
+  // Puts stage kt in flight.  CODES: its codes were fetched one stage ago; they
+  // go to LDS and the next stage's are fetched.
   auto load = [&](int kt) __attribute__((always_inline)) {
     uint8_t* s = smem + (kt % S) * STAGE;
-    lw.stage(s, kdim - kt * BK);
     lx.stage(s + WB, kdim - kt * BK);
+    if constexpr (FP4) {
+      lw.codes.put(s);
+      lw.codes.fetch(kdim - (kt + 1) * BK);
+    } else {
+      lw.rows.stage(s, kdim - kt * BK);
+    }
   };
 
   v4f acc[FN][FM];
@@ -65,30 +100,29 @@ __global__ __launch_bounds__(64 * WN * WM) void dense_tile_kernel(DenseParams p)
 #pragma unroll
     for (int j = 0; j < FM; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
+  if constexpr (FP4) lw.codes.fetch(kdim);
 #pragma unroll
   for (int s = 0; s < S - 1; ++s)
     if (s < KT) load(s);
   for (int kt = 0; kt < KT; ++kt) {
-    // stage kt has landed once only the later stages' loads are pending
-    if (kt + S - 2 < KT) wait_vm<(S - 2) * LPS>();
+    // stage kt has landed once only the later stages' loads (and the codes
+    // fetched with and after it) are pending
+    if (kt + S - 2 < KT) wait_vm<(S - 2) * LPS + (S - 1) * LPC>();
     else wait_vm<0>();
     wait_lds();  // this wavefront's reads of the slot to be refilled are done
     wg_barrier();
     if (kt + S - 1 < KT) load(kt + S - 1);
     const uint8_t* tw = smem + (kt % S) * STAGE;
     const uint8_t* tx = tw + WB;
+    v8bf a[2][FN], b[2][FM];
+    rw.read(a, tw);
+    rx.read(b, tx);
 #pragma unroll
-    for (int kk = 0; kk < BK / 32; ++kk) {
-      v8bf a[FN], b[FM];
-#pragma unroll
-      for (int i = 0; i < FN; ++i) a[i] = rw.read(tw, wn * FN + i, kk);
-#pragma unroll
-      for (int j = 0; j < FM; ++j) b[j] = rx.read(tx, wm * FM + j, kk);
+    for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
       for (int i = 0; i < FN; ++i)
 #pragma unroll
-        for (int j = 0; j < FM; ++j) acc[i][j] = mfma16(a[i], b[j], acc[i][j]);
-    }
+        for (int j = 0; j < FM; ++j) acc[i][j] = mfma16(a[kk][i], b[kk][j], acc[i][j]);
   }
   wait_lds();
   wg_barrier();  // every wavefront is done with the stages: their LDS becomes the epilogue's
@@ -107,14 +141,141 @@ __global__ __launch_bounds__(64 * WN * WM) void dense_tile_kernel(DenseParams p)
     }
     gated_epilogue<FM>(g, u, p.gated, mb, n0 + wn * 32, lane, region);
   } else {
-    PlainOut o = p.plain;
-    if (p.partial) {
-      o.out = p.partial + (int64_t)blockIdx.y * o.m * o.n;
-      o.bias = nullptr;
-      o.out_fmt = OUT_F32;
-    }
-    plain_epilogue<FM>(acc, o, mb, n0 + wn * 64, lane, region);
+    plain_epilogue<FM>(acc, plain_of(p), mb, n0 + wn * 64, lane, region);
   }
+}
+
+// ---------------------------------------------------------------------------
+// Wide kernel: 256 x 256 outputs, eight wavefronts in two groups of four (one
+// wavefront of each group per SIMD), 128 KB of LDS in two stages of BK.
+//
+// Each operand's stage is two half tiles of 128 rows.  A wavefront owns 64
+// rows of each W half (group g: rows 64 g ..) and 32 rows of each X half: 128 x
+// 64 outputs.  One step of k is two phases, each: read operands from LDS and put
+// half tiles of later stages in flight; barrier; 32 matrix instructions;
+// barrier.  The second group runs one barrier behind, so on every SIMD one
+// wavefront reads while the other multiplies.
+//
+//   phase  LDS reads     loads issued            outputs
+//     0    W0, X0, X1    W1 of step t + 1        W0 x (X0, X1)
+//     1    W1            W0, X0, X1 of t + 2     W1 x (X0, X1)
+// (CODES: W's codes are fetched one step earlier still; "issued" means decoded
+// into LDS, and each half tile's fetch is two loads like its ROWS form.)
+// A half tile is refilled no earlier than the phase after its last read: every
+// wavefront waits for its LDS reads before the barrier that ends its reading
+// part, and the other group is one barrier away.  Eight loads per wavefront
+// (four half tiles) stay in flight when a phase waits for the next one's.
+// Loads past the last step read zeros (they are masked) and keep the counts.
+// (Four phases of 16 instructions were slower: 1693 against the time above
+// the launcher, the barriers and the LDS latency of each phase exceeded its
+// matrix instructions.)
+// ---------------------------------------------------------------------------
+template <int LX, int LW, int EPI>
+__global__ __launch_bounds__(512, 2) void dense_wide_kernel(DenseParams p) {
+  constexpr bool PAIR = EPI == EPI_GATED, FP4 = LW == CODES;
+  constexpr int HALF = 128 * BK * 2, STAGE = 4 * HALF;  // W0, W1, X0, X1
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+
+  int64_t tm, tn;
+  if (!tile_of(blockIdx.x, p.tiles_m, p.tiles_n, p.group, tm, tn)) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wn = wave >> 2, wm = wave & 3;
+  constexpr int HN = PAIR ? 64 : 128;  // W rows (of one of the pair) per half tile
+  const int64_t m0 = tm * 256, n0 = tn * (2 * HN);
+  const int64_t k0 = blockIdx.y * p.k_per_split;
+  const int kdim = (int)min(p.k - k0, p.k_per_split), KT = (kdim + BK - 1) / BK;
+
+  WLoader<LW, 128, 8, PAIR> lw0(p, n0, k0, wave, lane);
+  WLoader<LW, 128, 8, PAIR> lw1(p, n0 + HN, k0, wave, lane);
+  Loader<LX, 128, 8, false> lx0(p.x, p.ldx, m0, p.rows_m, k0, wave, lane);
+  Loader<LX, 128, 8, false> lx1(p.x, p.ldx, m0 + 128, p.rows_m, k0, wave, lane);
+  const Reader<FP4 ? ROWS : LW, 128, 4> rw(wn * 4, lane);
+  const Reader<LX, 128, 2> rx(wm * 2, lane);
+
+  v4f acc[2][2][4][2];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) acc[i >> 4][(i >> 3) & 1][(i >> 1) & 3][i & 1] = v4f{0.f, 0.f, 0.f, 0.f};
+
+  auto load_x = [&](int t) __attribute__((always_inline)) {
+    uint8_t* s = smem + (t & 1) * STAGE;
+    lx0.stage(s + 2 * HALF, kdim - t * BK);
+    lx1.stage(s + 3 * HALF, kdim - t * BK);
+  };
+  // half tile `part` of W; CODES: the codes fetched one step ago go to LDS and the next step's are fetched
+  auto load_w = [&](auto& l, int part, int t) __attribute__((always_inline)) {
+    uint8_t* tile = smem + (t & 1) * STAGE + part * HALF;
+    if constexpr (FP4) {
+      l.codes.put(tile);
+      l.codes.fetch(kdim - (t + 1) * BK);
+    } else {
+      l.rows.stage(tile, kdim - t * BK);
+    }
+  };
+  if constexpr (FP4) {
+    lw0.codes.fetch(kdim);
+    lw1.codes.fetch(kdim);
+  }
+  load_w(lw0, 0, 0);
+  load_x(0);
+  load_w(lw1, 1, 0);
+  load_w(lw0, 0, 1);
+  load_x(1);
+  wait_vm<8>();
+  wait_lds();
+  wg_barrier();
+  if (wn == 1) wg_barrier();
+
+  v8bf w[2][4], x0[2][2], x1[2][2];
+  auto multiply = [&](v4f(&c0)[4][2], v4f(&c1)[4][2]) __attribute__((always_inline)) {
+    wait_vm<8>();
+    wait_lds();
+    wg_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) c0[i][j] = mfma16(w[kk][i], x0[kk][j], c0[i][j]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) c1[i][j] = mfma16(w[kk][i], x1[kk][j], c1[i][j]);
+      }
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+    wg_barrier();
+  };
+  for (int t = 0; t < KT; ++t) {
+    const uint8_t* s = smem + (t & 1) * STAGE;
+    rx.read2(x0, x1, s + 2 * HALF, HALF);
+    rw.read(w, s);
+    load_w(lw1, 1, t + 1);
+    multiply(acc[0][0], acc[0][1]);
+
+    rw.read(w, s + HALF);
+    load_w(lw0, 0, t + 2);
+    load_x(t + 2);
+    multiply(acc[1][0], acc[1][1]);
+  }
+  if (wn == 0) wg_barrier();
+  wait_vm<0>();
+  wg_barrier();  // every load has landed: the stages become the epilogue's
+
+  uint8_t* region = smem + wave * 16384;
+#pragma unroll
+  for (int hw = 0; hw < 2; ++hw)
+#pragma unroll
+    for (int hx = 0; hx < 2; ++hx) {
+      const int64_t mb = m0 + hx * 128 + wm * 32;
+      v4f(&a)[4][2] = acc[hw][hx];
+      if constexpr (EPI == EPI_GATED) {
+        const v4f g[2][2] = {{a[0][0], a[0][1]}, {a[2][0], a[2][1]}};
+        const v4f u[2][2] = {{a[1][0], a[1][1]}, {a[3][0], a[3][1]}};
+        gated_epilogue<2>(g, u, p.gated, mb, n0 + hw * 64 + wn * 32, lane, region);
+      } else {
+        plain_epilogue<2>(a, plain_of(p), mb, n0 + hw * 128 + wn * 64, lane, region);
+      }
+    }
 }
 
 // Sums the slices in order, adds the bias, rounds once.
@@ -156,42 +317,119 @@ hipError_t run_tile(DenseParams p, int slices, hipStream_t stream) {
 }
 
 template <int LX, int LW, int EPI>
-hipError_t run_dense(const DenseParams& p, int slices, hipStream_t stream) {
-  if (p.rows_m > 64) return run_tile<LX, LW, EPI, 128, 128, 2, 2, 2>(p, slices, stream);
-  return run_tile<LX, LW, EPI, 64, 64, 1, 4, 3>(p, slices, stream);
+hipError_t run_wide(DenseParams p, int slices, hipStream_t stream) {
+  constexpr int bytes = 2 * 4 * 128 * BK * 2;
+  auto* kernel = dense_wide_kernel<LX, LW, EPI>;
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != hipSuccess) return e;
+  constexpr int cover = EPI == EPI_GATED ? 128 : 256;
+  p.tiles_m = (p.rows_m + 255) / 256;
+  p.tiles_n = (p.rows_n + cover - 1) / cover;
+  p.group = 8;
+  const int64_t grid = (p.tiles_m * p.tiles_n + 7) / 8 * 8;
+  kernel<<<dim3((unsigned)grid, (unsigned)slices), dim3(512), bytes, stream>>>(p);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Choice of kernel and of the number of slices of the sum: the smallest
+// modelled time.  A configuration covers BN x BM outputs per workgroup, `slots`
+// workgroups at once on 256 CUs; a round takes `full` per stage of k when
+// every CU holds as many workgroups as fit, `one` when it holds at most one
+// (us per stage, measured: see the table of the launchers' comment).  Slices
+// (plain outputs only) add a pass over their binary32 partial sums.
+// ---------------------------------------------------------------------------
+enum { CFG_WIDE = 0, CFG_128 = 1, CFG_128x64 = 2, CFG_64 = 3, CFG_COUNT = 4 };
+struct Config {
+  int bn, bm, per_cu;
+  double full, one;
+};
+constexpr Config kConfigs[CFG_COUNT] = {
+    {256, 256, 1, 1.34, 1.34}, {128, 128, 2, 0.95, 0.58}, {128, 64, 2, 0.64, 0.40}, {64, 64, 3, 0.55, 0.30}};
+struct Choice {
+  int config, slices;
+  int64_t k_per_split;
+};
+
+// n: columns of the output's tiles (2 f when gated).
+Choice choose(int64_t m, int64_t n, int64_t k, bool can_slice) {
+  const int64_t stages = (k + BK - 1) / BK;
+  Choice best{CFG_64, 1, k};
+  double least = 1e300;
+  for (int c = 0; c < CFG_COUNT; ++c) {
+    const Config& g = kConfigs[c];
+    const int64_t tiles = ((m + g.bm - 1) / g.bm) * ((n + g.bn - 1) / g.bn);
+    for (int s = 1; s <= (can_slice ? 16 : 1); ++s) {
+      const int64_t per = (stages + s - 1) / s;
+      if (s > 1 && (per < 8 || (stages + per - 1) / per != s)) continue;
+      const int64_t total = tiles * s, slots = 256 * g.per_cu, rest = total % slots;
+      double t = (total / slots) * g.full + (rest == 0 ? 0 : rest <= 256 ? g.one : g.full);
+      t = t * per + 3.0 + (s > 1 ? 3.0 + 8.0 * s * m * n / 3.5e6 : 0.0);
+      if (t < least) {
+        least = t;
+        best = Choice{c, s, s == 1 ? k : per * BK};
+      }
+    }
+  }
+  return best;
+}
+
+template <int LX, int LW, int EPI>
+hipError_t run_dense(DenseParams p, const Choice& c, void* workspace, hipStream_t stream) {
+  p.k_per_split = c.k_per_split;
+  p.partial = c.slices > 1 ? static_cast<float*>(workspace) : nullptr;
+  hipError_t e = c.config == CFG_WIDE     ? run_wide<LX, LW, EPI>(p, c.slices, stream)
+                 : c.config == CFG_128    ? run_tile<LX, LW, EPI, 128, 128, 2, 2, 2>(p, c.slices, stream)
+                 : c.config == CFG_128x64 ? run_tile<LX, LW, EPI, 128, 64, 2, 2, 3>(p, c.slices, stream)
+                                          : run_tile<LX, LW, EPI, 64, 64, 1, 4, 3>(p, c.slices, stream);
+  if (e != hipSuccess || c.slices == 1) return e;
+  const int64_t quads = p.plain.m * p.plain.n / 4;
+  dense_reduce_kernel<<<dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream>>>(p.partial, c.slices, p.plain);
+  return hipGetLastError();
+}
+
+int64_t slice_bytes(int64_t m, int64_t n, int64_t k) {
+  const Choice c = choose(m, n, k, true);
+  return c.slices > 1 ? c.slices * m * n * 4 : 0;
 }
 
 }  // namespace
 
-
+// Workspace: the slices' partial sums.
+int64_t dense_nt_workspace_bytes(int64_t m, int64_t n, int64_t k) { return slice_bytes(m, n, k); }
+int64_t dense_dx_workspace_bytes(int64_t m, int64_t k, int64_t f2) { return slice_bytes(m, k, f2); }
 
 hipError_t launch_gated_dense(const GatedArgs& a, hipStream_t stream) {
   DenseParams p{};
   p.x = a.x;
-  p.w = a.w;
+  p.w = static_cast<const uint16_t*>(a.w);
+  p.w_scale = a.w_scale;
   p.ldx = p.ldw = a.k;
   p.rows_m = a.m;
   p.rows_n = a.f;
-  p.k = p.k_per_split = a.k;
+  p.k = a.k;
   p.gated = GatedOut{a.h, a.gu, a.gu_scale, a.m, a.f, a.act, a.gu_fmt};
-  return run_dense<ROWS, ROWS, EPI_GATED>(p, 1, stream);
+  const Choice c = choose(a.m, 2 * a.f, a.k, false);
+  return a.w_scale ? run_dense<ROWS, CODES, EPI_GATED>(p, c, nullptr, stream)
+                   : run_dense<ROWS, ROWS, EPI_GATED>(p, c, nullptr, stream);
 }
 
-hipError_t launch_dense_nt(const uint16_t* x, const uint16_t* w, int64_t m, int64_t n, int64_t k, const uint16_t* bias,
-                           void* out, int out_fmt, hipStream_t stream) {
+hipError_t launch_mxfp4_dense(const StreamArgs& a, void* workspace, hipStream_t stream) {
   DenseParams p{};
-  p.x = x;
-  p.w = w;
-  p.ldx = p.ldw = k;
-  p.rows_m = m;
-  p.rows_n = n;
-  p.k = p.k_per_split = k;
-  p.plain = PlainOut{out, bias, m, n, out_fmt};
-  return run_dense<ROWS, ROWS, EPI_PLAIN>(p, 1, stream);
+  p.x = a.x;
+  p.w = static_cast<const uint16_t*>(a.w);
+  p.w_scale = a.w_scale;
+  p.ldx = a.k;
+  p.rows_m = a.m;
+  p.rows_n = a.rows;
+  p.k = a.k;
+  p.plain = PlainOut{a.out, a.bias, a.m, a.rows, a.out_fmt};
+  return run_dense<ROWS, CODES, EPI_PLAIN>(p, choose(a.m, a.rows, a.k, true), workspace, stream);
 }
 
 hipError_t launch_dense_dx(const uint16_t* dgu, const uint16_t* w, int64_t m, int64_t k, int64_t f2, uint16_t* dx,
-                           hipStream_t stream) {
+                           void* workspace, hipStream_t stream) {
   DenseParams p{};
   p.x = dgu;
   p.w = w;
@@ -199,9 +437,9 @@ hipError_t launch_dense_dx(const uint16_t* dgu, const uint16_t* w, int64_t m, in
   p.ldw = k;
   p.rows_m = m;
   p.rows_n = k;
-  p.k = p.k_per_split = f2;
+  p.k = f2;
   p.plain = PlainOut{dx, nullptr, m, k, OUT_BF16};
-  return run_dense<ROWS, COLS, EPI_PLAIN>(p, 1, stream);
+  return run_dense<ROWS, COLS, EPI_PLAIN>(p, choose(m, k, f2, true), workspace, stream);
 }
 
 hipError_t launch_dense_dw(const uint16_t* dgu, const uint16_t* x, int64_t m, int64_t k, int64_t f2, uint16_t* dw,
@@ -213,9 +451,9 @@ hipError_t launch_dense_dw(const uint16_t* dgu, const uint16_t* x, int64_t m, in
   p.ldw = k;
   p.rows_m = f2;
   p.rows_n = k;
-  p.k = p.k_per_split = m;
+  p.k = m;
   p.plain = PlainOut{dw, nullptr, f2, k, OUT_BF16};
-  return run_dense<COLS, COLS, EPI_PLAIN>(p, 1, stream);
+  return run_dense<COLS, COLS, EPI_PLAIN>(p, choose(f2, k, m, false), nullptr, stream);
 }
 
 }  // namespace sfr

@@ -97,26 +97,30 @@ hipError_t launch_gated(const GatedArgs& a, hipStream_t stream) {
   return launch_gated_dense(a, stream);
 }
 
-// Workspace: dgu [m, 2 f] bf16, then (8-bit x) x [m, k] bf16.
+// Workspace: dgu [m, 2 f] bf16, then what one of the products needs at a time:
+// dx its partial sums, dW (8-bit x) x [m, k] decoded to bf16.
 int64_t gated_backward_workspace_bytes(int64_t m, int64_t k, int64_t f, bool x_mx) {
-  return align256(m * 2 * f * 2) + (x_mx ? align256(m * k * 2) : 0);
+  if (m == 0) return 0;
+  const int64_t partial = dense_dx_workspace_bytes(m, k, 2 * f), decoded = x_mx ? m * k * 2 : 0;
+  return align256(m * 2 * f * 2) + align256(partial > decoded ? partial : decoded);
 }
 
 hipError_t launch_gated_backward(const GatedBackwardArgs& a, void* workspace, hipStream_t stream) {
   uint16_t* dgu = static_cast<uint16_t*>(workspace);
-  uint16_t* xw = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + align256(a.m * 2 * a.f * 2));
+  void* more = static_cast<uint8_t*>(workspace) + align256(a.m * 2 * a.f * 2);
   if (a.m == 0) return a.dw ? launch_dense_dw(dgu, nullptr, 0, a.k, 2 * a.f, a.dw, stream) : hipSuccess;  // zeros
   hipError_t e = a.gu_fmt == GU_BF16   ? run_grad<GU_BF16>(a, dgu, stream)
                  : a.gu_fmt == GU_E4M3 ? run_grad<GU_E4M3>(a, dgu, stream)
                                        : run_grad<GU_E5M2>(a, dgu, stream);
   if (e != hipSuccess) return e;
   if (a.dx) {
-    e = launch_dense_dx(dgu, a.w, a.m, a.k, 2 * a.f, a.dx, stream);
+    e = launch_dense_dx(dgu, a.w, a.m, a.k, 2 * a.f, a.dx, more, stream);
     if (e != hipSuccess) return e;
   }
   if (a.dw) {
     const uint16_t* x = static_cast<const uint16_t*>(a.x);
     if (a.x_fmt != GU_BF16) {
+      uint16_t* const xw = static_cast<uint16_t*>(more);
       e = launch_dequantize_mx(static_cast<const uint8_t*>(a.x), a.x_scale, a.m, a.k,
                                a.x_fmt == GU_E4M3 ? MX_E4M3 : MX_E5M2, xw, stream);
       if (e != hipSuccess) return e;
@@ -127,20 +131,17 @@ hipError_t launch_gated_backward(const GatedBackwardArgs& a, void* workspace, hi
   return e;
 }
 
-// A 4-bit weight: few rows read the codes directly, more decode it once into
-// the workspace (exactly) for the dense product.
-int64_t mxfp4_workspace_bytes(int64_t m, int64_t n, int64_t k) { return stream_rows(m) ? 0 : align256(n * k * 2); }
+int64_t mxfp4_workspace_bytes(int64_t m, int64_t n, int64_t k, bool gated) {
+  return gated || stream_rows(m) ? 0 : align256(dense_nt_workspace_bytes(m, n, k));
+}
 
 hipError_t launch_mxfp4(const StreamArgs& a, void* workspace, hipStream_t stream) {
   if (stream_rows(a.m)) return launch_stream(a, stream);
-  uint16_t* w = static_cast<uint16_t*>(workspace);
-  const int64_t n = a.gated ? 2 * a.rows : a.rows;
-  hipError_t e = launch_dequantize_mx(static_cast<const uint8_t*>(a.w), a.w_scale, n, a.k, MX_E2M1, w, stream);
-  if (e != hipSuccess) return e;
-  if (!a.gated) return launch_dense_nt(a.x, w, a.m, a.rows, a.k, a.bias, a.out, a.out_fmt, stream);
+  if (!a.gated) return launch_mxfp4_dense(a, workspace, stream);
   GatedArgs g{};
   g.x = a.x;
-  g.w = w;
+  g.w = a.w;
+  g.w_scale = a.w_scale;
   g.m = a.m;
   g.k = a.k;
   g.f = a.rows;

@@ -18,15 +18,16 @@
 
 namespace sfr {
 
-enum { ROWS = 0, COLS = 1 };
+//   CODES: a 4-bit weight, row-major codes and block scales; decoded into the
+//     ROWS layout of LDS by the wavefronts that load it.
+enum { ROWS = 0, COLS = 1, CODES = 2 };
 
-typedef __bf16 v4bf __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void* lds_void_t;
 
 constexpr int BK = 64;  // k of one stage
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buf_rsrc(const void* base, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)(bytes > 0 ? bytes : 0), 0x00020000);
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buf_rsrc(const void* base, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, bytes, 0x00020000);
 }
 
 // Lane l's 16 bytes at `voff` land at lds + 16 l.  The range check covers the
@@ -55,15 +56,16 @@ __device__ __forceinline__ void wg_barrier() {
 // LDS layouts of one operand tile of BR rows x BK.
 //   ROWS: 128 bytes per row; 16-byte chunk c of row r at c ^ (r % 8), so the 8
 //     lanes of one 128-byte LDS cycle (8 rows, one chunk) take all banks once.
-//   COLS: BR * 2 bytes per k; a transposing read takes 32 bytes of each of four
-//     k (per 16 lanes), whose rows start at the same bank, so the 32-byte unit
-//     u of row k sits at u ^ cols_swizzle(k).
+//   COLS: BR * 2 bytes per k; 32 lanes of a transposing read take 32 bytes of
+//     each of eight k (0 .. 3 and 8 .. 11 from a multiple of 16), so the
+//     32-byte unit u of k sits at u ^ cols_swizzle(k): eight different units of
+//     a 256-byte line of banks (BR = 64: a line holds two k, four units each).
 // A 1 KB load covers 8 rows (ROWS) or 512 / BR of k (COLS); the swizzles are
 // applied to the global address of each lane.
 // ---------------------------------------------------------------------------
 template <int BR>
 __device__ __forceinline__ int cols_swizzle(int k) {
-  return BR >= 128 ? (k & 3) | (((k >> 3) & 1) << 2) : (k & 3);
+  return BR >= 128 ? (k & 3) | (((k >> 3) & 1) << 2) : ((k >> 1) & 1) | (((k >> 3) & 1) << 1);
 }
 
 // One operand's loads, shared evenly by NW wavefronts; load j = wave + q * NW.
@@ -76,84 +78,246 @@ struct Loader {
   static_assert(BR / 8 % NW == 0, "loads split evenly");
   static_assert(!PAIR || (L == ROWS && NW % 4 == 0), "a wavefront's loads stay in one half");
   const uint8_t* base;
-  int64_t left;  // bytes from base to the end of what may be read
-  int64_t step;  // bytes per stage of k
-  int voff[PER];
-  int wave, chunk;
+  int64_t step;   // bytes per stage of k
+  int voff[PER];  // past the range for rows that do not exist
+  int first[PER];  // the load's first k in the stage
+  int wave;
 
-  // rows r0 .. of `rows`; ld elements between stored rows; k from k0 (a multiple of BK) of `kdim`
-  __device__ __forceinline__ Loader(const uint16_t* p, int64_t ld, int64_t r0, int64_t rows, int64_t k0, int64_t kdim,
-                                    int wave_, int lane)
+  // rows r0 .. of `rows`; ld elements between stored rows; k from k0 on
+  __device__ __forceinline__ Loader(const uint16_t* p, int64_t ld, int64_t r0, int64_t rows, int64_t k0, int wave_,
+                                    int lane)
       : wave(wave_) {
+    const int n = (int)min(rows - r0, (int64_t)BR);
     if constexpr (L == ROWS) {
       const int part = PAIR ? (wave >> 1) & 1 : 0;
-      const int64_t first = part * rows + r0;
-      const int64_t n = min(rows - r0, (int64_t)(PAIR ? BR / 2 : BR));
-      base = reinterpret_cast<const uint8_t*>(p + first * ld + k0);
-      left = (n * ld - k0) * 2;
+      base = reinterpret_cast<const uint8_t*>(p + (part * rows + r0) * ld + k0);
       step = BK * 2;
-      chunk = (lane & 7) ^ (lane >> 3);
+      const int chunk = (lane & 7) ^ (lane >> 3);
 #pragma unroll
       for (int q = 0; q < PER; ++q) {
         const int j = wave + q * NW;
         const int row = (PAIR ? (j >> 2) * 16 + (j & 1) * 8 : j * 8) + (lane >> 3);
-        voff[q] = row * (int)(ld * 2) + chunk * 16;
+        voff[q] = row < n ? row * (int)(ld * 2) + chunk * 16 : kPastRange;
+        first[q] = chunk * 8;
       }
     } else {
       constexpr int RPL = 512 / BR, CPR = 64 / RPL;  // k per load, 16-byte chunks per k
       base = reinterpret_cast<const uint8_t*>(p + k0 * ld + r0);
-      left = ((kdim - k0) * ld - r0) * 2;
       step = BK * 2 * ld;
-      chunk = 0;
 #pragma unroll
       for (int q = 0; q < PER; ++q) {
         const int k = (wave + q * NW) * RPL + lane / CPR;
-        voff[q] = k * (int)(ld * 2) + 16 * ((lane % CPR) ^ (cols_swizzle<BR>(k) << 1));
+        const int chunk = (lane % CPR) ^ (cols_swizzle<BR>(k) << 1);
+        voff[q] = chunk * 8 < n ? k * (int)(ld * 2) + 16 * chunk : kPastRange;
+        first[q] = k;
       }
     }
   }
   // Puts the next stage's loads in flight and moves on.  k_left: k not yet
-  // loaded; in a ROWS operand's last stage the chunks past it read zeros (a
-  // COLS operand's lie past the range by themselves).
+  // loaded; what lies past it reads zeros.  Every lane that is not masked reads
+  // inside the operand (rows are a multiple of 8 long), so the range is fixed.
   __device__ __forceinline__ void stage(uint8_t* lds, int k_left) {
-    const __amdgpu_buffer_rsrc_t r = buf_rsrc(base, min(left, (int64_t)0x7FFFFF00));
+    const __amdgpu_buffer_rsrc_t r = buf_rsrc(base, 0x7FFFFF00);
 #pragma unroll
-    for (int q = 0; q < PER; ++q) {
-      int v = voff[q];
-      if constexpr (L == ROWS) v = chunk * 8 < k_left ? v : kPastRange;
-      buf_to_lds(r, lds + (wave + q * NW) * 1024, v);
-    }
+    for (int q = 0; q < PER; ++q) buf_to_lds(r, lds + (wave + q * NW) * 1024, first[q] < k_left ? voff[q] : kPastRange);
     base += step;
-    left -= step;
   }
 };
 
-// Operand reads of 16-row fragments from a tile of BR rows.
-template <int L, int BR>
-struct Reader {
-  int a, b, c;  // lane parts of the address
-  __device__ __forceinline__ Reader(int lane) {
-    const int r16 = lane & 15, lg = lane >> 4;
-    if constexpr (L == ROWS) {
-      a = r16 * 128;
-      b = lg;
-      c = r16 & 7;
+// A 4-bit weight's loads: every thread of NW wavefronts holds E codes of one
+// row, decodes them (exactly) to bf16 and writes them to LDS in the ROWS layout.
+// fetch puts the next stage's codes in flight in registers, put writes them.
+// A fetch is exactly two loads (codes; scale), which the wait counts rely on.
+template <int BR, int NW, bool PAIR>
+struct CodeLoader {
+  static constexpr int E = BR * BK / (64 * NW), LOADS = 2;
+  static_assert(E == 16 || E == 32, "8 or 16 bytes of codes, one block's scale");
+  __amdgpu_buffer_rsrc_t rq, rs;
+  int voff, soff, first, lds;
+  bool exists;
+  uint32_t xor1;
+  v4i code;
+  uint32_t scale;
+
+  __device__ __forceinline__ CodeLoader(const void* q, const uint8_t* sc, int64_t k, int64_t r0, int64_t rows,
+                                        int64_t k0, int wave, int lane) {
+    constexpr int TPR = BK / E, G = 4 / TPR;  // threads per row, groups of 16 rows per wavefront
+    first = lane % TPR * E;
+    // PAIR: a wavefront's rows all belong to half wave % 2 of the weight
+    const int part = PAIR ? wave & 1 : 0, group = (PAIR ? wave >> 1 : wave) * G + lane / (16 * TPR);
+    const int row = group * 16 + lane / TPR % 16;  // from r0
+    const int r = PAIR ? (2 * group + part) * 16 + lane / TPR % 16 : row;
+    const int64_t at = part * rows + r0;
+    rq = buf_rsrc(static_cast<const uint8_t*>(q) + at * (k / 2) + k0 / 2, kPastRange);
+    rs = buf_rsrc(sc + at * (k / 32) + k0 / 32, kPastRange);
+    exists = row < rows - r0;
+    voff = row * (int)(k / 2) + first / 2;
+    soff = row * (int)(k / 32) + first / 32;
+    lds = r * 128;
+    xor1 = (uint32_t)(r & 7);
+  }
+  __device__ __forceinline__ void fetch(int k_left) {
+    const bool in = exists && first < k_left;
+    const int v = in ? voff : kPastRange;  // past the range: zeros
+    if constexpr (E == 16) {
+      typedef int v2i __attribute__((ext_vector_type(2)));
+      const v2i c = __builtin_bit_cast(v2i, __builtin_amdgcn_raw_buffer_load_b64(rq, v, 0, 0));
+      code[0] = c[0];
+      code[1] = c[1];
     } else {
-      a = (8 * lg + (r16 >> 2)) * (BR * 2) + 16 * ((r16 & 3) >> 1) + 8 * (r16 & 1);
-      b = cols_swizzle<BR>(8 * lg + (r16 >> 2));
-      c = 0;
+      code = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rq, v, 0, 0));
+    }
+    scale = __builtin_amdgcn_raw_buffer_load_b8(rs, in ? soff : kPastRange, 0, 0);
+    voff += BK / 2;
+    soff += BK / 32;
+  }
+  // Written by asm: before an ordinary LDS store the compiler waits for the
+  // global -> LDS loads in flight.  The caller waits for its LDS writes
+  // (wait_lds) before the barrier that publishes them.
+  __device__ __forceinline__ void put(uint8_t* tile) const {
+    const float f = mx_scale_value(scale & 0xFFu);
+    const uint32_t row = (uint32_t)(uintptr_t)(lds_void_t)tile + lds;
+#pragma unroll
+    for (int i = 0; i < E / 8; ++i) {
+      typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+      const uint4 v = mx_widen8_e2m1(code[i], f);
+      asm volatile("ds_write_b128 %0, %1" ::"v"(row + 16 * ((uint32_t)(first / 8 + i) ^ xor1)),
+                   "v"(v4u{v.x, v.y, v.z, v.w})
+                   : "memory");
     }
   }
-  // fragment frag (rows 16 frag ..), k 32 kk .. 32 kk + 31 of the stage
-  __device__ __forceinline__ v8bf read(const uint8_t* tile, int frag, int kk) const {
+};
+
+// Transposing reads from LDS, four (at offsets O0 .. O3) from each of N
+// addresses, and the wait for them.  One asm block: the builtin makes the
+// compiler wait for every global -> LDS load in flight before each such read,
+// which would end the prefetch; inside the block the reads have landed before
+// anything uses their registers.
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+template <int N, int O0, int O1, int O2, int O3>
+__device__ __forceinline__ void read_tr(v2u (&r)[N][4], const uint32_t (&a)[N]) {
+  static_assert(N == 1 || N == 2 || N == 4, "blocks written out below");
+  if constexpr (N == 1) {
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %4 offset:%5\n\t"
+        "ds_read_b64_tr_b16 %1, %4 offset:%6\n\t"
+        "ds_read_b64_tr_b16 %2, %4 offset:%7\n\t"
+        "ds_read_b64_tr_b16 %3, %4 offset:%8\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[0][2]), "=&v"(r[0][3])
+        : "v"(a[0]), "n"(O0), "n"(O1), "n"(O2), "n"(O3)
+        : "memory");
+  } else if constexpr (N == 2) {
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %8 offset:%10\n\t"
+        "ds_read_b64_tr_b16 %1, %8 offset:%11\n\t"
+        "ds_read_b64_tr_b16 %2, %8 offset:%12\n\t"
+        "ds_read_b64_tr_b16 %3, %8 offset:%13\n\t"
+        "ds_read_b64_tr_b16 %4, %9 offset:%10\n\t"
+        "ds_read_b64_tr_b16 %5, %9 offset:%11\n\t"
+        "ds_read_b64_tr_b16 %6, %9 offset:%12\n\t"
+        "ds_read_b64_tr_b16 %7, %9 offset:%13\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[0][2]), "=&v"(r[0][3]), "=&v"(r[1][0]), "=&v"(r[1][1]),
+          "=&v"(r[1][2]), "=&v"(r[1][3])
+        : "v"(a[0]), "v"(a[1]), "n"(O0), "n"(O1), "n"(O2), "n"(O3)
+        : "memory");
+  } else {
+    asm volatile(
+        "ds_read_b64_tr_b16 %0, %16 offset:%20\n\t"
+        "ds_read_b64_tr_b16 %1, %16 offset:%21\n\t"
+        "ds_read_b64_tr_b16 %2, %16 offset:%22\n\t"
+        "ds_read_b64_tr_b16 %3, %16 offset:%23\n\t"
+        "ds_read_b64_tr_b16 %4, %17 offset:%20\n\t"
+        "ds_read_b64_tr_b16 %5, %17 offset:%21\n\t"
+        "ds_read_b64_tr_b16 %6, %17 offset:%22\n\t"
+        "ds_read_b64_tr_b16 %7, %17 offset:%23\n\t"
+        "ds_read_b64_tr_b16 %8, %18 offset:%20\n\t"
+        "ds_read_b64_tr_b16 %9, %18 offset:%21\n\t"
+        "ds_read_b64_tr_b16 %10, %18 offset:%22\n\t"
+        "ds_read_b64_tr_b16 %11, %18 offset:%23\n\t"
+        "ds_read_b64_tr_b16 %12, %19 offset:%20\n\t"
+        "ds_read_b64_tr_b16 %13, %19 offset:%21\n\t"
+        "ds_read_b64_tr_b16 %14, %19 offset:%22\n\t"
+        "ds_read_b64_tr_b16 %15, %19 offset:%23\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(r[0][0]), "=&v"(r[0][1]), "=&v"(r[0][2]), "=&v"(r[0][3]), "=&v"(r[1][0]), "=&v"(r[1][1]),
+          "=&v"(r[1][2]), "=&v"(r[1][3]), "=&v"(r[2][0]), "=&v"(r[2][1]), "=&v"(r[2][2]), "=&v"(r[2][3]),
+          "=&v"(r[3][0]), "=&v"(r[3][1]), "=&v"(r[3][2]), "=&v"(r[3][3])
+        : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(O0), "n"(O1), "n"(O2), "n"(O3)
+        : "memory");
+  }
+}
+
+__device__ __forceinline__ v8bf join8(v2u lo, v2u hi) {
+  typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(v8bf, v4u{lo[0], lo[1], hi[0], hi[1]});
+}
+
+// Operand reads of NF 16-row fragments from `first` on of a tile of BR rows.
+template <int L, int BR, int NF>
+struct Reader {
+  uint32_t at[NF];  // ROWS: the lane's row (the chunk is XORed in); COLS: the lane's whole address, kk = 0
+  int lg, c;
+  static constexpr int HI = 4 * BR * 2, KK = 32 * BR * 2;  // COLS: from lower to upper four k; from kk = 0 to 1
+  __device__ __forceinline__ Reader(int first, int lane) {
+    const int r16 = lane & 15;
+    lg = lane >> 4;
+    c = r16 & 7;
+#pragma unroll
+    for (int i = 0; i < NF; ++i) {
+      if constexpr (L == ROWS) {
+        at[i] = (first + i) * 2048 + r16 * 128;
+      } else {
+        const int k = 8 * lg + (r16 >> 2);
+        at[i] = k * (BR * 2) + 32 * ((first + i) ^ cols_swizzle<BR>(k)) + 16 * ((r16 & 3) >> 1) + 8 * (r16 & 1);
+      }
+    }
+  }
+  // out[kk][i]: fragment i with k 32 kk .. 32 kk + 31 of the stage
+  __device__ __forceinline__ void read(v8bf (&out)[2][NF], const uint8_t* tile) const {
     if constexpr (L == ROWS) {
-      return *reinterpret_cast<const v8bf*>(tile + a + frag * 2048 + 16 * ((kk * 4 + b) ^ c));
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int i = 0; i < NF; ++i)
+          out[kk][i] = *reinterpret_cast<const v8bf*>(tile + at[i] + 16 * ((kk * 4 + lg) ^ c));
     } else {
-      const uint8_t* p = tile + a + kk * (32 * BR * 2) + 32 * (frag ^ b);
-      typedef __attribute__((address_space(3))) v4bf* lds_v4_t;
-      const v4bf lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_v4_t)(p));
-      const v4bf hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_v4_t)(p + 4 * BR * 2));
-      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      const uint32_t base = (uint32_t)(uintptr_t)(lds_void_t)tile;
+      uint32_t a[NF];
+      v2u r[NF][4];
+#pragma unroll
+      for (int i = 0; i < NF; ++i) a[i] = base + at[i];
+      read_tr<NF, 0, HI, KK, KK + HI>(r, a);
+#pragma unroll
+      for (int i = 0; i < NF; ++i) {
+        out[0][i] = join8(r[i][0], r[i][1]);
+        out[1][i] = join8(r[i][2], r[i][3]);
+      }
+    }
+  }
+  // The same of two tiles, `apart` bytes apart, in one block.
+  __device__ __forceinline__ void read2(v8bf (&o0)[2][NF], v8bf (&o1)[2][NF], const uint8_t* tile, int apart) const {
+    if constexpr (L == ROWS) {
+      read(o0, tile);
+      read(o1, tile + apart);
+    } else {
+      const uint32_t base = (uint32_t)(uintptr_t)(lds_void_t)tile;
+      uint32_t a[2 * NF];
+      v2u r[2 * NF][4];
+#pragma unroll
+      for (int i = 0; i < NF; ++i) {
+        a[i] = base + at[i];
+        a[NF + i] = a[i] + apart;
+      }
+      read_tr<2 * NF, 0, HI, KK, KK + HI>(r, a);
+#pragma unroll
+      for (int i = 0; i < NF; ++i) {
+        o0[0][i] = join8(r[i][0], r[i][1]);
+        o0[1][i] = join8(r[i][2], r[i][3]);
+        o1[0][i] = join8(r[NF + i][0], r[NF + i][1]);
+        o1[1][i] = join8(r[NF + i][2], r[NF + i][3]);
+      }
     }
   }
 };

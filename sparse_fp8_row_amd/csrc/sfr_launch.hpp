@@ -86,7 +86,9 @@ hipError_t launch_dequantize_mx(const uint8_t* q, const uint8_t* scale, int64_t 
 enum { GU_NONE = 0, GU_BF16 = 1, GU_E4M3 = 2, GU_E5M2 = 3 };
 
 struct GatedArgs {
-  const uint16_t *x, *w;  // [m, k]; [2 f, k]
+  const uint16_t* x;       // [m, k]
+  const void* w;           // [2 f, k]: bf16, or 4-bit codes
+  const uint8_t* w_scale;  // the codes' scales; null for bf16
   int64_t m, k, f;
   int act;
   uint16_t* h;  // [m, f]
@@ -112,11 +114,10 @@ struct GatedBackwardArgs {
 int64_t gated_backward_workspace_bytes(int64_t m, int64_t k, int64_t f, bool x_mx);
 hipError_t launch_gated_backward(const GatedBackwardArgs& a, void* workspace, hipStream_t stream);
 
-// Dense bf16 products: out[m, n] = x w^T (+ bias); dx = dgu w; dw = dgu^T x.
-hipError_t launch_dense_nt(const uint16_t* x, const uint16_t* w, int64_t m, int64_t n, int64_t k, const uint16_t* bias,
-                           void* out, int out_fmt, hipStream_t stream);
+// Dense products with binary32 sums: dx = dgu w; dw = dgu^T x.
+int64_t dense_dx_workspace_bytes(int64_t m, int64_t k, int64_t f2);
 hipError_t launch_dense_dx(const uint16_t* dgu, const uint16_t* w, int64_t m, int64_t k, int64_t f2, uint16_t* dx,
-                           hipStream_t stream);
+                           void* workspace, hipStream_t stream);
 hipError_t launch_dense_dw(const uint16_t* dgu, const uint16_t* x, int64_t m, int64_t k, int64_t f2, uint16_t* dw,
                            hipStream_t stream);
 
@@ -135,7 +136,10 @@ struct StreamArgs {
 };
 bool stream_rows(int64_t m);
 hipError_t launch_stream(const StreamArgs& a, hipStream_t stream);
-int64_t mxfp4_workspace_bytes(int64_t m, int64_t n, int64_t k);
+// The matrix-core form of the 4-bit linear layer (not gated), any m.
+int64_t dense_nt_workspace_bytes(int64_t m, int64_t n, int64_t k);
+hipError_t launch_mxfp4_dense(const StreamArgs& a, void* workspace, hipStream_t stream);
+int64_t mxfp4_workspace_bytes(int64_t m, int64_t n, int64_t k, bool gated);
 hipError_t launch_mxfp4(const StreamArgs& a, void* workspace, hipStream_t stream);
 
 }  // namespace sfr

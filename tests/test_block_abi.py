@@ -66,6 +66,7 @@ def test_gated_backward_validation(sfr):
     lib = sfr.load()
     need = lib.sfr_gated_backward_workspace_bytes
     assert need(4, 64, 96, 1) == 4 * 192 * 2 and need(4, 64, 96, 2) == 4 * 192 * 2 + 4 * 64 * 2
+    assert need(4, 64, 1 << 14, 1) > 4 * (1 << 15) * 2  # a long sum over f: slices
     assert need(0, 64, 96, 2) == 0 and need(4, 48, 96, 2) == 0 and need(4, 64, 96, 0) == 0 and need(-1, 64, 96, 1) == 0
     call = caller(lib.gated_linear_bf16_backward, "dh m k f act gu gs gsave x xs xsave w dx dw work bytes",
                   dict(dh=A, m=4, k=64, f=96, act=1, gu=A, gs=A, gsave=2, x=A, xs=A, xsave=3, w=A, dx=A, dw=A, work=A,
@@ -92,8 +93,8 @@ def test_mxfp4_validation(sfr, gated):
     assert need(0, 64, 64) == 0 and need(4, 64, 48) == 0 and need(4, 40, 64) == 0
     assert need(1, 64, 64) == 0
     if gated:
-        call = caller(lib.mxfp4_gated_linear, "x m k wq ws f act out work bytes",
-                      dict(x=A, m=4, k=64, wq=A, ws=A, f=64, act=0, out=A, work=A, bytes=1 << 40))
+        call = caller(lib.mxfp4_gated_linear, "x m k wq ws f act out",
+                      dict(x=A, m=4, k=64, wq=A, ws=A, f=64, act=0, out=A))
         assert call(act=5) == DTYPE
         bads = (dict(f=0), dict(f=48), dict(f=BIG // 2 + 32))
     else:
@@ -105,13 +106,14 @@ def test_mxfp4_validation(sfr, gated):
         bads = (dict(n=40), dict(n=-16), dict(n=BIG + 16))
     for bad in bads + (dict(m=-1), dict(m=(1 << 30) + 1), dict(k=48), dict(k=0), dict(k=BIG + 32)):
         assert call(**bad) == SHAPE, bad
-    assert call(m=0, x=None, out=None, work=None) == OK
+    assert call(m=0, x=None, out=None) == OK
     for t in ("x", "wq", "ws", "out"):
         assert call(**{t: None}) == NULL and call(**{t: U}) == ALIGN
-    m = 4096
-    if need(m, 128 if gated else 64, 64):
-        assert call(m=m, bytes=need(m, 128 if gated else 64, 64) - 1) == SHAPE
-        assert call(m=m, work=None) == NULL and call(m=m, work=U) == ALIGN
+    if not gated:  # few outputs and a long sum: slices of the sum in the workspace
+        m, k = 100, 1 << 15
+        assert need(m, 64, k) > 0 and need(m, 64, k) % (m * 64 * 4) in range(256)
+        assert call(m=m, k=k, bytes=need(m, 64, k) - 1) == SHAPE
+        assert call(m=m, k=k, work=None) == NULL and call(m=m, k=k, work=U) == ALIGN
 
 
 def test_binding_refuses(sfr):
