@@ -134,7 +134,7 @@ struct StreamArgs {
   void* out;
   int out_fmt;
 };
-bool stream_rows(int64_t m);
+bool stream_rows(int64_t m, int64_t n, int64_t k, bool fp4);  // n: weight rows (2 f when gated)
 hipError_t launch_stream(const StreamArgs& a, hipStream_t stream);
 // The matrix-core form of the 4-bit linear layer (not gated), any m.
 int64_t dense_nt_workspace_bytes(int64_t m, int64_t n, int64_t k);
