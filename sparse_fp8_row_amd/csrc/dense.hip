@@ -6,6 +6,8 @@
 // and the product with a decoded 4-bit weight.  Bound by the matrix cores for
 // many rows (4 m k f operations forward, twice that backward), by reading the
 // weight for few.
+#include <type_traits>
+
 #include "sfr_dense.hpp"
 
 namespace sfr {
@@ -146,64 +148,81 @@ __global__ __launch_bounds__(64 * WN * WM) void dense_tile_kernel(DenseParams p)
 }
 
 // ---------------------------------------------------------------------------
-// Wide kernel: 256 x 256 outputs, eight wavefronts in two groups of four (one
-// wavefront of each group per SIMD), 128 KB of LDS in two stages of BK.
+// Wide kernel: 128 WH x 64 XF outputs (256 x 256, 256 x 192, 384 x 192), eight
+// wavefronts in two groups of four (one wavefront of each group per SIMD), two
+// stages of BK in LDS.
 //
-// Each operand's stage is two half tiles of 128 rows.  A wavefront owns 64
-// rows of each W half (group g: rows 64 g ..) and 32 rows of each X half: 128 x
-// 64 outputs.  One step of k is two phases, each: read operands from LDS and put
-// half tiles of later stages in flight; barrier; 32 matrix instructions;
-// barrier.  The second group runs one barrier behind, so on every SIMD one
-// wavefront reads while the other multiplies.
+// W's stage is WH part tiles of 128 rows, of which a wavefront owns 64 rows each
+// (group g: rows 64 g ..); it owns 16 XF of X's 64 XF rows.  One step of k is WH
+// phases, each: read operands from LDS and put tiles of later stages in flight;
+// barrier; 8 XF matrix instructions; barrier.  The second group runs one
+// barrier behind, so on every SIMD one wavefront reads while the other
+// multiplies.
 //
-//   phase  LDS reads     loads issued            outputs
-//     0    W0, X0, X1    W1 of step t + 1        W0 x (X0, X1)
-//     1    W1            W0, X0, X1 of t + 2     W1 x (X0, X1)
+//   phase  LDS reads   loads issued                    outputs
+//     0    W0, X       last part of W, step t + 1      W0 x X
+//     1    W1          W0 and X of t + 2               W1 x X
+//     2    W2          W1 of t + 2                     W2 x X      (WH = 3)
 // (CODES: W's codes are fetched one step earlier still; "issued" means decoded
-// into LDS, and each half tile's fetch is two loads like its ROWS form.)
-// A half tile is refilled no earlier than the phase after its last read: every
+// into LDS, and each part tile's fetch is two loads like its ROWS form.)
+// A tile is refilled no earlier than the phase after its last read: every
 // wavefront waits for its LDS reads before the barrier that ends its reading
-// part, and the other group is one barrier away.  Eight loads per wavefront
-// (four half tiles) stay in flight when a phase waits for the next one's.
-// Loads past the last step read zeros (they are masked) and keep the counts.
-// (Four phases of 16 instructions were slower: 1693 against the time above
-// the launcher, the barriers and the LDS latency of each phase exceeded its
-// matrix instructions.)
+// part, and the other group is one barrier away.  `pending` loads per
+// wavefront (issued after the ones that the next phase needs) stay in flight
+// when a phase waits.  Loads past the last step read zeros (they are masked)
+// and keep the counts.
+//
+// Measured at m = 8192, k = 4096, f = 14336 (256 x 256): 1.29 PFLOP/s forward,
+// 1.22 dx, 1.24 dW, with the matrix units busy 80% of the cycles at a clock
+// that power holds near 1.5 GHz; without the global loads it would be 1.51
+// PFLOP/s, without the LDS reads 1.31.  Phases of 16 instructions took 1693
+// us forward in place of 1485.
 // ---------------------------------------------------------------------------
-template <int LX, int LW, int EPI>
+template <int LX, int LW, int EPI, int WH, int XF>
 __global__ __launch_bounds__(512, 2) void dense_wide_kernel(DenseParams p) {
   constexpr bool PAIR = EPI == EPI_GATED, FP4 = LW == CODES;
-  constexpr int HALF = 128 * BK * 2, STAGE = 4 * HALF;  // W0, W1, X0, X1
+  // X in LDS: one tile of all its rows, or (COLS) tiles of 128
+  constexpr int XT = LX == COLS ? XF / 2 : 1, XR = 64 * XF / XT, XFT = XF / XT;
+  constexpr int WPART = 128 * BK * 2, XPART = XR * BK * 2, STAGE = WH * WPART + XT * XPART;
+  static_assert(XR % 64 == 0 && (LX != COLS || XR == 128), "tile layouts");
+  constexpr int LOADS_X = XF, LOADS_W = 2;  // per wavefront: X's stage, a part of W
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
 
   int64_t tm, tn;
   if (!tile_of(blockIdx.x, p.tiles_m, p.tiles_n, p.group, tm, tn)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wave >> 2, wm = wave & 3;
-  constexpr int HN = PAIR ? 64 : 128;  // W rows (of one of the pair) per half tile
-  const int64_t m0 = tm * 256, n0 = tn * (2 * HN);
+  constexpr int HN = PAIR ? 64 : 128;  // W rows (of one of the pair) per part
+  const int64_t m0 = tm * (64 * XF), n0 = tn * (WH * HN);
   const int64_t k0 = blockIdx.y * p.k_per_split;
   const int kdim = (int)min(p.k - k0, p.k_per_split), KT = (kdim + BK - 1) / BK;
 
   WLoader<LW, 128, 8, PAIR> lw0(p, n0, k0, wave, lane);
   WLoader<LW, 128, 8, PAIR> lw1(p, n0 + HN, k0, wave, lane);
-  Loader<LX, 128, 8, false> lx0(p.x, p.ldx, m0, p.rows_m, k0, wave, lane);
-  Loader<LX, 128, 8, false> lx1(p.x, p.ldx, m0 + 128, p.rows_m, k0, wave, lane);
+  WLoader<LW, 128, 8, PAIR> lw2(p, n0 + 2 * HN, k0, wave, lane);  // WH = 3
+  Loader<LX, XR, 8, false> lx0(p.x, p.ldx, m0, p.rows_m, k0, wave, lane);
+  Loader<LX, XR, 8, false> lx1(p.x, p.ldx, m0 + XR, p.rows_m, k0, wave, lane);  // XT = 2
   const Reader<FP4 ? ROWS : LW, 128, 4> rw(wn * 4, lane);
-  const Reader<LX, 128, 2> rx(wm * 2, lane);
+  const Reader<LX, XR, XFT> rx(wm * XFT, lane);
 
-  v4f acc[2][2][4][2];
+  v4f acc[WH][XT][4][XFT];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) acc[i >> 4][(i >> 3) & 1][(i >> 1) & 3][i & 1] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int h = 0; h < WH; ++h)
+#pragma unroll
+    for (int q = 0; q < XT; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < XFT; ++j) acc[h][q][i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
   auto load_x = [&](int t) __attribute__((always_inline)) {
-    uint8_t* s = smem + (t & 1) * STAGE;
-    lx0.stage(s + 2 * HALF, kdim - t * BK);
-    lx1.stage(s + 3 * HALF, kdim - t * BK);
+    uint8_t* s = smem + (t & 1) * STAGE + WH * WPART;
+    lx0.stage(s, kdim - t * BK);
+    if constexpr (XT == 2) lx1.stage(s + XPART, kdim - t * BK);
   };
-  // half tile `part` of W; CODES: the codes fetched one step ago go to LDS and the next step's are fetched
+  // part `part` of W; CODES: the codes fetched one step ago go to LDS and the next step's are fetched
   auto load_w = [&](auto& l, int part, int t) __attribute__((always_inline)) {
-    uint8_t* tile = smem + (t & 1) * STAGE + part * HALF;
+    uint8_t* tile = smem + (t & 1) * STAGE + part * WPART;
     if constexpr (FP4) {
       l.codes.put(tile);
       l.codes.fetch(kdim - (t + 1) * BK);
@@ -211,23 +230,28 @@ __global__ __launch_bounds__(512, 2) void dense_wide_kernel(DenseParams p) {
       l.rows.stage(tile, kdim - t * BK);
     }
   };
+  // the loads in the order of the phases
   if constexpr (FP4) {
     lw0.codes.fetch(kdim);
     lw1.codes.fetch(kdim);
+    if constexpr (WH == 3) lw2.codes.fetch(kdim);
   }
   load_w(lw0, 0, 0);
   load_x(0);
   load_w(lw1, 1, 0);
+  if constexpr (WH == 3) load_w(lw2, 2, 0);
   load_w(lw0, 0, 1);
   load_x(1);
-  wait_vm<8>();
+  if constexpr (WH == 3) load_w(lw1, 1, 1);
+  // W0 and X of step 0 have landed
+  wait_vm<(WH == 3 ? 4 : 2) * LOADS_W + LOADS_X>();
   wait_lds();
   wg_barrier();
   if (wn == 1) wg_barrier();
 
-  v8bf w[2][4], x0[2][2], x1[2][2];
-  auto multiply = [&](v4f(&c0)[4][2], v4f(&c1)[4][2]) __attribute__((always_inline)) {
-    wait_vm<8>();
+  v8bf w[2][4], x[XT][2][XFT];
+  auto multiply = [&](auto pending, v4f(&c)[XT][4][XFT]) __attribute__((always_inline)) {
+    wait_vm<pending.value>();
     wait_lds();
     wg_barrier();
     __builtin_amdgcn_sched_barrier(0);
@@ -235,45 +259,60 @@ __global__ __launch_bounds__(512, 2) void dense_wide_kernel(DenseParams p) {
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) c0[i][j] = mfma16(w[kk][i], x0[kk][j], c0[i][j]);
+        for (int q = 0; q < XT; ++q)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) c1[i][j] = mfma16(w[kk][i], x1[kk][j], c1[i][j]);
-      }
+          for (int j = 0; j < XFT; ++j) c[q][i][j] = mfma16(w[kk][i], x[q][kk][j], c[q][i][j]);
     __builtin_amdgcn_s_setprio(0);
     __builtin_amdgcn_sched_barrier(0);
     wg_barrier();
   };
+  // loads issued after the ones that the phase after 0, after 1 (WH = 3) and after the last needs
+  constexpr std::integral_constant<int, (WH == 3 ? 4 : 2) * LOADS_W + LOADS_X> after0{}, after_last{};
+  constexpr std::integral_constant<int, 4 * LOADS_W + 2 * LOADS_X> after1{};
   for (int t = 0; t < KT; ++t) {
     const uint8_t* s = smem + (t & 1) * STAGE;
-    rx.read2(x0, x1, s + 2 * HALF, HALF);
+    if constexpr (XT == 2) rx.read2(x[0], x[1], s + WH * WPART, XPART);
+    else rx.read(x[0], s + WH * WPART);
     rw.read(w, s);
-    load_w(lw1, 1, t + 1);
-    multiply(acc[0][0], acc[0][1]);
+    if constexpr (WH == 3) load_w(lw2, 2, t + 1);
+    else load_w(lw1, 1, t + 1);
+    multiply(after0, acc[0]);
 
-    rw.read(w, s + HALF);
+    rw.read(w, s + WPART);
     load_w(lw0, 0, t + 2);
     load_x(t + 2);
-    multiply(acc[1][0], acc[1][1]);
+    if constexpr (WH == 3) {
+      multiply(after1, acc[1]);
+      rw.read(w, s + 2 * WPART);
+      load_w(lw1, 1, t + 2);
+    }
+    multiply(after_last, acc[WH - 1]);
   }
   if (wn == 0) wg_barrier();
   wait_vm<0>();
   wg_barrier();  // every load has landed: the stages become the epilogue's
 
-  uint8_t* region = smem + wave * 16384;
+  uint8_t* region = smem + wave * (XFT * 2048);
 #pragma unroll
-  for (int hw = 0; hw < 2; ++hw)
+  for (int h = 0; h < WH; ++h)
 #pragma unroll
-    for (int hx = 0; hx < 2; ++hx) {
-      const int64_t mb = m0 + hx * 128 + wm * 32;
-      v4f(&a)[4][2] = acc[hw][hx];
+    for (int q = 0; q < XT; ++q) {
+      const int64_t mb = m0 + q * XR + wm * (XFT * 16);
+      v4f(&a)[4][XFT] = acc[h][q];
       if constexpr (EPI == EPI_GATED) {
-        const v4f g[2][2] = {{a[0][0], a[0][1]}, {a[2][0], a[2][1]}};
-        const v4f u[2][2] = {{a[1][0], a[1][1]}, {a[3][0], a[3][1]}};
-        gated_epilogue<2>(g, u, p.gated, mb, n0 + hw * 64 + wn * 32, lane, region);
+        v4f g[2][XFT], u[2][XFT];
+#pragma unroll
+        for (int j = 0; j < XFT; ++j) {
+          g[0][j] = a[0][j];
+          u[0][j] = a[1][j];
+          g[1][j] = a[2][j];
+          u[1][j] = a[3][j];
+        }
+        gated_epilogue<XFT>(g, u, p.gated, mb, n0 + h * 64 + wn * 32, lane, region);
       } else {
-        plain_epilogue<2>(a, plain_of(p), mb, n0 + hw * 128 + wn * 64, lane, region);
+        plain_epilogue<XFT>(a, plain_of(p), mb, n0 + h * 128 + wn * 64, lane, region);
       }
     }
 }
@@ -316,15 +355,16 @@ hipError_t run_tile(DenseParams p, int slices, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int LX, int LW, int EPI>
+template <int LX, int LW, int EPI, int WH, int XF>
 hipError_t run_wide(DenseParams p, int slices, hipStream_t stream) {
-  constexpr int bytes = 2 * 4 * 128 * BK * 2;
-  auto* kernel = dense_wide_kernel<LX, LW, EPI>;
+  constexpr int bytes = 2 * (WH * 128 + XF * 64) * BK * 2;
+  static_assert(bytes <= 160 * 1024, "LDS of a CU");
+  auto* kernel = dense_wide_kernel<LX, LW, EPI, WH, XF>;
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != hipSuccess) return e;
-  constexpr int cover = EPI == EPI_GATED ? 128 : 256;
-  p.tiles_m = (p.rows_m + 255) / 256;
+  constexpr int cover = EPI == EPI_GATED ? 64 * WH : 128 * WH;
+  p.tiles_m = (p.rows_m + 64 * XF - 1) / (64 * XF);
   p.tiles_n = (p.rows_n + cover - 1) / cover;
   p.group = 8;
   const int64_t grid = (p.tiles_m * p.tiles_n + 7) / 8 * 8;
@@ -334,38 +374,59 @@ hipError_t run_wide(DenseParams p, int slices, hipStream_t stream) {
 
 // ---------------------------------------------------------------------------
 // Choice of kernel and of the number of slices of the sum: the smallest
-// modelled time.  A configuration covers BN x BM outputs per workgroup, `slots`
-// workgroups at once on 256 CUs; a round takes `full` per stage of k when
-// every CU holds as many workgroups as fit, `one` when it holds at most one
-// (us per stage, measured: see the table of the launchers' comment).  Slices
-// (plain outputs only) add a pass over their binary32 partial sums.
+// modelled time.  A configuration covers bn x bm outputs per workgroup, per_cu
+// workgroups fit on a CU.  us per stage of k of one round of tiles, measured
+// (forward, k = 4096, 64 stages): `one` with few tiles, `all` with one on each of
+// 256 CUs, `full` with every CU full; `lasting` in a run of several rounds,
+// where power lowers the clock of the wide kernels; `cols` times as long with a
+// COLS W operand (dx).  Examples (measured, us):
+//   m = 300, f = 14336: 256x192 71, 256x256 86, 128x128 97, 128x64 108, 384x192 98
+//   m = 517, f = 14336: 384x192 107, 256x192 135, 128x128 158, 256x256 161
+//   m = 128, f = 14336: 128x64 48, 128x128 49, 256x256 76
+//   m = 8192, f = 14336: 256x256 1485, 256x192 1618, 384x192 1662, 128x128 1868
+//   dx m = 1000, k = 2048, f = 5632: 128x128 in 1, 2, 4, 8 slices 118, 73, 55, 67,
+//     256x256 211, 122, 76, 59;  m = 4096, k = f = 2048: 128x128 63, 256x192 85
+// Slices (plain outputs only) add a pass over their binary32 partial sums.
 // ---------------------------------------------------------------------------
-enum { CFG_WIDE = 0, CFG_128 = 1, CFG_128x64 = 2, CFG_64 = 3, CFG_COUNT = 4 };
+enum { CFG_WIDE = 0, CFG_WIDE_192, CFG_WIDE_384, CFG_128, CFG_128x64, CFG_64, CFG_COUNT };
 struct Config {
   int bn, bm, per_cu;
-  double full, one;
+  double one, all, full, lasting, fixed, cols;
 };
 constexpr Config kConfigs[CFG_COUNT] = {
-    {256, 256, 1, 1.34, 1.34}, {128, 128, 2, 0.95, 0.58}, {128, 64, 2, 0.64, 0.40}, {64, 64, 3, 0.55, 0.30}};
+    {256, 256, 1, 0.95, 1.37, 1.37, 1.66, 5.6, 1.18}, {256, 192, 1, 0.80, 1.06, 1.06, 1.34, 5.0, 1.25},
+    {384, 192, 1, 1.16, 1.60, 1.60, 2.06, 7.0, 1.18}, {128, 128, 2, 0.58, 0.76, 1.05, 1.05, 3.7, 1.0},
+    {128, 64, 2, 0.45, 0.51, 0.67, 0.67, 3.8, 1.0},  {64, 64, 3, 0.36, 0.40, 0.59, 0.59, 3.0, 1.0}};
 struct Choice {
   int config, slices;
   int64_t k_per_split;
 };
 
-// n: columns of the output's tiles (2 f when gated).
-Choice choose(int64_t m, int64_t n, int64_t k, bool can_slice) {
+double model_us(const Config& g, int64_t tiles, int64_t stages, bool cols_w) {
+  const int64_t slots = 256 * g.per_cu, rounds = tiles / slots, rest = tiles % slots;
+  const double tail = rest == 0     ? 0
+                      : rest <= 256 ? g.one + (g.all - g.one) * rest / 256
+                                    : g.all + (g.full - g.all) * (rest - 256) / (slots - 256);
+  const double fixed = g.fixed * (rounds + (rest != 0));
+  const double us = (cols_w ? g.cols : 1.0) * stages;
+  const double t = (rounds * g.full + tail) * us + fixed;
+  return t < 250 ? t : (rounds * g.lasting + tail) * us + fixed;
+}
+
+// n: columns of the output's tiles (2 f when gated).  lx, lw: the operands'
+// layouts (the kernels of 192 rows need X by rows).  can_slice: a plain output.
+Choice choose(int64_t m, int64_t n, int64_t k, int lx, int lw, bool can_slice) {
   const int64_t stages = (k + BK - 1) / BK;
   Choice best{CFG_64, 1, k};
   double least = 1e300;
   for (int c = 0; c < CFG_COUNT; ++c) {
     const Config& g = kConfigs[c];
+    if (g.bm == 192 && lx != ROWS) continue;
     const int64_t tiles = ((m + g.bm - 1) / g.bm) * ((n + g.bn - 1) / g.bn);
     for (int s = 1; s <= (can_slice ? 16 : 1); ++s) {
       const int64_t per = (stages + s - 1) / s;
       if (s > 1 && (per < 8 || (stages + per - 1) / per != s)) continue;
-      const int64_t total = tiles * s, slots = 256 * g.per_cu, rest = total % slots;
-      double t = (total / slots) * g.full + (rest == 0 ? 0 : rest <= 256 ? g.one : g.full);
-      t = t * per + 3.0 + (s > 1 ? 3.0 + 8.0 * s * m * n / 3.5e6 : 0.0);
+      const double t = model_us(g, tiles * s, per, lw == COLS) + (s > 1 ? 3.0 + 8.0 * s * m * n / 6e6 : 0.0);
       if (t < least) {
         least = t;
         best = Choice{c, s, s == 1 ? k : per * BK};
@@ -379,26 +440,35 @@ template <int LX, int LW, int EPI>
 hipError_t run_dense(DenseParams p, const Choice& c, void* workspace, hipStream_t stream) {
   p.k_per_split = c.k_per_split;
   p.partial = c.slices > 1 ? static_cast<float*>(workspace) : nullptr;
-  hipError_t e = c.config == CFG_WIDE     ? run_wide<LX, LW, EPI>(p, c.slices, stream)
-                 : c.config == CFG_128    ? run_tile<LX, LW, EPI, 128, 128, 2, 2, 2>(p, c.slices, stream)
-                 : c.config == CFG_128x64 ? run_tile<LX, LW, EPI, 128, 64, 2, 2, 3>(p, c.slices, stream)
-                                          : run_tile<LX, LW, EPI, 64, 64, 1, 4, 3>(p, c.slices, stream);
+  hipError_t e = hipErrorInvalidValue;
+  switch (c.config) {
+    case CFG_WIDE: e = run_wide<LX, LW, EPI, 2, 4>(p, c.slices, stream); break;
+    case CFG_WIDE_192:
+      if constexpr (LX == ROWS) e = run_wide<LX, LW, EPI, 2, 3>(p, c.slices, stream);
+      break;
+    case CFG_WIDE_384:
+      if constexpr (LX == ROWS) e = run_wide<LX, LW, EPI, 3, 3>(p, c.slices, stream);
+      break;
+    case CFG_128: e = run_tile<LX, LW, EPI, 128, 128, 2, 2, 2>(p, c.slices, stream); break;
+    case CFG_128x64: e = run_tile<LX, LW, EPI, 128, 64, 2, 2, 3>(p, c.slices, stream); break;
+    default: e = run_tile<LX, LW, EPI, 64, 64, 1, 4, 3>(p, c.slices, stream);
+  }
   if (e != hipSuccess || c.slices == 1) return e;
   const int64_t quads = p.plain.m * p.plain.n / 4;
   dense_reduce_kernel<<<dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream>>>(p.partial, c.slices, p.plain);
   return hipGetLastError();
 }
 
-int64_t slice_bytes(int64_t m, int64_t n, int64_t k) {
-  const Choice c = choose(m, n, k, true);
+int64_t slice_bytes(int64_t m, int64_t n, int64_t k, int lw) {
+  const Choice c = choose(m, n, k, ROWS, lw, true);
   return c.slices > 1 ? c.slices * m * n * 4 : 0;
 }
 
 }  // namespace
 
 // Workspace: the slices' partial sums.
-int64_t dense_nt_workspace_bytes(int64_t m, int64_t n, int64_t k) { return slice_bytes(m, n, k); }
-int64_t dense_dx_workspace_bytes(int64_t m, int64_t k, int64_t f2) { return slice_bytes(m, k, f2); }
+int64_t dense_nt_workspace_bytes(int64_t m, int64_t n, int64_t k) { return slice_bytes(m, n, k, CODES); }
+int64_t dense_dx_workspace_bytes(int64_t m, int64_t k, int64_t f2) { return slice_bytes(m, k, f2, COLS); }
 
 hipError_t launch_gated_dense(const GatedArgs& a, hipStream_t stream) {
   DenseParams p{};
@@ -410,7 +480,7 @@ hipError_t launch_gated_dense(const GatedArgs& a, hipStream_t stream) {
   p.rows_n = a.f;
   p.k = a.k;
   p.gated = GatedOut{a.h, a.gu, a.gu_scale, a.m, a.f, a.act, a.gu_fmt};
-  const Choice c = choose(a.m, 2 * a.f, a.k, false);
+  const Choice c = choose(a.m, 2 * a.f, a.k, ROWS, ROWS, false);
   return a.w_scale ? run_dense<ROWS, CODES, EPI_GATED>(p, c, nullptr, stream)
                    : run_dense<ROWS, ROWS, EPI_GATED>(p, c, nullptr, stream);
 }
@@ -425,7 +495,7 @@ hipError_t launch_mxfp4_dense(const StreamArgs& a, void* workspace, hipStream_t 
   p.rows_n = a.rows;
   p.k = a.k;
   p.plain = PlainOut{a.out, a.bias, a.m, a.rows, a.out_fmt};
-  return run_dense<ROWS, CODES, EPI_PLAIN>(p, choose(a.m, a.rows, a.k, true), workspace, stream);
+  return run_dense<ROWS, CODES, EPI_PLAIN>(p, choose(a.m, a.rows, a.k, ROWS, CODES, true), workspace, stream);
 }
 
 hipError_t launch_dense_dx(const uint16_t* dgu, const uint16_t* w, int64_t m, int64_t k, int64_t f2, uint16_t* dx,
@@ -439,7 +509,7 @@ hipError_t launch_dense_dx(const uint16_t* dgu, const uint16_t* w, int64_t m, in
   p.rows_n = k;
   p.k = f2;
   p.plain = PlainOut{dx, nullptr, m, k, OUT_BF16};
-  return run_dense<ROWS, COLS, EPI_PLAIN>(p, choose(m, k, f2, true), workspace, stream);
+  return run_dense<ROWS, COLS, EPI_PLAIN>(p, choose(m, k, f2, ROWS, COLS, true), workspace, stream);
 }
 
 hipError_t launch_dense_dw(const uint16_t* dgu, const uint16_t* x, int64_t m, int64_t k, int64_t f2, uint16_t* dw,
@@ -453,7 +523,7 @@ hipError_t launch_dense_dw(const uint16_t* dgu, const uint16_t* x, int64_t m, in
   p.rows_n = k;
   p.k = m;
   p.plain = PlainOut{dw, nullptr, f2, k, OUT_BF16};
-  return run_dense<COLS, COLS, EPI_PLAIN>(p, choose(f2, k, m, false), nullptr, stream);
+  return run_dense<COLS, COLS, EPI_PLAIN>(p, choose(f2, k, m, COLS, COLS, false), nullptr, stream);
 }
 
 }  // namespace sfr

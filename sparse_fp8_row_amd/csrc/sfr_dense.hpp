@@ -101,6 +101,7 @@ struct Loader {
         first[q] = chunk * 8;
       }
     } else {
+      static_assert(L != COLS || 512 % BR == 0, "whole k per load");
       constexpr int RPL = 512 / BR, CPR = 64 / RPL;  // k per load, 16-byte chunks per k
       base = reinterpret_cast<const uint8_t*>(p + k0 * ld + r0);
       step = BK * 2 * ld;

@@ -110,7 +110,7 @@ def test_mxfp4_validation(sfr, gated):
     for t in ("x", "wq", "ws", "out"):
         assert call(**{t: None}) == NULL and call(**{t: U}) == ALIGN
     if not gated:  # few outputs and a long sum: slices of the sum in the workspace
-        m, k = 100, 1 << 15
+        m, k = 200, 1 << 15
         assert need(m, 64, k) > 0 and need(m, 64, k) % (m * 64 * 4) in range(256)
         assert call(m=m, k=k, bytes=need(m, 64, k) - 1) == SHAPE
         assert call(m=m, k=k, work=None) == NULL and call(m=m, k=k, work=U) == ALIGN
