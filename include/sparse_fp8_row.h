@@ -417,8 +417,8 @@ sfr_status bsr_linear_bf16(const uint16_t* x, int64_t m, int64_t k, const int32_
  * binary32 arithmetic does (an MX block that holds one decodes to NaN).
  *
  * Sizes: 0 <= m <= SFR_MAX_DIM; 0 < k, 2 f, n <= SFR_MAX_BLOCK_DIM; k % 32 == 0,
- * f % 32 == 0, n % 16 == 0; a call whose output takes more than 2^24 tiles of
- * 128 x 128 (64 x 64 up to 64 rows) is SFR_ERR_SHAPE.  Results do not depend on anything
+ * f % 32 == 0, n % 16 == 0; a call one of whose products has more than 2^21 tiles
+ * of 128 x 128 outputs (64 x 64 up to 64 rows) is SFR_ERR_SHAPE.  Results do not depend on anything
  * but the arguments: the order of every sum is fixed, no atomics.
  * ---------------------------------------------------------------------------
  */

@@ -518,17 +518,36 @@ _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device
 def _placed(fn):
     """Runs fn with its first argument's device current and, with an explicit
     `stream`, with that stream current, so that what the call allocates belongs
-    to the stream its kernels run on.  Nothing is switched when both are so
-    already."""
+    to the stream its kernels run on, and the memory of its arguments is not
+    used again before that stream is done with them (the stream has to be
+    ordered after what produced them, as for any work).  Nothing is switched
+    when both are so already."""
     @functools.wraps(fn)
     def call(first, *args, stream=None, **kw):
         t = first.codes if isinstance(first, MxTensor) else first
-        device = t.get_device()
+        device = t.get_device() if isinstance(t, torch.Tensor) else -1
         if device < 0 or (stream is None and device == _current_device()):
             return fn(first, *args, **kw)
         with torch.cuda.device(device), torch.cuda.stream(stream):
-            return fn(first, *args, **kw)
+            out = fn(first, *args, **kw)
+            if stream is not None:
+                for a in (first, *args, *kw.values()):
+                    _keep(a, stream)
+            return out
     return call
+
+
+def _keep(a, stream):
+    """The caching allocator keeps a's memory until `stream` has passed this point."""
+    if isinstance(a, torch.Tensor):
+        if a.is_cuda:
+            a.record_stream(stream)
+    elif isinstance(a, MxTensor):
+        _keep(a.codes, stream)
+        _keep(a.scale, stream)
+    elif isinstance(a, GatedCheckpoint):
+        _keep(a.x, stream)
+        _keep(a.gu, stream)
 
 
 def _gpu(t: torch.Tensor, name: str, device: int) -> int:
@@ -598,7 +617,7 @@ def quantize_mx(x: torch.Tensor, dtype=torch.float8_e4m3fn) -> MxTensor:
 @_placed
 def dequantize_mx(t: MxTensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """MxTensor -> the bf16 values it stands for (exact)."""
-    device = t.codes.get_device()
+    device = t.codes.get_device() if isinstance(t, MxTensor) else -1
     rows, cols, pq, ps = _mx_parts(t, "t", device)
     out = _output(out, rows, cols, torch.bfloat16, t.codes)
     _check(load().dequantize_mx(pq, ps, rows, cols, _MX[t.codes.dtype], out.data_ptr(), _raw_stream(device)),

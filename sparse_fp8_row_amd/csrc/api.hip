@@ -21,7 +21,7 @@ bool block_dim(int64_t d, int64_t multiple) { return d > 0 && d <= SFR_MAX_BLOCK
 // An output of the dense products: its tiles make one grid.
 bool dense_ok(int64_t rows, int64_t cols) {
   const int64_t t = rows > 64 ? 128 : 64;
-  return ((rows + t - 1) / t) * ((cols + t - 1) / t) <= ((int64_t)1 << 24);
+  return ((rows + t - 1) / t) * ((cols + t - 1) / t) <= ((int64_t)1 << 21);
 }
 bool gated_shape(int64_t m, int64_t k, int64_t f) {
   return m >= 0 && m <= SFR_MAX_DIM && block_dim(k, 32) && block_dim(2 * f, 64) && dense_ok(m, 2 * f) &&

@@ -22,8 +22,7 @@ struct DenseParams {
   int64_t rows_m, rows_n;  // rows of X; rows of W (GATED: of one half)
   int64_t k;
   int64_t k_per_split;  // multiple of BK; k of one slice of the sum
-  int64_t tiles_m, tiles_n;
-  int group;
+  int tiles_m, tiles_n, group;
   float* partial;  // with several slices: binary32 [slices, m, n], summed by dense_reduce_kernel
   PlainOut plain;
   GatedOut gated;
@@ -336,6 +335,17 @@ __global__ __launch_bounds__(256) void dense_reduce_kernel(const float* __restri
   else reinterpret_cast<uint2*>(o.out)[at] = make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
 }
 
+// Tiles of bm x `cover` rows; the workgroups of the grid, or -1 where the tiles
+// pass what the kernels index (the entry points refuse such sizes).
+int64_t set_tiles(DenseParams& p, int64_t bm, int64_t cover) {
+  const int64_t tm = (p.rows_m + bm - 1) / bm, tn = (p.rows_n + cover - 1) / cover;
+  if (tm * tn > ((int64_t)1 << 23) - 8) return -1;
+  p.tiles_m = (int)tm;
+  p.tiles_n = (int)tn;
+  p.group = 8;
+  return (tm * tn + 7) / 8 * 8;
+}
+
 template <int LX, int LW, int EPI, int BN, int BM, int WN, int WM, int S>
 hipError_t run_tile(DenseParams p, int slices, hipStream_t stream) {
   constexpr int bytes = S * (BN + BM) * BK * 2;
@@ -346,11 +356,8 @@ hipError_t run_tile(DenseParams p, int slices, hipStream_t stream) {
     if (e != hipSuccess) return e;
   }
   constexpr int cover = EPI == EPI_GATED ? BN / 2 : BN;
-  p.tiles_m = (p.rows_m + BM - 1) / BM;
-  p.tiles_n = (p.rows_n + cover - 1) / cover;
-  p.group = 8;
-  const int64_t grid = (p.tiles_m * p.tiles_n + 7) / 8 * 8;
-  if (grid > (1 << 24)) return hipErrorInvalidValue;
+  const int64_t grid = set_tiles(p, BM, cover);
+  if (grid < 0) return hipErrorInvalidValue;
   kernel<<<dim3((unsigned)grid, (unsigned)slices), dim3(64 * WN * WM), bytes, stream>>>(p);
   return hipGetLastError();
 }
@@ -364,10 +371,8 @@ hipError_t run_wide(DenseParams p, int slices, hipStream_t stream) {
                                            hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != hipSuccess) return e;
   constexpr int cover = EPI == EPI_GATED ? 64 * WH : 128 * WH;
-  p.tiles_m = (p.rows_m + 64 * XF - 1) / (64 * XF);
-  p.tiles_n = (p.rows_n + cover - 1) / cover;
-  p.group = 8;
-  const int64_t grid = (p.tiles_m * p.tiles_n + 7) / 8 * 8;
+  const int64_t grid = set_tiles(p, 64 * XF, cover);
+  if (grid < 0) return hipErrorInvalidValue;
   kernel<<<dim3((unsigned)grid, (unsigned)slices), dim3(512), bytes, stream>>>(p);
   return hipGetLastError();
 }
@@ -423,7 +428,7 @@ Choice choose(int64_t m, int64_t n, int64_t k, int lx, int lw, bool can_slice) {
     const Config& g = kConfigs[c];
     if (g.bm == 192 && lx != ROWS) continue;
     const int64_t tiles = ((m + g.bm - 1) / g.bm) * ((n + g.bn - 1) / g.bn);
-    for (int s = 1; s <= (can_slice ? 16 : 1); ++s) {
+    for (int s = 1; s <= (can_slice && m * n <= ((int64_t)1 << 30) ? 16 : 1); ++s) {
       const int64_t per = (stages + s - 1) / s;
       if (s > 1 && (per < 8 || (stages + per - 1) / per != s)) continue;
       const double t = model_us(g, tiles * s, per, lw == COLS) + (s > 1 ? 3.0 + 8.0 * s * m * n / 6e6 : 0.0);

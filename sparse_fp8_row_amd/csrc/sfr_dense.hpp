@@ -511,14 +511,14 @@ __device__ __forceinline__ void plain_epilogue(v4f (&acc)[4][FM], const PlainOut
 
 // Tile of workgroup `id` of 8 * ceil(T / 8): XCD id % 8 (each has its own L2)
 // owns a contiguous run of the tiles, taken in groups of `group` n tiles.
-// False past the last tile.
-__device__ __forceinline__ bool tile_of(int64_t id, int64_t tiles_m, int64_t tiles_n, int group, int64_t& tm,
+// False past the last tile.  (32-bit: the launchers bound T by 2^23.)
+__device__ __forceinline__ bool tile_of(uint32_t id, uint32_t tiles_m, uint32_t tiles_n, uint32_t group, int64_t& tm,
                                         int64_t& tn) {
-  const int64_t T = tiles_m * tiles_n, per = (T + 7) / 8;
-  const int64_t lid = (id % 8) * per + id / 8;
+  const uint32_t T = tiles_m * tiles_n, per = (T + 7) / 8;
+  const uint32_t lid = (id % 8) * per + id / 8;
   if (id / 8 >= per || lid >= T) return false;
-  const int64_t g = lid / (group * tiles_m), first = g * group;
-  const int64_t size = min(tiles_n - first, (int64_t)group), within = lid - first * tiles_m;
+  const uint32_t g = lid / (group * tiles_m), first = g * group;
+  const uint32_t size = min(tiles_n - first, group), within = lid - first * tiles_m;
   tn = first + within % size;
   tm = within / size;
   return true;
