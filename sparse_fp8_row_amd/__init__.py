@@ -528,6 +528,8 @@ def _placed(fn):
         device = t.get_device() if isinstance(t, torch.Tensor) else -1
         if device < 0 or (stream is None and device == _current_device()):
             return fn(first, *args, **kw)
+        if stream is not None and stream.device_index != device:
+            raise ValueError(f"stream belongs to GPU {stream.device_index}, the arguments to GPU {device}")
         with torch.cuda.device(device), torch.cuda.stream(stream):
             out = fn(first, *args, **kw)
             if stream is not None:
@@ -588,11 +590,22 @@ def _act_enum(name: str) -> int:
     return SFR_ACT[name]
 
 
-def _output(out, rows: int, cols: int, dtype, like: torch.Tensor):
+def _span(t: torch.Tensor):
+    return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+
+
+def _output(out, rows: int, cols: int, dtype, *inputs):
+    """out, checked (also against overlapping an input), or a new tensor on the inputs' device."""
     if out is None:
-        return like.new_empty((rows, cols), dtype=dtype)
-    if out.shape != (rows, cols) or out.dtype is not dtype or not out.is_contiguous() or out.device != like.device:
+        return inputs[0].new_empty((rows, cols), dtype=dtype)
+    if out.shape != (rows, cols) or out.dtype is not dtype or not out.is_contiguous() or \
+            out.device != inputs[0].device:
         raise ValueError("out has the wrong shape, dtype or device")
+    start, end = _span(out)
+    for t in inputs:
+        a, b = _span(t)
+        if a < end and start < b:
+            raise ValueError("out overlaps an input")
     return out
 
 
@@ -619,7 +632,7 @@ def dequantize_mx(t: MxTensor, out: Optional[torch.Tensor] = None) -> torch.Tens
     """MxTensor -> the bf16 values it stands for (exact)."""
     device = t.codes.get_device() if isinstance(t, MxTensor) else -1
     rows, cols, pq, ps = _mx_parts(t, "t", device)
-    out = _output(out, rows, cols, torch.bfloat16, t.codes)
+    out = _output(out, rows, cols, torch.bfloat16, t.codes, t.scale)
     _check(load().dequantize_mx(pq, ps, rows, cols, _MX[t.codes.dtype], out.data_ptr(), _raw_stream(device)),
            "dequantize_mx")
     return out
@@ -641,7 +654,7 @@ def gated_linear(x: torch.Tensor, w: torch.Tensor, activation: str = "silu",
     """h [m, f] = act(x @ w[:f].T) * (x @ w[f:].T) for bf16 x [m, k], w [2 f, k]."""
     device, px, pw, m, k, f = _gated_operands(x, w)
     act = _act_enum(activation)
-    out = _output(out, m, f, torch.bfloat16, x)
+    out = _output(out, m, f, torch.bfloat16, x, w)
     _check(load().gated_linear_bf16(px, m, k, pw, f, act, out.data_ptr(), 0, None, None, _raw_stream(device)),
            "gated_linear")
     return out
@@ -732,7 +745,7 @@ def mxfp4_linear(x: torch.Tensor, w: MxTensor, bias: Optional[torch.Tensor] = No
             raise ValueError("bias must be bfloat16 [n]")
     if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise ValueError("out_dtype must be bfloat16 or float32")
-    out = _output(out, m, n, out_dtype, x)
+    out = _output(out, m, n, out_dtype, x, w.codes, w.scale)
     nbytes = _mxfp4_workspace_bytes(m, n, k)
     work = x.new_empty((nbytes,), dtype=torch.uint8) if nbytes else None
     _check(load().mxfp4_linear(px, m, k, pq, ps, n, pb, out.data_ptr(),
@@ -749,7 +762,7 @@ def mxfp4_gated_linear(x: torch.Tensor, w: MxTensor, activation: str = "silu",
     act = _act_enum(activation)
     if n % 2 != 0:
         raise ValueError("w must be [2 f, k]")
-    out = _output(out, m, n // 2, torch.bfloat16, x)
+    out = _output(out, m, n // 2, torch.bfloat16, x, w.codes, w.scale)
     _check(load().mxfp4_gated_linear(px, m, k, pq, ps, n // 2, act, out.data_ptr(), _raw_stream(device)),
            "mxfp4_gated_linear")
     return out

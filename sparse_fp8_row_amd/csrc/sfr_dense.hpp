@@ -32,9 +32,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buf_rsrc(const void* base, int
 
 // Lane l's 16 bytes at `voff` land at lds + 16 l.  The range check covers the
 // whole offset (it is all in the vector offset): a lane past the range writes zeros.
+// NT: non-temporal (data read once).
+template <bool NT = false>
 __device__ __forceinline__ void buf_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* lds, int voff) {
   const uint32_t a = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void_t)lds);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t)(uintptr_t)a, 16, voff, 0, 0, 0);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t)(uintptr_t)a, 16, voff, 0, 0, NT ? 2 : 0);
 }
 constexpr int kPastRange = 0x7FFFFFF0;  // an offset past every descriptor's range
 

@@ -47,7 +47,7 @@ struct Stream {
   static_assert((D - 1) * LOADS < 64, "wait counts");
 };
 
-template <bool FP4, bool GATED, int RT, int R, int NW, int D>
+template <bool FP4, bool GATED, int RT, int R, int NW, int D, bool NT>
 __global__ __launch_bounds__(64 * NW) void stream_kernel(StreamArgs p) {
   using S = Stream<FP4, RT, R, NW, D>;
   static_assert(!GATED || RT % 2 == 0, "row tiles come in pairs");
@@ -80,7 +80,7 @@ __global__ __launch_bounds__(64 * NW) void stream_kernel(StreamArgs p) {
 #pragma unroll
       for (int j = 0; j < S::WL; ++j) {
         const int row = j * WPL + lane / WC, c = (lane % WC) ^ (row & 7);
-        buf_to_lds(rw[t], b + t * S::TILE + j * 1024,
+        buf_to_lds<NT>(rw[t], b + t * S::TILE + j * 1024,
                    c * (FP4 ? 32 : 8) < left ? row * wrow + u * S::WROW + c * 16 : kPastRange);
       }
 #pragma unroll
@@ -177,11 +177,11 @@ __global__ __launch_bounds__(64 * NW) void stream_kernel(StreamArgs p) {
   }
 }
 
-template <bool FP4, bool GATED, int RT, int R, int NW, int D>
+template <bool FP4, bool GATED, int RT, int R, int NW, int D, bool NT = false>
 hipError_t run_stream(const StreamArgs& a, hipStream_t stream) {
   constexpr int cover = (GATED ? RT / 2 : RT) * 16, bytes = Stream<FP4, RT, R, NW, D>::BYTES;
   static_assert(bytes <= 160 * 1024, "LDS of a CU");
-  auto* kernel = stream_kernel<FP4, GATED, RT, R, NW, D>;
+  auto* kernel = stream_kernel<FP4, GATED, RT, R, NW, D, NT>;
   if constexpr (bytes > 65536) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -221,10 +221,21 @@ hipError_t run_rows(const StreamArgs& a, hipStream_t stream) {
   return run_stream<FP4, GATED, RT16, 16, NW16, 2>(a, stream);
 }
 
+// A bf16 weight, read once, is loaded non-temporally (k = 4096, f = 14336: one
+// row 41.5 -> 38.3 us, 16 rows 44.4 -> 39.6; with more rows later passes find
+// it in the caches).  A 4-bit weight is not: 16 rows 16.9 -> 18.8 us where the
+// caches hold it, 20.6 -> 20.1 where they do not.
+hipError_t run_bf16(const StreamArgs& a, hipStream_t stream) {
+  if (a.m <= 2) return run_stream<false, true, 2, 2, 3, 2, true>(a, stream);
+  if (a.m <= 8) return run_stream<false, true, 2, 8, 3, 2, true>(a, stream);
+  if (a.m <= 16) return run_stream<false, true, 2, 16, 3, 2, true>(a, stream);
+  return run_stream<false, true, 2, 16, 3, 2>(a, stream);
+}
+
 }  // namespace
 
 hipError_t launch_stream(const StreamArgs& a, hipStream_t stream) {
-  if (!a.w_scale) return run_rows<false, true, 2, 4, 2, 4, 2, 4>(a, stream);
+  if (!a.w_scale) return run_bf16(a, stream);
   if (!a.gated) return run_rows<true, false, 1, 8, 1, 8, 1, 4>(a, stream);
   // 64 weight rows share an activation's loads where their workgroups still
   // cover 256 CUs (16 rows, k = 4096: f = 14336 17.0 against 20.8 us; f = 4096 8.2 against 6.4)

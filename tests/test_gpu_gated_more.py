@@ -330,6 +330,9 @@ def test_refusals(sfr):
         lambda: sfr.gated_linear(x, w.cpu()),
         lambda: sfr.gated_linear(x, w, out=torch.empty(8, 65, dtype=torch.bfloat16, device="cuda")),
         lambda: sfr.gated_linear(x, w, out=torch.empty(8, 64, device="cuda")),
+        lambda: sfr.gated_linear(x, w, out=x),                                     # [8, 64] like h, but an input
+        lambda: sfr.gated_linear(x, w, out=w[3:11]),
+        lambda: sfr.mxfp4_gated_linear(x, q, out=x),
         lambda: sfr.gated_linear_checkpointed(x, w, checkpoint=torch.float16),
         lambda: sfr.gated_linear_checkpointed(x, w, checkpoint=None),
         lambda: sfr.gated_linear_backward(dh[:4], w, saved),
