@@ -40,15 +40,15 @@ __device__ __forceinline__ PlainOut plain_of(const DenseParams& p) {
 }
 
 // The W operand's loader in the three forms.
-template <int LW, int BR, int NW, bool PAIR>
+template <int LW, int BR, int NW, bool PAIR, int DEPTH = 1>
 struct WLoader {
   Loader<LW, BR, NW, PAIR> rows;
   __device__ __forceinline__ WLoader(const DenseParams& p, int64_t r0, int64_t k0, int wave, int lane)
       : rows(p.w, p.ldw, r0, p.rows_n, k0, wave, lane) {}
 };
-template <int BR, int NW, bool PAIR>
-struct WLoader<CODES, BR, NW, PAIR> {
-  CodeLoader<BR, NW, PAIR> codes;
+template <int BR, int NW, bool PAIR, int DEPTH>
+struct WLoader<CODES, BR, NW, PAIR, DEPTH> {
+  CodeLoader<BR, NW, PAIR, DEPTH> codes;
   __device__ __forceinline__ WLoader(const DenseParams& p, int64_t r0, int64_t k0, int wave, int lane)
       : codes(p.w, p.w_scale, p.k, r0, p.rows_n, k0, wave, lane) {}
 };
@@ -64,7 +64,7 @@ __global__ __launch_bounds__(64 * WN * WM) void dense_tile_kernel(DenseParams p)
   constexpr int WB = BN * BK * 2, XB = BM * BK * 2, STAGE = WB + XB;
   constexpr bool FP4 = LW == CODES;
   // loads per wavefront and stage into LDS; of codes
-  constexpr int LPS = (FP4 ? 0 : BN / 8 / NW) + BM / 8 / NW, LPC = FP4 ? CodeLoader<BN, NW, PAIR>::LOADS : 0;
+  constexpr int LPS = (FP4 ? 0 : BN / 8 / NW) + BM / 8 / NW, LPC = FP4 ? CodeLoader<BN, NW, PAIR, 1>::LOADS : 0;
   static_assert(BN == WN * 64, "64 weight rows per wavefront");
   static_assert(NW * FM * 16 * 128 <= S * STAGE, "epilogue regions fit");
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
@@ -88,20 +88,19 @@ __global__ __launch_bounds__(64 * WN * WM) void dense_tile_kernel(DenseParams p)
     uint8_t* s = smem + (kt % S) * STAGE;
     lx.stage(s + WB, kdim - kt * BK);
     if constexpr (FP4) {
-      lw.codes.put(s);
-      lw.codes.fetch(kdim - (kt + 1) * BK);
+      lw.codes.template put<0>(s);
+      lw.codes.template fetch<0>(kdim - (kt + 1) * BK);
     } else {
       lw.rows.stage(s, kdim - kt * BK);
     }
   };
-
   v4f acc[FN][FM];
 #pragma unroll
   for (int i = 0; i < FN; ++i)
 #pragma unroll
     for (int j = 0; j < FM; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  if constexpr (FP4) lw.codes.fetch(kdim);
+  if constexpr (FP4) lw.codes.template fetch<0>(kdim);
 #pragma unroll
   for (int s = 0; s < S - 1; ++s)
     if (s < KT) load(s);
@@ -162,8 +161,8 @@ __global__ __launch_bounds__(64 * WN * WM) void dense_tile_kernel(DenseParams p)
 //     0    W0, X       last part of W, step t + 1      W0 x X
 //     1    W1          W0 and X of t + 2               W1 x X
 //     2    W2          W1 of t + 2                     W2 x X      (WH = 3)
-// (CODES: W's codes are fetched one step earlier still; "issued" means decoded
-// into LDS, and each part tile's fetch is two loads like its ROWS form.)
+// (CODES: W's codes are fetched one or two steps earlier still; "issued" means
+// decoded into LDS, and each part tile's fetch is two loads like its ROWS form.)
 // A tile is refilled no earlier than the phase after its last read: every
 // wavefront waits for its LDS reads before the barrier that ends its reading
 // part, and the other group is one barrier away.  `pending` loads per
@@ -185,6 +184,12 @@ __global__ __launch_bounds__(512, 2) void dense_wide_kernel(DenseParams p) {
   constexpr int WPART = 128 * BK * 2, XPART = XR * BK * 2, STAGE = WH * WPART + XT * XPART;
   static_assert(XR % 64 == 0 && (LX != COLS || XR == 128), "tile layouts");
   constexpr int LOADS_X = XF, LOADS_W = 2;  // per wavefront: X's stage, a part of W
+  // Steps in pairs, their LDS addresses fixed: dx at m = 8192 1566 -> 1506 us, m =
+  // 64 525 -> 442; a 4-bit weight (then fetched two steps ahead) in tiles of 256 x
+  // 192 at m = 300 89 -> 82 us, but in 256 x 256 104 -> 106.  The forward pass
+  // with a bf16 weight gains nothing (86 -> 88).
+  constexpr bool PAIRS = LW == COLS || (FP4 && WH * XF <= 6);
+  constexpr int DEPTH = FP4 && PAIRS ? 2 : 1;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
 
   int64_t tm, tn;
@@ -196,9 +201,9 @@ __global__ __launch_bounds__(512, 2) void dense_wide_kernel(DenseParams p) {
   const int64_t k0 = blockIdx.y * p.k_per_split;
   const int kdim = (int)min(p.k - k0, p.k_per_split), KT = (kdim + BK - 1) / BK;
 
-  WLoader<LW, 128, 8, PAIR> lw0(p, n0, k0, wave, lane);
-  WLoader<LW, 128, 8, PAIR> lw1(p, n0 + HN, k0, wave, lane);
-  WLoader<LW, 128, 8, PAIR> lw2(p, n0 + 2 * HN, k0, wave, lane);  // WH = 3
+  WLoader<LW, 128, 8, PAIR, DEPTH> lw0(p, n0, k0, wave, lane);
+  WLoader<LW, 128, 8, PAIR, DEPTH> lw1(p, n0 + HN, k0, wave, lane);
+  WLoader<LW, 128, 8, PAIR, DEPTH> lw2(p, n0 + 2 * HN, k0, wave, lane);  // WH = 3
   Loader<LX, XR, 8, false> lx0(p.x, p.ldx, m0, p.rows_m, k0, wave, lane);
   Loader<LX, XR, 8, false> lx1(p.x, p.ldx, m0 + XR, p.rows_m, k0, wave, lane);  // XT = 2
   const Reader<FP4 ? ROWS : LW, 128, 4> rw(wn * 4, lane);
@@ -219,29 +224,40 @@ __global__ __launch_bounds__(512, 2) void dense_wide_kernel(DenseParams p) {
     lx0.stage(s, kdim - t * BK);
     if constexpr (XT == 2) lx1.stage(s + XPART, kdim - t * BK);
   };
-  // part `part` of W; CODES: the codes fetched one step ago go to LDS and the next step's are fetched
-  auto load_w = [&](auto& l, int part, int t) __attribute__((always_inline)) {
-    uint8_t* tile = smem + (t & 1) * STAGE + part * WPART;
-    if constexpr (FP4) {
-      l.codes.put(tile);
-      l.codes.fetch(kdim - (t + 1) * BK);
+  // Part `part` of W of step t, whose stage is `slot` (a constant in pairs of
+  // steps); CODES: the codes fetched DEPTH steps ago go to LDS and those of step
+  // t + DEPTH are fetched.
+  using Even = std::integral_constant<int, 0>;
+  using Odd = std::integral_constant<int, 1>;
+  auto load_w = [&](auto slot, auto& l, int part, int t) __attribute__((always_inline)) {
+    uint8_t* tile = smem + slot * STAGE + part * WPART;
+    if constexpr (DEPTH == 2) {
+      l.codes.template put<decltype(slot)::value>(tile);
+      l.codes.template fetch<decltype(slot)::value>(kdim - (t + 2) * BK);
+    } else if constexpr (FP4) {
+      l.codes.template put<0>(tile);
+      l.codes.template fetch<0>(kdim - (t + 1) * BK);
     } else {
       l.rows.stage(tile, kdim - t * BK);
     }
   };
   // the loads in the order of the phases
   if constexpr (FP4) {
-    lw0.codes.fetch(kdim);
-    lw1.codes.fetch(kdim);
-    if constexpr (WH == 3) lw2.codes.fetch(kdim);
+    auto ahead = [&](auto& l) __attribute__((always_inline)) {
+      l.codes.template fetch<0>(kdim);
+      if constexpr (DEPTH == 2) l.codes.template fetch<1>(kdim - BK);
+    };
+    ahead(lw0);
+    ahead(lw1);
+    if constexpr (WH == 3) ahead(lw2);
   }
-  load_w(lw0, 0, 0);
+  load_w(Even{}, lw0, 0, 0);
   load_x(0);
-  load_w(lw1, 1, 0);
-  if constexpr (WH == 3) load_w(lw2, 2, 0);
-  load_w(lw0, 0, 1);
+  load_w(Even{}, lw1, 1, 0);
+  if constexpr (WH == 3) load_w(Even{}, lw2, 2, 0);
+  load_w(Odd{}, lw0, 0, 1);
   load_x(1);
-  if constexpr (WH == 3) load_w(lw1, 1, 1);
+  if constexpr (WH == 3) load_w(Odd{}, lw1, 1, 1);
   // W0 and X of step 0 have landed
   wait_vm<(WH == 3 ? 4 : 2) * LOADS_W + LOADS_X>();
   wait_lds();
@@ -270,24 +286,34 @@ __global__ __launch_bounds__(512, 2) void dense_wide_kernel(DenseParams p) {
   // loads issued after the ones that the phase after 0, after 1 (WH = 3) and after the last needs
   constexpr std::integral_constant<int, (WH == 3 ? 4 : 2) * LOADS_W + LOADS_X> after0{}, after_last{};
   constexpr std::integral_constant<int, 4 * LOADS_W + 2 * LOADS_X> after1{};
-  for (int t = 0; t < KT; ++t) {
-    const uint8_t* s = smem + (t & 1) * STAGE;
+  auto step = [&](auto slot, auto other, int t) __attribute__((always_inline)) {
+    const uint8_t* s = smem + slot * STAGE;
     if constexpr (XT == 2) rx.read2(x[0], x[1], s + WH * WPART, XPART);
     else rx.read(x[0], s + WH * WPART);
     rw.read(w, s);
-    if constexpr (WH == 3) load_w(lw2, 2, t + 1);
-    else load_w(lw1, 1, t + 1);
+    if constexpr (WH == 3) load_w(other, lw2, 2, t + 1);
+    else load_w(other, lw1, 1, t + 1);
     multiply(after0, acc[0]);
 
     rw.read(w, s + WPART);
-    load_w(lw0, 0, t + 2);
+    load_w(slot, lw0, 0, t + 2);
     load_x(t + 2);
     if constexpr (WH == 3) {
       multiply(after1, acc[1]);
       rw.read(w, s + 2 * WPART);
-      load_w(lw1, 1, t + 2);
+      load_w(slot, lw1, 1, t + 2);
     }
     multiply(after_last, acc[WH - 1]);
+  };
+  if constexpr (PAIRS) {
+    int t = 0;
+    for (; t + 1 < KT; t += 2) {
+      step(Even{}, Odd{}, t);
+      step(Odd{}, Even{}, t + 1);
+    }
+    if (t < KT) step(Even{}, Odd{}, t);
+  } else {
+    for (int t = 0; t < KT; ++t) step(t & 1, (t + 1) & 1, t);
   }
   if (wn == 0) wg_barrier();
   wait_vm<0>();
@@ -399,8 +425,8 @@ struct Config {
   double one, all, full, lasting, fixed, cols;
 };
 constexpr Config kConfigs[CFG_COUNT] = {
-    {256, 256, 1, 0.95, 1.37, 1.37, 1.66, 5.6, 1.18}, {256, 192, 1, 0.80, 1.06, 1.06, 1.34, 5.0, 1.25},
-    {384, 192, 1, 1.16, 1.60, 1.60, 2.06, 7.0, 1.18}, {128, 128, 2, 0.58, 0.76, 1.05, 1.05, 3.7, 1.0},
+    {256, 256, 1, 0.95, 1.37, 1.37, 1.66, 5.6, 1.0}, {256, 192, 1, 0.80, 1.06, 1.06, 1.34, 5.0, 1.06},
+    {384, 192, 1, 1.16, 1.60, 1.60, 2.06, 7.0, 1.04}, {128, 128, 2, 0.58, 0.76, 1.05, 1.05, 3.7, 1.0},
     {128, 64, 2, 0.45, 0.51, 0.67, 0.67, 3.8, 1.0},  {64, 64, 3, 0.36, 0.40, 0.59, 0.59, 3.0, 1.0}};
 struct Choice {
   int config, slices;

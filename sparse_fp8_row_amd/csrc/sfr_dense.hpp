@@ -129,9 +129,11 @@ struct Loader {
 
 // A 4-bit weight's loads: every thread of NW wavefronts holds E codes of one
 // row, decodes them (exactly) to bf16 and writes them to LDS in the ROWS layout.
-// fetch puts the next stage's codes in flight in registers, put writes them.
-// A fetch is exactly two loads (codes; scale), which the wait counts rely on.
-template <int BR, int NW, bool PAIR>
+// fetch puts the next stage's codes in flight in register set P of DEPTH, put
+// writes them: with two sets, taken in turn, codes are fetched two stages
+// before they are written.  A fetch is exactly two loads (codes; scale), which
+// the wait counts rely on.
+template <int BR, int NW, bool PAIR, int DEPTH>
 struct CodeLoader {
   static constexpr int E = BR * BK / (64 * NW), LOADS = 2;
   static_assert(E == 16 || E == 32, "8 or 16 bytes of codes, one block's scale");
@@ -139,8 +141,8 @@ struct CodeLoader {
   int voff, soff, first, lds;
   bool exists;
   uint32_t xor1;
-  v4i code;
-  uint32_t scale;
+  v4i code[DEPTH];
+  uint32_t scale[DEPTH];
 
   __device__ __forceinline__ CodeLoader(const void* q, const uint8_t* sc, int64_t k, int64_t r0, int64_t rows,
                                         int64_t k0, int wave, int lane) {
@@ -159,31 +161,33 @@ struct CodeLoader {
     lds = r * 128;
     xor1 = (uint32_t)(r & 7);
   }
+  template <int P>
   __device__ __forceinline__ void fetch(int k_left) {
     const bool in = exists && first < k_left;
     const int v = in ? voff : kPastRange;  // past the range: zeros
     if constexpr (E == 16) {
       typedef int v2i __attribute__((ext_vector_type(2)));
       const v2i c = __builtin_bit_cast(v2i, __builtin_amdgcn_raw_buffer_load_b64(rq, v, 0, 0));
-      code[0] = c[0];
-      code[1] = c[1];
+      code[P][0] = c[0];
+      code[P][1] = c[1];
     } else {
-      code = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rq, v, 0, 0));
+      code[P] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rq, v, 0, 0));
     }
-    scale = __builtin_amdgcn_raw_buffer_load_b8(rs, in ? soff : kPastRange, 0, 0);
+    scale[P] = __builtin_amdgcn_raw_buffer_load_b8(rs, in ? soff : kPastRange, 0, 0);
     voff += BK / 2;
     soff += BK / 32;
   }
   // Written by asm: before an ordinary LDS store the compiler waits for the
   // global -> LDS loads in flight.  The caller waits for its LDS writes
   // (wait_lds) before the barrier that publishes them.
+  template <int P>
   __device__ __forceinline__ void put(uint8_t* tile) const {
-    const float f = mx_scale_value(scale & 0xFFu);
+    const float f = mx_scale_value(scale[P] & 0xFFu);
     const uint32_t row = (uint32_t)(uintptr_t)(lds_void_t)tile + lds;
 #pragma unroll
     for (int i = 0; i < E / 8; ++i) {
       typedef uint32_t v4u __attribute__((ext_vector_type(4)));
-      const uint4 v = mx_widen8_e2m1(code[i], f);
+      const uint4 v = mx_widen8_e2m1((uint32_t)code[P][i], f);
       asm volatile("ds_write_b128 %0, %1" ::"v"(row + 16 * ((uint32_t)(first / 8 + i) ^ xor1)),
                    "v"(v4u{v.x, v.y, v.z, v.w})
                    : "memory");
