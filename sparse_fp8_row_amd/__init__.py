@@ -477,7 +477,8 @@ def bsr_linear(x: torch.Tensor, w: BsrWeight, bias: Optional[torch.Tensor] = Non
 # --------------------------------------------------------------------------
 MX_BLOCK = 32
 SFR_ACT = {"silu": 0, "gelu_tanh": 1, "relu": 2}
-_MX = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1, torch.float4_e2m1fn_x2: 2}
+_BF16, _E2M1, _E8M0 = torch.bfloat16, torch.float4_e2m1fn_x2, torch.float8_e8m0fnu
+_MX = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1, _E2M1: 2}
 _SAVE = {torch.bfloat16: 1, torch.float8_e4m3fn: 2, torch.float8_e5m2: 3}
 
 
@@ -494,7 +495,7 @@ class MxTensor:
     @property
     def shape(self):
         r, c = self.codes.shape
-        return (r, 2 * c if self.codes.dtype == torch.float4_e2m1fn_x2 else c)
+        return (r, 2 * c if self.codes.dtype is _E2M1 else c)
 
 
 @dataclass
@@ -515,28 +516,24 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_raw_stream
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _placed(fn):
-    """Runs fn with its first argument's device current and, with an explicit
-    `stream`, with that stream current, so that what the call allocates belongs
-    to the stream its kernels run on, and the memory of its arguments is not
-    used again before that stream is done with them (the stream has to be
-    ordered after what produced them, as for any work).  Nothing is switched
-    when both are so already."""
-    @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
-        t = first.codes if isinstance(first, MxTensor) else first
-        device = t.get_device() if isinstance(t, torch.Tensor) else -1
-        if device < 0 or (stream is None and device == _current_device()):
-            return fn(first, *args, **kw)
-        if stream is not None and stream.device_index != device:
-            raise ValueError(f"stream belongs to GPU {stream.device_index}, the arguments to GPU {device}")
-        with torch.cuda.device(device), torch.cuda.stream(stream):
-            out = fn(first, *args, **kw)
-            if stream is not None:
-                for a in (first, *args, *kw.values()):
-                    _keep(a, stream)
-            return out
-    return call
+def _elsewhere(fn, stream, first, *args):
+    """fn(first, *args) with first's device current and, with an explicit
+    `stream`, with that stream current: what the call allocates then belongs to
+    the stream its kernels run on, and the memory of its arguments is not used
+    again before that stream is done with them (the stream has to be ordered
+    after what produced them, as for any work)."""
+    t = first.codes if isinstance(first, MxTensor) else first
+    device = t.get_device()
+    if device < 0:
+        raise ValueError("the arguments must be GPU tensors")
+    if stream is not None and stream.device_index != device:
+        raise ValueError(f"stream belongs to GPU {stream.device_index}, the arguments to GPU {device}")
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        out = fn(first, *args)
+        if stream is not None:
+            for a in (first, *args):
+                _keep(a, stream)
+        return out
 
 
 def _keep(a, stream):
@@ -552,8 +549,10 @@ def _keep(a, stream):
         _keep(a.gu, stream)
 
 
-def _gpu(t: torch.Tensor, name: str, device: int) -> int:
-    """t's address; t must be contiguous and on GPU `device`."""
+def _refuse(t, name: str, device: int):
+    """The reason why t is not a contiguous tensor on GPU `device`."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
     d = t.get_device()
     if d < 0:
         raise ValueError(f"{name} must be a GPU tensor")
@@ -561,27 +560,37 @@ def _gpu(t: torch.Tensor, name: str, device: int) -> int:
         raise ValueError(f"{name} is on GPU {d}, another device than GPU {device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
 
 
 def _bf16_2d(t: torch.Tensor, name: str, device: int) -> int:
-    if t.dtype is not torch.bfloat16 or t.dim() != 2:
+    """t's address, checked."""
+    if t.dtype is not _BF16 or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D bfloat16 tensor")
-    return _gpu(t, name, device)
+    if t.get_device() != device or device < 0 or not t.is_contiguous():
+        _refuse(t, name, device)
+    return t.data_ptr()
 
 
 def _mx_parts(t, name: str, device: int, kinds=_MX):
     """(rows, cols, address of the codes, of the scales) of an MxTensor, checked."""
     if not isinstance(t, MxTensor):
         raise ValueError(f"{name} must be an MxTensor")
-    if t.codes.dtype not in kinds:
-        raise ValueError(f"{name}: unsupported element type {t.codes.dtype}")
-    if t.codes.dim() != 2 or t.scale.dtype is not torch.float8_e8m0fnu:
+    codes, scale = t.codes, t.scale
+    dtype = codes.dtype
+    if dtype not in kinds:
+        raise ValueError(f"{name}: unsupported element type {dtype}")
+    if codes.dim() != 2 or scale.dtype is not _E8M0:
         raise ValueError(f"{name}: codes must be 2-D and scale float8_e8m0fnu")
-    rows, cols = t.shape
-    if cols % MX_BLOCK != 0 or t.scale.shape != (rows, cols // MX_BLOCK):
+    rows, cols = codes.shape
+    if dtype is _E2M1:
+        cols *= 2
+    if cols % MX_BLOCK != 0 or scale.shape != (rows, cols // MX_BLOCK):
         raise ValueError(f"{name}: scale must have one entry per {MX_BLOCK} columns")
-    return rows, cols, _gpu(t.codes, f"{name}.codes", device), _gpu(t.scale, f"{name}.scale", device)
+    if codes.get_device() != device or scale.get_device() != device or device < 0 or not codes.is_contiguous() or \
+            not scale.is_contiguous():
+        _refuse(codes, f"{name}.codes", device)
+        _refuse(scale, f"{name}.scale", device)
+    return rows, cols, codes.data_ptr(), scale.data_ptr()
 
 
 def _act_enum(name: str) -> int:
@@ -594,10 +603,8 @@ def _span(t: torch.Tensor):
     return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
 
 
-def _output(out, rows: int, cols: int, dtype, *inputs):
-    """out, checked (also against overlapping an input), or a new tensor on the inputs' device."""
-    if out is None:
-        return inputs[0].new_empty((rows, cols), dtype=dtype)
+def _check_out(out: torch.Tensor, rows: int, cols: int, dtype, *inputs):
+    """out has the result's form and overlaps no input."""
     if out.shape != (rows, cols) or out.dtype is not dtype or not out.is_contiguous() or \
             out.device != inputs[0].device:
         raise ValueError("out has the wrong shape, dtype or device")
@@ -606,73 +613,86 @@ def _output(out, rows: int, cols: int, dtype, *inputs):
         a, b = _span(t)
         if a < end and start < b:
             raise ValueError("out overlaps an input")
-    return out
 
 
-@_placed
-def quantize_mx(x: torch.Tensor, dtype=torch.float8_e4m3fn) -> MxTensor:
+def quantize_mx(x: torch.Tensor, dtype=torch.float8_e4m3fn, *, stream=None) -> MxTensor:
     """bf16 [rows, cols] -> MxTensor of float8_e4m3fn, float8_e5m2 or
     float4_e2m1fn_x2 elements (cols a multiple of 32)."""
+    device = x.get_device()
+    if stream is not None or device < 0 or device != _current_device():
+        return _elsewhere(quantize_mx, stream, x, dtype)
     if dtype not in _MX:
         raise ValueError(f"unsupported element type {dtype}")
-    device = x.get_device()
     px = _bf16_2d(x, "x", device)
     rows, cols = x.shape
     if cols == 0 or cols % MX_BLOCK != 0:
         raise SfrError(2, "quantize_mx")
-    codes = x.new_empty((rows, cols // 2 if dtype is torch.float4_e2m1fn_x2 else cols), dtype=dtype)
-    scale = x.new_empty((rows, cols // MX_BLOCK), dtype=torch.float8_e8m0fnu)
+    codes = x.new_empty((rows, cols // 2), dtype=dtype) if dtype is _E2M1 else torch.empty_like(x, dtype=dtype)
+    scale = x.new_empty((rows, cols // MX_BLOCK), dtype=_E8M0)
     _check(load().quantize_mx(px, rows, cols, _MX[dtype], codes.data_ptr(), scale.data_ptr(), _raw_stream(device)),
            "quantize_mx")
     return MxTensor(codes, scale)
 
 
-@_placed
-def dequantize_mx(t: MxTensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+def dequantize_mx(t: MxTensor, out: Optional[torch.Tensor] = None, *, stream=None) -> torch.Tensor:
     """MxTensor -> the bf16 values it stands for (exact)."""
-    device = t.codes.get_device() if isinstance(t, MxTensor) else -1
+    if not isinstance(t, MxTensor):
+        raise ValueError("t must be an MxTensor")
+    codes = t.codes
+    device = codes.get_device()
+    if stream is not None or device < 0 or device != _current_device():
+        return _elsewhere(dequantize_mx, stream, t, out)
     rows, cols, pq, ps = _mx_parts(t, "t", device)
-    out = _output(out, rows, cols, torch.bfloat16, t.codes, t.scale)
-    _check(load().dequantize_mx(pq, ps, rows, cols, _MX[t.codes.dtype], out.data_ptr(), _raw_stream(device)),
+    if out is not None:
+        _check_out(out, rows, cols, _BF16, codes, t.scale)
+    else:
+        out = codes.new_empty((rows, cols), dtype=_BF16)
+    _check(load().dequantize_mx(pq, ps, rows, cols, _MX[codes.dtype], out.data_ptr(), _raw_stream(device)),
            "dequantize_mx")
     return out
 
 
-def _gated_operands(x: torch.Tensor, w: torch.Tensor):
-    device = x.get_device()
+def _gated_operands(x: torch.Tensor, w: torch.Tensor, device: int):
     px, pw = _bf16_2d(x, "x", device), _bf16_2d(w, "w", device)
     m, k = x.shape
     f2, kw = w.shape
     if kw != k or f2 % 2 != 0:
         raise ValueError("w must be [2 f, k] for x [m, k]")
-    return device, px, pw, m, k, f2 // 2
+    return px, pw, m, k, f2 // 2
 
 
-@_placed
-def gated_linear(x: torch.Tensor, w: torch.Tensor, activation: str = "silu",
-                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+def gated_linear(x: torch.Tensor, w: torch.Tensor, activation: str = "silu", out: Optional[torch.Tensor] = None, *,
+                 stream=None) -> torch.Tensor:
     """h [m, f] = act(x @ w[:f].T) * (x @ w[f:].T) for bf16 x [m, k], w [2 f, k]."""
-    device, px, pw, m, k, f = _gated_operands(x, w)
+    device = x.get_device()
+    if stream is not None or device < 0 or device != _current_device():
+        return _elsewhere(gated_linear, stream, x, w, activation, out)
+    px, pw, m, k, f = _gated_operands(x, w, device)
     act = _act_enum(activation)
-    out = _output(out, m, f, torch.bfloat16, x, w)
+    if out is not None:
+        _check_out(out, m, f, _BF16, x, w)
+    else:
+        out = x.new_empty((m, f))
     _check(load().gated_linear_bf16(px, m, k, pw, f, act, out.data_ptr(), 0, None, None, _raw_stream(device)),
            "gated_linear")
     return out
 
 
-@_placed
 def gated_linear_checkpointed(x: torch.Tensor, w: torch.Tensor, activation: str = "silu",
-                              checkpoint=torch.float8_e4m3fn):
+                              checkpoint=torch.float8_e4m3fn, *, stream=None):
     """(h, GatedCheckpoint): gated_linear, keeping for the backward pass x and
     the projections in 8 bits (checkpoint float8_e4m3fn or float8_e5m2: MX
     blocks), or x itself and the projections in bf16 (torch.bfloat16)."""
+    device = x.get_device()
+    if stream is not None or device < 0 or device != _current_device():
+        return _elsewhere(gated_linear_checkpointed, stream, x, w, activation, checkpoint)
     if checkpoint not in _SAVE:
         raise ValueError(f"unsupported checkpoint type {checkpoint}")
-    device, px, pw, m, k, f = _gated_operands(x, w)
+    px, pw, m, k, f = _gated_operands(x, w, device)
     act = _act_enum(activation)
     h = x.new_empty((m, f))
     gu = x.new_empty((m, 2 * f), dtype=checkpoint)
-    scale = None if checkpoint is torch.bfloat16 else x.new_empty((m, 2 * f // MX_BLOCK), dtype=torch.float8_e8m0fnu)
+    scale = None if checkpoint is _BF16 else x.new_empty((m, 2 * f // MX_BLOCK), dtype=_E8M0)
     _check(load().gated_linear_bf16(px, m, k, pw, f, act, h.data_ptr(), _SAVE[checkpoint], gu.data_ptr(),
                                     None if scale is None else scale.data_ptr(), _raw_stream(device)),
            "gated_linear_checkpointed")
@@ -686,15 +706,16 @@ def _saved_parts(t, name: str, device: int):
     if isinstance(t, MxTensor):
         return (*_mx_parts(t, name, device, _SAVE), _SAVE[t.codes.dtype])
     p = _bf16_2d(t, name, device)
-    return (*t.shape, p, None, _SAVE[torch.bfloat16])
+    return (*t.shape, p, None, _SAVE[_BF16])
 
 
-@_placed
 def gated_linear_backward(dh: torch.Tensor, w: torch.Tensor, saved: GatedCheckpoint, need_dx: bool = True,
-                          need_dw: bool = True):
+                          need_dw: bool = True, *, stream=None):
     """(dx [m, k], dw [2 f, k]) in bf16 from dh [m, f], w and what
     gated_linear_checkpointed kept; None in place of one that is not needed."""
     device = dh.get_device()
+    if stream is not None or device < 0 or device != _current_device():
+        return _elsewhere(gated_linear_backward, stream, dh, w, saved, need_dx, need_dw)
     pd, pw = _bf16_2d(dh, "dh", device), _bf16_2d(w, "w", device)
     xm, xk, px, pxs, x_save = _saved_parts(saved.x, "saved.x", device)
     gm, gf2, pg, pgs, g_save = _saved_parts(saved.gu, "saved.gu", device)
@@ -714,7 +735,7 @@ def gated_linear_backward(dh: torch.Tensor, w: torch.Tensor, saved: GatedCheckpo
     return dx, dw
 
 
-_FP4 = (torch.float4_e2m1fn_x2,)
+_FP4 = (_E2M1,)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -722,47 +743,57 @@ def _mxfp4_workspace_bytes(m: int, n: int, k: int) -> int:
     return load().sfr_mxfp4_workspace_bytes(m, n, k)
 
 
-def _mxfp4_operands(x: torch.Tensor, w: MxTensor):
-    device = x.get_device()
+def _mxfp4_operands(x: torch.Tensor, w: MxTensor, device: int):
     px = _bf16_2d(x, "x", device)
     n, wk, pq, ps = _mx_parts(w, "w", device, _FP4)
     m, k = x.shape
     if wk != k:
         raise ValueError("operand shapes do not match")
-    return device, px, pq, ps, m, n, k
+    return px, pq, ps, m, n, k
 
 
-@_placed
 def mxfp4_linear(x: torch.Tensor, w: MxTensor, bias: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
-                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                 out: Optional[torch.Tensor] = None, *, stream=None) -> torch.Tensor:
     """bf16 x [m, k] -> out [m, n] = x @ W.T (+ bias) for a 4-bit weight W [n, k]
     with one scale per 32 values, from quantize_mx(w, torch.float4_e2m1fn_x2)."""
-    device, px, pq, ps, m, n, k = _mxfp4_operands(x, w)
+    device = x.get_device()
+    if stream is not None or device < 0 or device != _current_device():
+        return _elsewhere(mxfp4_linear, stream, x, w, bias, out_dtype, out)
+    px, pq, ps, m, n, k = _mxfp4_operands(x, w, device)
     pb = None
     if bias is not None:
-        pb = _gpu(bias, "bias", device)
-        if bias.dtype is not torch.bfloat16 or bias.shape != (n,):
+        if bias.dtype is not _BF16 or bias.shape != (n,):
             raise ValueError("bias must be bfloat16 [n]")
-    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+        _refuse(bias, "bias", device)
+        pb = bias.data_ptr()
+    if out_dtype is not _BF16 and out_dtype is not torch.float32:
         raise ValueError("out_dtype must be bfloat16 or float32")
-    out = _output(out, m, n, out_dtype, x, w.codes, w.scale)
+    if out is not None:
+        _check_out(out, m, n, out_dtype, x, w.codes, w.scale, *(() if bias is None else (bias,)))
+    else:
+        out = x.new_empty((m, n), dtype=out_dtype)
     nbytes = _mxfp4_workspace_bytes(m, n, k)
     work = x.new_empty((nbytes,), dtype=torch.uint8) if nbytes else None
     _check(load().mxfp4_linear(px, m, k, pq, ps, n, pb, out.data_ptr(),
-                               SFR_OUT_BF16 if out_dtype is torch.bfloat16 else SFR_OUT_F32,
+                               SFR_OUT_BF16 if out_dtype is _BF16 else SFR_OUT_F32,
                                work.data_ptr() if nbytes else None, nbytes, _raw_stream(device)), "mxfp4_linear")
     return out
 
 
-@_placed
-def mxfp4_gated_linear(x: torch.Tensor, w: MxTensor, activation: str = "silu",
-                       out: Optional[torch.Tensor] = None) -> torch.Tensor:
+def mxfp4_gated_linear(x: torch.Tensor, w: MxTensor, activation: str = "silu", out: Optional[torch.Tensor] = None, *,
+                       stream=None) -> torch.Tensor:
     """gated_linear for a 4-bit weight [2 f, k] from quantize_mx(w, torch.float4_e2m1fn_x2)."""
-    device, px, pq, ps, m, n, k = _mxfp4_operands(x, w)
+    device = x.get_device()
+    if stream is not None or device < 0 or device != _current_device():
+        return _elsewhere(mxfp4_gated_linear, stream, x, w, activation, out)
+    px, pq, ps, m, n, k = _mxfp4_operands(x, w, device)
     act = _act_enum(activation)
     if n % 2 != 0:
         raise ValueError("w must be [2 f, k]")
-    out = _output(out, m, n // 2, torch.bfloat16, x, w.codes, w.scale)
+    if out is not None:
+        _check_out(out, m, n // 2, _BF16, x, w.codes, w.scale)
+    else:
+        out = x.new_empty((m, n // 2))
     _check(load().mxfp4_gated_linear(px, m, k, pq, ps, n // 2, act, out.data_ptr(), _raw_stream(device)),
            "mxfp4_gated_linear")
     return out
