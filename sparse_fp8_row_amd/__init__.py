@@ -12,6 +12,11 @@ device memory and the current HIP stream.
 Tensor-wise scaling (one scale per operand): ``quantize_tensorwise_fp8``,
 ``prepare_weight(..., scaling="tensor")`` and ``sparse_fp8_scaled_linear``.
 
+The gated feed-forward block (``gated_linear``, its gradients from 8-bit
+activations, its 4-bit form) and the MX block formats are at the end of this
+module.  None of these calls builds an autograd graph: the gradient is
+``gated_linear_backward``.
+
 The operator follows pytorch/ao PR #1671 ("Add CUTLASS-based row-wise scaled
 sparse FP8 kernel"); see the header for the exact contract of each call.
 There is no fallback: if the library is missing or no GPU is present the

@@ -408,8 +408,8 @@ hipError_t run_wide(DenseParams p, int slices, hipStream_t stream) {
 // modelled time.  A configuration covers bn x bm outputs per workgroup, per_cu
 // workgroups fit on a CU.  us per stage of k of one round of tiles, measured
 // (forward, k = 4096, 64 stages): `one` with few tiles, `all` with one on each of
-// 256 CUs, `full` with every CU full; `lasting` in a run of several rounds,
-// where power lowers the clock of the wide kernels; `cols` times as long with a
+// 256 CUs, `full` with every CU full; `lasting` in place of `full` in a run past
+// 250 us, where power lowers the clock of the wide kernels; `cols` times as long with a
 // COLS W operand (dx).  Examples (measured, us):
 //   m = 300, f = 14336: 256x192 71, 256x256 86, 128x128 97, 128x64 108, 384x192 98
 //   m = 517, f = 14336: 384x192 107, 256x192 135, 128x128 158, 256x256 161
@@ -440,8 +440,8 @@ double model_us(const Config& g, int64_t tiles, int64_t stages, bool cols_w) {
                                     : g.all + (g.full - g.all) * (rest - 256) / (slots - 256);
   const double fixed = g.fixed * (rounds + (rest != 0));
   const double us = (cols_w ? g.cols : 1.0) * stages;
-  const double t = (rounds * g.full + tail) * us + fixed;
-  return t < 250 ? t : (rounds * g.lasting + tail) * us + fixed;
+  const double t = (rounds * g.full + tail) * us;
+  return fixed + (t < 250 ? t : t * g.lasting / g.full);
 }
 
 // n: columns of the output's tiles (2 f when gated).  lx, lw: the operands'

@@ -66,7 +66,7 @@ def test_mxfp4_linear_tiles(sfr, m, k, n):
 @pytest.mark.parametrize("m,k,f", [(1, 2080, 2080), (1, 1056, 2080), (1, 4128, 416), (3000, 4128, 32), (385, 2080, 10272),
                                    (2049, 4128, 32), (130, 4128, 6176), (4097, 4128, 32), (257, 8224, 6176),
                                    (2049, 2080, 32), (65, 4128, 4128), (3000, 1056, 32), (1, 4128, 4128),
-                                   (1, 32, 1056), (1000, 2048, 5632)])
+                                   (1, 32, 1056), (1000, 2048, 5632), (130, 8224, 2080), (4097, 288, 8224)])
 def test_backward_tiles(sfr, m, k, f):
     x, w = inputs(m + f, m, k, 2 * f)
     dh = randn(m, m, f)
