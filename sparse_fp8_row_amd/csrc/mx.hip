@@ -76,14 +76,9 @@ __global__ __launch_bounds__(kThreads) void dequantize_mx_kernel(const uint8_t* 
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
     const int64_t at = base + i * kThreads;
-    const float f = mx_scale_value(s[i]);
     uint4 v;
-    if constexpr (FMT == MX_E2M1) {
-      v = mx_widen8_e2m1(c[i].x, f);
-    } else {
-      v = make_uint4(mx_widen2<FMT, false>(c[i].x, f), mx_widen2<FMT, true>(c[i].x, f),
-                     mx_widen2<FMT, false>(c[i].y, f), mx_widen2<FMT, true>(c[i].y, f));
-    }
+    if constexpr (FMT == MX_E2M1) v = mx_widen8_e2m1(c[i].x, mx_scale_value(s[i]));
+    else v = mx_widen8_fp8<FMT>(c[i], s[i]);
     if (at < chunks) out[at] = v;
   }
 }

@@ -95,6 +95,14 @@ __device__ __forceinline__ uint4 mx_widen8_e2m1(uint32_t w, float scale) {
                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3)));
 }
 
+// Eight FP8 elements and their block's scale byte, as eight bf16 values.
+template <int FMT>
+__device__ __forceinline__ uint4 mx_widen8_fp8(uint2 c, uint32_t code) {
+  const float f = mx_scale_value(code);
+  return make_uint4(mx_widen2<FMT, false>(c.x, f), mx_widen2<FMT, true>(c.x, f), mx_widen2<FMT, false>(c.y, f),
+                    mx_widen2<FMT, true>(c.y, f));
+}
+
 // ---------------------------------------------------------------------------
 // Activation functions.  silu(g) = g s(g); gelu_tanh(g) = g s(2 c (g + 0.044715
 // g^3)) with c = sqrt(2 / pi) (0.5 (1 + tanh z) is s(2 z)); s the logistic
