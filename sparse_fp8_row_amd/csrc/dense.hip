@@ -55,10 +55,13 @@ struct WLoader<CODES, BR, NW, PAIR, DEPTH> {
 
 // ---------------------------------------------------------------------------
 // Tiled kernel: BN x BM outputs per workgroup, WN x WM wavefronts of 64 (n) x
-// BM / WM (m), S stages of BK in LDS.
+// BM / WM (m), S stages of BK in LDS.  KS = 2: two such groups of wavefronts in
+// the workgroup, each with half of k and stages of its own; the second's sums
+// are added to the first's through LDS.  With few tiles, where a CU would hold
+// one group and every stage waits out its latencies, two of them overlap.
 // ---------------------------------------------------------------------------
-template <int LX, int LW, int EPI, int BN, int BM, int WN, int WM, int S>
-__global__ __launch_bounds__(64 * WN * WM) void dense_tile_kernel(DenseParams p) {
+template <int LX, int LW, int EPI, int BN, int BM, int WN, int WM, int S, int KS>
+__global__ __launch_bounds__(64 * WN * WM * KS) void dense_tile_kernel(DenseParams p) {
   constexpr int NW = WN * WM, FM = BM / WM / 16, FN = 4;
   constexpr bool PAIR = EPI == EPI_GATED;
   constexpr int WB = BN * BK * 2, XB = BM * BK * 2, STAGE = WB + XB;
@@ -67,16 +70,22 @@ __global__ __launch_bounds__(64 * WN * WM) void dense_tile_kernel(DenseParams p)
   constexpr int LPS = (FP4 ? 0 : BN / 8 / NW) + BM / 8 / NW, LPC = FP4 ? CodeLoader<BN, NW, PAIR, 1>::LOADS : 0;
   static_assert(BN == WN * 64, "64 weight rows per wavefront");
   static_assert(NW * FM * 16 * 128 <= S * STAGE, "epilogue regions fit");
-  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  static_assert(NW * FN * FM * 1024 <= S * STAGE, "the second group's sums fit in its stages");
+  extern __shared__ __attribute__((aligned(1024))) uint8_t all_smem[];
 
   int64_t tm, tn;
   if (!tile_of(blockIdx.x, p.tiles_m, p.tiles_n, p.group, tm, tn)) return;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, wave_id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kg = KS == 1 ? 0 : wave_id / NW, wave = KS == 1 ? wave_id : wave_id % NW;
+  uint8_t* const smem = all_smem + kg * (S * STAGE);
   const int wn = wave / WM, wm = wave % WM;
   const int64_t m0 = tm * BM, n0 = tn * (PAIR ? BN / 2 : BN);
-  const int64_t k0 = blockIdx.y * p.k_per_split;
-  const int kdim = (int)min(p.k - k0, p.k_per_split);
-  const int KT = (kdim + BK - 1) / BK;
+  const int64_t ks = blockIdx.y * p.k_per_split;
+  const int kslice = (int)min(p.k - ks, p.k_per_split);
+  // every group runs the same number of stages; k past the slice reads zeros
+  const int KT = ((kslice + BK - 1) / BK + KS - 1) / KS;
+  const int64_t k0 = ks + kg * KT * BK;
+  const int kdim = min(kslice - kg * KT * BK, KT * BK);
 
   WLoader<LW, BN, NW, PAIR> lw(p, n0, k0, wave, lane);
   Loader<LX, BM, NW, false> lx(p.x, p.ldx, m0, p.rows_m, k0, wave, lane);
@@ -126,6 +135,23 @@ __global__ __launch_bounds__(64 * WN * WM) void dense_tile_kernel(DenseParams p)
   }
   wait_lds();
   wg_barrier();  // every wavefront is done with the stages: their LDS becomes the epilogue's
+
+  if constexpr (KS == 2) {
+    v4f* const sums = reinterpret_cast<v4f*>(all_smem + S * STAGE) + wave * (FN * FM * 64) + lane;
+    if (kg == 1) {
+#pragma unroll
+      for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j) sums[(i * FM + j) * 64] = acc[i][j];
+      wait_lds();
+    }
+    wg_barrier();
+    if (kg == 1) return;
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FM; ++j) acc[i][j] += sums[(i * FM + j) * 64];
+  }
 
   uint8_t* region = smem + wave * (FM * 16 * 128);
   const int64_t mb = m0 + wm * (FM * 16);
@@ -372,10 +398,11 @@ int64_t set_tiles(DenseParams& p, int64_t bm, int64_t cover) {
   return (tm * tn + 7) / 8 * 8;
 }
 
-template <int LX, int LW, int EPI, int BN, int BM, int WN, int WM, int S>
+template <int LX, int LW, int EPI, int BN, int BM, int WN, int WM, int S, int KS = 1>
 hipError_t run_tile(DenseParams p, int slices, hipStream_t stream) {
-  constexpr int bytes = S * (BN + BM) * BK * 2;
-  auto* kernel = dense_tile_kernel<LX, LW, EPI, BN, BM, WN, WM, S>;
+  constexpr int bytes = KS * S * (BN + BM) * BK * 2;
+  static_assert(bytes <= 160 * 1024, "LDS of a CU");
+  auto* kernel = dense_tile_kernel<LX, LW, EPI, BN, BM, WN, WM, S, KS>;
   if (bytes > 65536) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -384,7 +411,7 @@ hipError_t run_tile(DenseParams p, int slices, hipStream_t stream) {
   constexpr int cover = EPI == EPI_GATED ? BN / 2 : BN;
   const int64_t grid = set_tiles(p, BM, cover);
   if (grid < 0) return hipErrorInvalidValue;
-  kernel<<<dim3((unsigned)grid, (unsigned)slices), dim3(64 * WN * WM), bytes, stream>>>(p);
+  kernel<<<dim3((unsigned)grid, (unsigned)slices), dim3(64 * WN * WM * KS), bytes, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -413,21 +440,38 @@ hipError_t run_wide(DenseParams p, int slices, hipStream_t stream) {
 // COLS W operand (dx).  Examples (measured, us):
 //   m = 300, f = 14336: 256x192 71, 256x256 86, 128x128 97, 128x64 108, 384x192 98
 //   m = 517, f = 14336: 384x192 107, 256x192 135, 128x128 158, 256x256 161
-//   m = 128, f = 14336: 128x64 48, 128x128 49, 256x256 76
+//   m = 128, f = 14336: 128x64 48, 128x128 49 (KS = 2: 44), 256x256 76
+//   m = 140, f = 4096: 64x64 30 (KS = 2: 25), 128x64 32 (25), 128x128 41 (35)
+//   m = 33, k = f = 512: 64x64 5.3 (KS = 2: 4.6), 128x64 6.6 (5.8)
 //   m = 8192, f = 14336: 256x256 1485, 256x192 1618, 384x192 1662, 128x128 1868
 //   dx m = 1000, k = 2048, f = 5632: 128x128 in 1, 2, 4, 8 slices 118, 73, 55, 67,
 //     256x256 211, 122, 76, 59;  m = 4096, k = f = 2048: 128x128 63, 256x192 85
 // Slices (plain outputs only) add a pass over their binary32 partial sums.
 // ---------------------------------------------------------------------------
-enum { CFG_WIDE = 0, CFG_WIDE_192, CFG_WIDE_384, CFG_128, CFG_128x64, CFG_64, CFG_COUNT };
+// _K2: two groups of wavefronts, each with half of k (KS = 2)
+enum {
+  CFG_WIDE = 0,
+  CFG_WIDE_192,
+  CFG_WIDE_384,
+  CFG_128,
+  CFG_128x64,
+  CFG_64,
+  CFG_128_K2,
+  CFG_128x64_K2,
+  CFG_64_K2,
+  CFG_COUNT
+};
 struct Config {
   int bn, bm, per_cu;
+  bool rows_x;  // built for X by rows only
   double one, all, full, lasting, fixed, cols;
 };
 constexpr Config kConfigs[CFG_COUNT] = {
-    {256, 256, 1, 0.95, 1.37, 1.37, 1.66, 5.6, 1.0}, {256, 192, 1, 0.80, 1.06, 1.06, 1.34, 5.0, 1.06},
-    {384, 192, 1, 1.16, 1.60, 1.60, 2.06, 7.0, 1.04}, {128, 128, 2, 0.58, 0.76, 1.05, 1.05, 3.7, 1.0},
-    {128, 64, 2, 0.45, 0.51, 0.67, 0.67, 3.8, 1.0},  {64, 64, 3, 0.36, 0.40, 0.59, 0.59, 3.0, 1.0}};
+    {256, 256, 1, false, 0.95, 1.37, 1.37, 1.66, 5.6, 1.0}, {256, 192, 1, true, 0.80, 1.06, 1.06, 1.34, 5.0, 1.06},
+    {384, 192, 1, true, 1.16, 1.60, 1.60, 2.06, 7.0, 1.04}, {128, 128, 2, false, 0.58, 0.76, 1.05, 1.05, 3.7, 1.0},
+    {128, 64, 2, false, 0.45, 0.51, 0.67, 0.67, 3.8, 1.0},  {64, 64, 3, false, 0.36, 0.40, 0.59, 0.59, 3.0, 1.0},
+    {128, 128, 1, true, 0.45, 0.58, 0.58, 0.58, 4.0, 1.0},  {128, 64, 1, true, 0.30, 0.34, 0.34, 0.34, 4.0, 1.0},
+    {64, 64, 2, true, 0.23, 0.32, 0.42, 0.42, 3.0, 1.0}};
 struct Choice {
   int config, slices;
   int64_t k_per_split;
@@ -445,18 +489,19 @@ double model_us(const Config& g, int64_t tiles, int64_t stages, bool cols_w) {
 }
 
 // n: columns of the output's tiles (2 f when gated).  lx, lw: the operands'
-// layouts (the kernels of 192 rows need X by rows).  can_slice: a plain output.
+// layouts.  can_slice: a plain output.
 Choice choose(int64_t m, int64_t n, int64_t k, int lx, int lw, bool can_slice) {
   const int64_t stages = (k + BK - 1) / BK;
   Choice best{CFG_64, 1, k};
   double least = 1e300;
   for (int c = 0; c < CFG_COUNT; ++c) {
     const Config& g = kConfigs[c];
-    if (g.bm == 192 && lx != ROWS) continue;
+    if (g.rows_x && lx != ROWS) continue;
     const int64_t tiles = ((m + g.bm - 1) / g.bm) * ((n + g.bn - 1) / g.bn);
     for (int s = 1; s <= (can_slice && m * n <= ((int64_t)1 << 30) ? 16 : 1); ++s) {
       const int64_t per = (stages + s - 1) / s;
       if (s > 1 && (per < 8 || (stages + per - 1) / per != s)) continue;
+      if (c >= CFG_128_K2 && per < 2) continue;  // nothing for the second group
       const double t = model_us(g, tiles * s, per, lw == COLS) + (s > 1 ? 3.0 + 8.0 * s * m * n / 6e6 : 0.0);
       if (t < least) {
         least = t;
@@ -479,6 +524,15 @@ hipError_t run_dense(DenseParams p, const Choice& c, void* workspace, hipStream_
       break;
     case CFG_WIDE_384:
       if constexpr (LX == ROWS) e = run_wide<LX, LW, EPI, 3, 3>(p, c.slices, stream);
+      break;
+    case CFG_128_K2:
+      if constexpr (LX == ROWS) e = run_tile<LX, LW, EPI, 128, 128, 2, 2, 2, 2>(p, c.slices, stream);
+      break;
+    case CFG_128x64_K2:
+      if constexpr (LX == ROWS) e = run_tile<LX, LW, EPI, 128, 64, 2, 2, 3, 2>(p, c.slices, stream);
+      break;
+    case CFG_64_K2:
+      if constexpr (LX == ROWS) e = run_tile<LX, LW, EPI, 64, 64, 1, 4, 2, 2>(p, c.slices, stream);
       break;
     case CFG_128: e = run_tile<LX, LW, EPI, 128, 128, 2, 2, 2>(p, c.slices, stream); break;
     case CFG_128x64: e = run_tile<LX, LW, EPI, 128, 64, 2, 2, 3>(p, c.slices, stream); break;
