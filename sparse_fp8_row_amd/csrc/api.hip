@@ -18,13 +18,14 @@ bool out_ok(int dt) { return dt == SFR_OUT_BF16 || dt == SFR_OUT_F32; }
 bool save_ok(int s) { return s >= SFR_SAVE_NONE && s <= SFR_SAVE_E5M2; }
 bool save8(int s) { return s == SFR_SAVE_E4M3 || s == SFR_SAVE_E5M2; }
 bool block_dim(int64_t d, int64_t multiple) { return d > 0 && d <= SFR_MAX_BLOCK_DIM && d % multiple == 0; }
+bool gated_dim(int64_t f) { return block_dim(f, 32) && 2 * f <= SFR_MAX_BLOCK_DIM; }
 // An output of the dense products: its tiles make one grid.
 bool dense_ok(int64_t rows, int64_t cols) {
   const int64_t t = rows > 64 ? 128 : 64;
   return ((rows + t - 1) / t) * ((cols + t - 1) / t) <= ((int64_t)1 << 21);
 }
 bool gated_shape(int64_t m, int64_t k, int64_t f) {
-  return m >= 0 && m <= SFR_MAX_DIM && block_dim(k, 32) && block_dim(2 * f, 64) && dense_ok(m, 2 * f) &&
+  return m >= 0 && m <= SFR_MAX_DIM && block_dim(k, 32) && gated_dim(f) && dense_ok(m, 2 * f) &&
          dense_ok(m, k) && dense_ok(2 * f, k);
 }
 
@@ -307,7 +308,7 @@ sfr_status mxfp4_linear(const uint16_t* x, int64_t m, int64_t k, const uint8_t* 
 sfr_status mxfp4_gated_linear(const uint16_t* x, int64_t m, int64_t k, const uint8_t* wq, const uint8_t* ws, int64_t f,
                               sfr_act_t act, uint16_t* h, void* stream) {
   if (!act_ok(act)) return SFR_ERR_DTYPE;
-  if (m < 0 || m > SFR_MAX_DIM || !block_dim(2 * f, 64) || !block_dim(k, 32) || !dense_ok(m, 2 * f))
+  if (m < 0 || m > SFR_MAX_DIM || !gated_dim(f) || !block_dim(k, 32) || !dense_ok(m, 2 * f))
     return SFR_ERR_SHAPE;
   if (m == 0) return SFR_OK;
   if (!x || !wq || !ws || !h) return SFR_ERR_NULL;

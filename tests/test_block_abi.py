@@ -51,7 +51,7 @@ def test_gated_validation(sfr):
                   dict(x=A, m=4, k=64, w=A, f=96, act=0, h=A, save=2, gu=A, gs=A))
     assert call(act=3) == DTYPE and call(act=-1) == DTYPE and call(save=4) == DTYPE and call(save=-1) == DTYPE
     for bad in (dict(m=-1), dict(m=(1 << 30) + 1), dict(k=48), dict(k=0), dict(k=BIG + 32), dict(f=48), dict(f=0),
-                dict(f=-32), dict(f=BIG // 2 + 32), dict(m=1 << 30, f=BIG // 2)):
+                dict(f=-32), dict(f=BIG // 2 + 32), dict(m=1 << 30, f=BIG // 2), dict(f=32 - (1 << 63))):
         assert call(**bad) == SHAPE, bad
     assert call(m=0, x=None, h=None, gu=None, gs=None) == OK
     for t in ("x", "w", "h", "gu", "gs"):
@@ -74,7 +74,7 @@ def test_gated_backward_validation(sfr):
     assert call(act=7) == DTYPE
     for s in (0, 4, -1):
         assert call(gsave=s) == DTYPE and call(xsave=s) == DTYPE
-    for bad in (dict(m=-1), dict(k=40), dict(k=0), dict(f=16), dict(f=0), dict(k=BIG + 32),
+    for bad in (dict(m=-1), dict(k=40), dict(k=0), dict(f=16), dict(f=0), dict(k=BIG + 32), dict(f=32 - (1 << 63)),
                 dict(bytes=need(4, 64, 96, 3) - 1), dict(bytes=-1)):
         assert call(**bad) == SHAPE, bad
     assert call(dx=None, dw=None) == OK
@@ -96,7 +96,7 @@ def test_mxfp4_validation(sfr, gated):
         call = caller(lib.mxfp4_gated_linear, "x m k wq ws f act out",
                       dict(x=A, m=4, k=64, wq=A, ws=A, f=64, act=0, out=A))
         assert call(act=5) == DTYPE
-        bads = (dict(f=0), dict(f=48), dict(f=BIG // 2 + 32))
+        bads = (dict(f=0), dict(f=48), dict(f=BIG // 2 + 32), dict(f=32 - (1 << 63)))
     else:
         call = caller(lib.mxfp4_linear, "x m k wq ws n bias out od work bytes",
                       dict(x=A, m=4, k=64, wq=A, ws=A, n=64, bias=None, out=A, od=0, work=A, bytes=1 << 40))

@@ -320,6 +320,32 @@ def test_two_graphs_and_streams(sfr):
             assert torch.equal(a, b)
 
 
+def test_host_threads(sfr):
+    """Calls from several host threads at once, each on a stream of its own: no state is shared."""
+    import threading
+    sets = []
+    for i, (m, k, f) in enumerate([(300, 544, 1056), (130, 4128, 2080), (5, 160, 64)]):
+        x, w = inputs(60 + i, m, k, 2 * f)
+        sets.append((x, w, sfr.quantize_mx(w, FP4), randn(70 + i, m, f), randn(80 + i, 2 * f), E4M3))
+    wants = [[t.clone() for t in everything(sfr, *a)] for a in sets]
+    torch.cuda.synchronize()
+    same = [False] * len(sets)
+
+    def run(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            got = [everything(sfr, *sets[i]) for _ in range(5)]
+        s.synchronize()
+        same[i] = all(torch.equal(a, b) for g in got for a, b in zip(g, wants[i]))
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(sets))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert all(same)
+
+
 def test_refusals(sfr):
     x, w = inputs(1, 8, 64, 128)
     q, dh = sfr.quantize_mx(w, FP4), randn(2, 8, 64)
