@@ -22,17 +22,17 @@ struct DenseParams {
   int64_t rows_m, rows_n;  // rows of X; rows of W (GATED: of one half)
   int64_t k;
   int64_t k_per_split;  // multiple of BK; k of one slice of the sum
-  int tiles_m, tiles_n, group;
+  int slices, tiles_m, tiles_n, group;
   float* partial;  // with several slices: binary32 [slices, m, n], summed by dense_reduce_kernel
   PlainOut plain;
   GatedOut gated;
 };
 
 // Where this workgroup's outputs go: the output, or its slice's partial sums.
-__device__ __forceinline__ PlainOut plain_of(const DenseParams& p) {
+__device__ __forceinline__ PlainOut plain_of(const DenseParams& p, uint32_t slice) {
   PlainOut o = p.plain;
   if (p.partial) {
-    o.out = p.partial + (int64_t)blockIdx.y * o.m * o.n;
+    o.out = p.partial + (int64_t)slice * o.m * o.n;
     o.bias = nullptr;
     o.out_fmt = OUT_F32;
   }
@@ -73,14 +73,15 @@ __global__ __launch_bounds__(64 * WN * WM * KS) void dense_tile_kernel(DensePara
   static_assert(NW * FN * FM * 1024 <= S * STAGE, "the second group's sums fit in its stages");
   extern __shared__ __attribute__((aligned(1024))) uint8_t all_smem[];
 
+  uint32_t slice;
   int64_t tm, tn;
-  if (!tile_of(blockIdx.x, p.tiles_m, p.tiles_n, p.group, tm, tn)) return;
+  if (!tile_of(blockIdx.x, p.slices, p.tiles_m, p.tiles_n, p.group, slice, tm, tn)) return;
   const int lane = threadIdx.x & 63, wave_id = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kg = KS == 1 ? 0 : wave_id / NW, wave = KS == 1 ? wave_id : wave_id % NW;
   uint8_t* const smem = all_smem + kg * (S * STAGE);
   const int wn = wave / WM, wm = wave % WM;
   const int64_t m0 = tm * BM, n0 = tn * (PAIR ? BN / 2 : BN);
-  const int64_t ks = blockIdx.y * p.k_per_split;
+  const int64_t ks = slice * p.k_per_split;
   const int kslice = (int)min(p.k - ks, p.k_per_split);
   // every group runs the same number of stages; k past the slice reads zeros
   const int KT = ((kslice + BK - 1) / BK + KS - 1) / KS;
@@ -167,7 +168,7 @@ __global__ __launch_bounds__(64 * WN * WM * KS) void dense_tile_kernel(DensePara
     }
     gated_epilogue<FM>(g, u, p.gated, mb, n0 + wn * 32, lane, region);
   } else {
-    plain_epilogue<FM>(acc, plain_of(p), mb, n0 + wn * 64, lane, region);
+    plain_epilogue<FM>(acc, plain_of(p, slice), mb, n0 + wn * 64, lane, region);
   }
 }
 
@@ -218,13 +219,14 @@ __global__ __launch_bounds__(512, 2) void dense_wide_kernel(DenseParams p) {
   constexpr int DEPTH = FP4 && PAIRS ? 2 : 1;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
 
+  uint32_t slice;
   int64_t tm, tn;
-  if (!tile_of(blockIdx.x, p.tiles_m, p.tiles_n, p.group, tm, tn)) return;
+  if (!tile_of(blockIdx.x, p.slices, p.tiles_m, p.tiles_n, p.group, slice, tm, tn)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wave >> 2, wm = wave & 3;
   constexpr int HN = PAIR ? 64 : 128;  // W rows (of one of the pair) per part
   const int64_t m0 = tm * (64 * XF), n0 = tn * (WH * HN);
-  const int64_t k0 = blockIdx.y * p.k_per_split;
+  const int64_t k0 = slice * p.k_per_split;
   const int kdim = (int)min(p.k - k0, p.k_per_split), KT = (kdim + BK - 1) / BK;
 
   WLoader<LW, 128, 8, PAIR, DEPTH> lw0(p, n0, k0, wave, lane);
@@ -363,7 +365,7 @@ __global__ __launch_bounds__(512, 2) void dense_wide_kernel(DenseParams p) {
         }
         gated_epilogue<XFT>(g, u, p.gated, mb, n0 + h * 64 + wn * 32, lane, region);
       } else {
-        plain_epilogue<XFT>(a, plain_of(p), mb, n0 + h * 128 + wn * 64, lane, region);
+        plain_epilogue<XFT>(a, plain_of(p, slice), mb, n0 + h * 128 + wn * 64, lane, region);
       }
     }
 }
@@ -375,7 +377,16 @@ __global__ __launch_bounds__(256) void dense_reduce_kernel(const float* __restri
   if (at >= quads) return;
   const v4f* p = reinterpret_cast<const v4f*>(partial);
   v4f s = p[at];
-  for (int i = 1; i < slices; ++i) s += p[at + i * quads];
+  int i = 1;
+  for (; i + 4 <= slices; i += 4) {  // four loads in flight
+    const v4f a = p[at + i * quads], b = p[at + (i + 1) * quads], c = p[at + (i + 2) * quads],
+              d = p[at + (i + 3) * quads];
+    s += a;
+    s += b;
+    s += c;
+    s += d;
+  }
+  for (; i < slices; ++i) s += p[at + i * quads];
   if (o.bias) {
     const uint2 b = *reinterpret_cast<const uint2*>(o.bias + at * 4 % o.n);
     s[0] += bf16_to_f32(b.x & 0xFFFFu);
@@ -389,13 +400,15 @@ __global__ __launch_bounds__(256) void dense_reduce_kernel(const float* __restri
 
 // Tiles of bm x `cover` rows; the workgroups of the grid, or -1 where the tiles
 // pass what the kernels index (the entry points refuse such sizes).
-int64_t set_tiles(DenseParams& p, int64_t bm, int64_t cover) {
+int64_t set_tiles(DenseParams& p, int64_t bm, int64_t cover, int slices) {
   const int64_t tm = (p.rows_m + bm - 1) / bm, tn = (p.rows_n + cover - 1) / cover;
-  if (tm * tn > ((int64_t)1 << 23) - 8) return -1;
+  const int64_t items = tm * tn * slices;
+  if (items > ((int64_t)1 << 23) - 8) return -1;
+  p.slices = slices;
   p.tiles_m = (int)tm;
   p.tiles_n = (int)tn;
   p.group = 8;
-  return (tm * tn + 7) / 8 * 8;
+  return (items + 7) / 8 * 8;
 }
 
 template <int LX, int LW, int EPI, int BN, int BM, int WN, int WM, int S, int KS = 1>
@@ -409,9 +422,9 @@ hipError_t run_tile(DenseParams p, int slices, hipStream_t stream) {
     if (e != hipSuccess) return e;
   }
   constexpr int cover = EPI == EPI_GATED ? BN / 2 : BN;
-  const int64_t grid = set_tiles(p, BM, cover);
+  const int64_t grid = set_tiles(p, BM, cover, slices);
   if (grid < 0) return hipErrorInvalidValue;
-  kernel<<<dim3((unsigned)grid, (unsigned)slices), dim3(64 * WN * WM * KS), bytes, stream>>>(p);
+  kernel<<<dim3((unsigned)grid), dim3(64 * WN * WM * KS), bytes, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -424,9 +437,9 @@ hipError_t run_wide(DenseParams p, int slices, hipStream_t stream) {
                                            hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != hipSuccess) return e;
   constexpr int cover = EPI == EPI_GATED ? 64 * WH : 128 * WH;
-  const int64_t grid = set_tiles(p, 64 * XF, cover);
+  const int64_t grid = set_tiles(p, 64 * XF, cover, slices);
   if (grid < 0) return hipErrorInvalidValue;
-  kernel<<<dim3((unsigned)grid, (unsigned)slices), dim3(512), bytes, stream>>>(p);
+  kernel<<<dim3((unsigned)grid), dim3(512), bytes, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -502,6 +515,11 @@ Choice choose(int64_t m, int64_t n, int64_t k, int lx, int lw, bool can_slice) {
       const int64_t per = (stages + s - 1) / s;
       if (s > 1 && (per < 8 || (stages + per - 1) / per != s)) continue;
       if (c >= CFG_128_K2 && per < 2) continue;  // nothing for the second group
+      // with few stages the stores are most of the time, and only where a CU
+      // holds several workgroups does another's work go on meanwhile (128x128
+      // against 256x256, m = 8192, f = 14336, k = 64: 92, 111 us; dW k = 4096, f =
+      // 14336: m = 64 51, 57; m = 190 75, 79; m = 250 84, 82..90; m = 300 98, 91)
+      if (c <= CFG_WIDE_384 && per < 4) continue;
       const double t = model_us(g, tiles * s, per, lw == COLS) + (s > 1 ? 3.0 + 8.0 * s * m * n / 6e6 : 0.0);
       if (t < least) {
         least = t;

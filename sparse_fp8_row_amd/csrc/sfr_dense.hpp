@@ -515,14 +515,17 @@ __device__ __forceinline__ void plain_epilogue(v4f (&acc)[4][FM], const PlainOut
   }
 }
 
-// Tile of workgroup `id` of 8 * ceil(T / 8): XCD id % 8 (each has its own L2)
-// owns a contiguous run of the tiles, taken in groups of `group` n tiles.
-// False past the last tile.  (32-bit: the launchers bound T by 2^23.)
-__device__ __forceinline__ bool tile_of(uint32_t id, uint32_t tiles_m, uint32_t tiles_n, uint32_t group, int64_t& tm,
-                                        int64_t& tn) {
-  const uint32_t T = tiles_m * tiles_n, per = (T + 7) / 8;
-  const uint32_t lid = (id % 8) * per + id / 8;
-  if (id / 8 >= per || lid >= T) return false;
+// Slice and tile of workgroup `id` of 8 * ceil(slices * T / 8): XCD id % 8 (each
+// has its own L2) owns a contiguous run of them, slice by slice, the tiles of a
+// slice in groups of `group` n tiles.  False past the last.  (32-bit: the
+// launchers bound slices * T by 2^23.)
+__device__ __forceinline__ bool tile_of(uint32_t id, uint32_t slices, uint32_t tiles_m, uint32_t tiles_n,
+                                        uint32_t group, uint32_t& slice, int64_t& tm, int64_t& tn) {
+  const uint32_t T = tiles_m * tiles_n, items = slices * T, per = (items + 7) / 8;
+  uint32_t lid = (id % 8) * per + id / 8;
+  if (id / 8 >= per || lid >= items) return false;
+  slice = slices == 1 ? 0 : lid / T;
+  lid -= slice * T;
   const uint32_t g = lid / (group * tiles_m), first = g * group;
   const uint32_t size = min(tiles_n - first, group), within = lid - first * tiles_m;
   tn = first + within % size;

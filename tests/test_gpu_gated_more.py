@@ -26,12 +26,13 @@ def randn(seed, *shape, scale=1.0):
     return (scale * torch.randn(*shape, generator=torch.Generator().manual_seed(seed))).bfloat16().cuda()
 
 
-# Per product the smallest shapes (m, k, f) at which the choice takes each tile
-# size, with one half stage of k (k = 32), and others with more and odd stages.
+# Per product shapes (m, k, f) at which the choice takes each tile size, the
+# smallest with half a stage of k (k = 32), others with more and odd stages.
 @pytest.mark.parametrize("m,k,f", [(3000, 32, 2080), (2049, 32, 2080), (2049, 32, 4128), (1001, 32, 2080),
                                    (513, 32, 3104), (3000, 288, 2080), (300, 544, 14336), (517, 288, 14336),
                                    (1001, 416, 2080), (200, 1056, 14336), (130, 32, 32), (513, 288, 3104),
-                                   (385, 1056, 2080), (130, 96, 160), (77, 1120, 96)])
+                                   (385, 1056, 2080), (130, 96, 160), (77, 1120, 96), (1300, 288, 3104),
+                                   (257, 288, 16416)])
 def test_forward_tiles(sfr, m, k, f):
     x, w = inputs(m + f, m, k, 2 * f)
     h, bound, (g, u, eg, eu) = gated64(x.double(), w.double(), "silu")
@@ -54,7 +55,8 @@ def test_forward_tiles(sfr, m, k, f):
                                    (4097, 32, 4128), (300, 8224, 16416), (2049, 32, 2080), (65, 4128, 8224),
                                    (3000, 32, 1056), (65, 2080, 8224), (130, 2080, 48), (4097, 96, 4128),
                                    (130, 4128, 4128), (130, 32, 32), (65, 4128, 4128), (1001, 288, 3104),
-                                   (65, 4128, 6176), (385, 1056, 4128), (65, 8224, 2080), (130, 96, 48)])
+                                   (65, 4128, 6176), (385, 1056, 4128), (65, 8224, 2080), (130, 96, 48),
+                                   (3000, 288, 4128), (2049, 288, 4128), (4097, 288, 4128), (130, 8224, 6176)])
 def test_mxfp4_linear_tiles(sfr, m, k, n):
     x, w = inputs(m + n, m, k, n)
     q = sfr.quantize_mx(w, FP4)
@@ -70,7 +72,8 @@ def test_mxfp4_linear_tiles(sfr, m, k, n):
                                    (2049, 4128, 32), (130, 4128, 6176), (4097, 4128, 32), (257, 8224, 6176),
                                    (2049, 2080, 32), (65, 4128, 4128), (3000, 1056, 32), (1, 4128, 4128),
                                    (1, 32, 1056), (1000, 2048, 5632), (130, 8224, 2080), (4097, 288, 8224),
-                                   (1, 32, 32), (1, 32, 96), (1, 4128, 3104), (3000, 1056, 416), (1, 2080, 8224)])
+                                   (1, 32, 32), (1, 32, 96), (1, 4128, 3104), (3000, 1056, 416), (1, 2080, 8224),
+                                   (3000, 4128, 416), (2049, 4128, 416), (4097, 4128, 416), (257, 2080, 2080)])
 def test_backward_tiles(sfr, m, k, f):
     x, w = inputs(m + f, m, k, 2 * f)
     dh = randn(m, m, f)
