@@ -488,10 +488,11 @@ constexpr Config kConfigs[CFG_COUNT] = {
 struct Choice {
   int config, slices;
   int64_t k_per_split;
+  double us;  // modelled
 };
 
-double model_us(const Config& g, int64_t tiles, int64_t stages, bool cols_w) {
-  const int64_t slots = 256 * g.per_cu, rounds = tiles / slots, rest = tiles % slots;
+double model_us(const Config& g, uint32_t tiles, uint32_t stages, bool cols_w) {
+  const uint32_t slots = 256 * g.per_cu, rounds = tiles / slots, rest = tiles % slots;
   const double tail = rest == 0     ? 0
                       : rest <= 256 ? g.one + (g.all - g.one) * rest / 256
                                     : g.all + (g.full - g.all) * (rest - 256) / (slots - 256);
@@ -502,29 +503,34 @@ double model_us(const Config& g, int64_t tiles, int64_t stages, bool cols_w) {
 }
 
 // n: columns of the output's tiles (2 f when gated).  lx, lw: the operands'
-// layouts.  can_slice: a plain output.
+// layouts.  can_slice: a plain output.  (On the way of every call: 32-bit
+// divisions, and no slices where the tiles alone make four rounds.)
 Choice choose(int64_t m, int64_t n, int64_t k, int lx, int lw, bool can_slice) {
-  const int64_t stages = (k + BK - 1) / BK;
-  Choice best{CFG_64, 1, k};
-  double least = 1e300;
+  const uint32_t stages = (uint32_t)((k + BK - 1) / BK);
+  uint32_t tiles[CFG_COUNT];
   for (int c = 0; c < CFG_COUNT; ++c) {
-    const Config& g = kConfigs[c];
-    if (g.rows_x && lx != ROWS) continue;
-    const int64_t tiles = ((m + g.bm - 1) / g.bm) * ((n + g.bn - 1) / g.bn);
-    for (int s = 1; s <= (can_slice && m * n <= ((int64_t)1 << 30) ? 16 : 1); ++s) {
-      const int64_t per = (stages + s - 1) / s;
-      if (s > 1 && (per < 8 || (stages + per - 1) / per != s)) continue;
+    const uint32_t bm = kConfigs[c].bm, bn = kConfigs[c].bn;
+    tiles[c] = (((uint32_t)m + bm - 1) / bm) * (((uint32_t)n + bn - 1) / bn);
+  }
+  Choice best{CFG_64, 1, k, 1e300};
+  const uint32_t most = can_slice && m * n <= ((int64_t)1 << 30) ? 16 : 1;
+  for (uint32_t s = 1; s <= most; ++s) {
+    const uint32_t per = s == 1 ? stages : (stages + s - 1) / s;
+    if (s > 1 && per < 8) break;
+    if (s > 1 && (stages + per - 1) / per != s) continue;
+    const double join = s > 1 ? 3.0 + 8.0 * s * m * n / 6e6 : 0.0;
+    if (join >= best.us) break;
+    for (int c = 0; c < CFG_COUNT; ++c) {
+      const Config& g = kConfigs[c];
+      if ((g.rows_x && lx != ROWS) || (s > 1 && tiles[c] * s > 1024)) continue;
       if (c >= CFG_128_K2 && per < 2) continue;  // nothing for the second group
       // with few stages the stores are most of the time, and only where a CU
       // holds several workgroups does another's work go on meanwhile (128x128
       // against 256x256, m = 8192, f = 14336, k = 64: 92, 111 us; dW k = 4096, f =
       // 14336: m = 64 51, 57; m = 190 75, 79; m = 250 84, 82..90; m = 300 98, 91)
       if (c <= CFG_WIDE_384 && per < 4) continue;
-      const double t = model_us(g, tiles * s, per, lw == COLS) + (s > 1 ? 3.0 + 8.0 * s * m * n / 6e6 : 0.0);
-      if (t < least) {
-        least = t;
-        best = Choice{c, s, s == 1 ? k : per * BK};
-      }
+      const double t = model_us(g, tiles[c] * s, per, lw == COLS) + join;
+      if (t < best.us) best = Choice{c, (int)s, s == 1 ? k : (int64_t)per * BK, t};
     }
   }
   return best;
@@ -568,6 +574,10 @@ int64_t slice_bytes(int64_t m, int64_t n, int64_t k, int lw) {
 }
 
 }  // namespace
+
+double dense_us(int64_t m, int64_t n, int64_t k, bool fp4, bool gated) {
+  return choose(m, n, k, ROWS, fp4 ? CODES : ROWS, !gated).us;
+}
 
 // Workspace: the slices' partial sums.
 int64_t dense_nt_workspace_bytes(int64_t m, int64_t n, int64_t k) { return slice_bytes(m, n, k, CODES); }

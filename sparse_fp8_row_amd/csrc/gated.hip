@@ -91,7 +91,7 @@ int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
 }  // namespace
 
 hipError_t launch_gated(const GatedArgs& a, hipStream_t stream) {
-  if (a.gu_fmt == GU_NONE && stream_rows(a.m, 2 * a.f, a.k, false)) {
+  if (a.gu_fmt == GU_NONE && stream_rows(a.m, 2 * a.f, a.k, false, true)) {
     StreamArgs s{};
     s.x = a.x;
     s.w = a.w;
@@ -146,11 +146,11 @@ hipError_t launch_gated_backward(const GatedBackwardArgs& a, void* workspace, hi
 }
 
 int64_t mxfp4_workspace_bytes(int64_t m, int64_t n, int64_t k, bool gated) {
-  return gated || stream_rows(m, n, k, true) ? 0 : align256(dense_nt_workspace_bytes(m, n, k));
+  return gated || stream_rows(m, n, k, true, false) ? 0 : align256(dense_nt_workspace_bytes(m, n, k));
 }
 
 hipError_t launch_mxfp4(const StreamArgs& a, void* workspace, hipStream_t stream) {
-  if (stream_rows(a.m, a.gated ? 2 * a.rows : a.rows, a.k, true)) return launch_stream(a, stream);
+  if (stream_rows(a.m, a.gated ? 2 * a.rows : a.rows, a.k, true, a.gated)) return launch_stream(a, stream);
   if (!a.gated) return launch_mxfp4_dense(a, workspace, stream);
   GatedArgs g{};
   g.x = a.x;

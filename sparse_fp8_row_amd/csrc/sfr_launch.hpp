@@ -134,8 +134,10 @@ struct StreamArgs {
   void* out;
   int out_fmt;
 };
-bool stream_rows(int64_t m, int64_t n, int64_t k, bool fp4);  // n: weight rows (2 f when gated)
+bool stream_rows(int64_t m, int64_t n, int64_t k, bool fp4, bool gated);  // n: weight rows (2 f when gated)
 hipError_t launch_stream(const StreamArgs& a, hipStream_t stream);
+// Modelled time of the matrix-core form, us.
+double dense_us(int64_t m, int64_t n, int64_t k, bool fp4, bool gated);
 // The matrix-core form of the 4-bit linear layer (not gated), any m.
 int64_t dense_nt_workspace_bytes(int64_t m, int64_t n, int64_t k);
 hipError_t launch_mxfp4_dense(const StreamArgs& a, void* workspace, hipStream_t stream);

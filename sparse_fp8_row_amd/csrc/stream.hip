@@ -195,17 +195,24 @@ hipError_t run_stream(const StreamArgs& a, hipStream_t stream) {
 }  // namespace
 
 // Whether the weight is streamed per 16 activation rows or multiplied in tiles
-// that hold every row.  A 4-bit weight up to 32 rows (k = 4096, f = 14336: 31.7
-// us against 40.4 at 32 rows, 44.4 against 40.4 at 33), a bf16 one up to 16
-// (45.8 against 50.8 us at 16, 76.5 against 51.1 at 17).  More rows where all
-// passes over the weight together stay small, since a tile walks the whole of k
-// by itself: below 32 MB of codes (n = 6144, k = 4096: 11.7 against 15.6 us at
-// 27 MB, 18.0 against 16.9 at 40 MB) or 64 MB of bf16 (k = f = 2048: 9.7
-// against 12.3 us at 50 MB).
-bool stream_rows(int64_t m, int64_t n, int64_t k, bool fp4) {
+// that hold every row: up to 8 rows always, up to eight passes over the weight
+// where the modelled time is less than the tiles' (us: what each tile of 16
+// weight rows and each byte of the weight cost a pass, from k = 480 .. 4096 and
+// n = 704 .. 28672; the tiles walk all of k by themselves, but read the weight once).
+// Measured, stream against tiles, us:
+//   bf16, k = 4096, f = 4096: 17 rows 15.9, 22.1; 33 rows 25.8, 22.2
+//         k = 704, f = 9248: 17 rows 11.9, 8.7
+//   4-bit linear, k = 320, n = 10240: 16 rows 6.4, 4.5; k = 4096, n = 8192: 8.2, 14.5
+//   4-bit gated, k = 4096, f = 4096: 48 rows 15.0, 19.7; 96 rows 27.7, 20.4
+//   4-bit linear, k = 4096, n = 8192: 32 rows 14.8, 15.6; 33 rows 21.0, 15.7
+bool stream_rows(int64_t m, int64_t n, int64_t k, bool fp4, bool gated) {
   const int64_t passes = (m + 15) / 16;
-  if (passes <= (fp4 ? 2 : 1)) return true;
-  return passes <= 8 && passes * n * k * (fp4 ? 1 : 4) <= (int64_t)(fp4 ? 64 : 128) << 20;
+  if (m <= 8) return true;
+  if (passes > 8) return false;
+  const double bytes = (double)n * k * (fp4 ? 0.5 : 2.0);
+  const double pass = !fp4 ? bytes / 9e6 : (gated ? 0.0043 / 32 : 0.0057 / 16) * n + bytes / 5e6;
+  const double tiles = dense_us(m, n, k, fp4, gated), read = bytes / 4.8e6 + 3;
+  return (fp4 ? 2 : 3) + passes * pass <= (tiles > read ? tiles : read);
 }
 
 namespace {

@@ -32,7 +32,7 @@ def randn(seed, *shape, scale=1.0):
                                    (513, 32, 3104), (3000, 288, 2080), (300, 544, 14336), (517, 288, 14336),
                                    (1001, 416, 2080), (200, 1056, 14336), (130, 32, 32), (513, 288, 3104),
                                    (385, 1056, 2080), (130, 96, 160), (77, 1120, 96), (1300, 288, 3104),
-                                   (257, 288, 16416)])
+                                   (257, 288, 16416), (16, 1056, 8224), (27, 2080, 8224), (50, 1120, 1056)])
 def test_forward_tiles(sfr, m, k, f):
     x, w = inputs(m + f, m, k, 2 * f)
     h, bound, (g, u, eg, eu) = gated64(x.double(), w.double(), "silu")
@@ -56,7 +56,8 @@ def test_forward_tiles(sfr, m, k, f):
                                    (3000, 32, 1056), (65, 2080, 8224), (130, 2080, 48), (4097, 96, 4128),
                                    (130, 4128, 4128), (130, 32, 32), (65, 4128, 4128), (1001, 288, 3104),
                                    (65, 4128, 6176), (385, 1056, 4128), (65, 8224, 2080), (130, 96, 48),
-                                   (3000, 288, 4128), (2049, 288, 4128), (4097, 288, 4128), (130, 8224, 6176)])
+                                   (3000, 288, 4128), (2049, 288, 4128), (4097, 288, 4128), (130, 8224, 6176),
+                                   (385, 4128, 1056)])
 def test_mxfp4_linear_tiles(sfr, m, k, n):
     x, w = inputs(m + n, m, k, n)
     q = sfr.quantize_mx(w, FP4)
