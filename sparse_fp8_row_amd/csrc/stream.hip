@@ -196,23 +196,24 @@ hipError_t run_stream(const StreamArgs& a, hipStream_t stream) {
 
 // Whether the weight is streamed per 16 activation rows or multiplied in tiles
 // that hold every row: up to 8 rows always, up to eight passes over the weight
-// where the modelled time is less than the tiles' (us: what each tile of 16
-// weight rows and each byte of the weight cost a pass, from k = 480 .. 4096 and
-// n = 704 .. 28672; the tiles walk all of k by themselves, but read the weight once).
+// where the modelled time is less than the tiles' (us: what each 16 weight rows
+// and each byte of the weight cost a pass, within a quarter of what 12 sizes
+// from k = 704 to 8192 took; the tiles walk all of k by themselves, but read the
+// weight once).
 // Measured, stream against tiles, us:
 //   bf16, k = 4096, f = 4096: 17 rows 15.9, 22.1; 33 rows 25.8, 22.2
 //         k = 704, f = 9248: 17 rows 11.9, 8.7
-//   4-bit linear, k = 320, n = 10240: 16 rows 6.4, 4.5; k = 4096, n = 8192: 8.2, 14.5
-//   4-bit gated, k = 4096, f = 4096: 48 rows 15.0, 19.7; 96 rows 27.7, 20.4
-//   4-bit linear, k = 4096, n = 8192: 32 rows 14.8, 15.6; 33 rows 21.0, 15.7
+//   4-bit linear, k = 4096, n = 8192: 32 rows 9.6, 15.6; 100 rows 25.9, 22.9
+//   4-bit gated, k = 4096, f = 4096: 64 rows 15.3, 19.6; 100 rows 27.0, 20.7
+//         k = 704, f = 9248: 16 rows 5.4, 8.6; 48 rows 12.5, 8.6
 bool stream_rows(int64_t m, int64_t n, int64_t k, bool fp4, bool gated) {
   const int64_t passes = (m + 15) / 16;
   if (m <= 8) return true;
   if (passes > 8) return false;
   const double bytes = (double)n * k * (fp4 ? 0.5 : 2.0);
-  const double pass = !fp4 ? bytes / 9e6 : (gated ? 0.0043 / 32 : 0.0057 / 16) * n + bytes / 5e6;
+  const double pass = fp4 ? 0.0015 / 16 * n + bytes / 5.6e6 : bytes / 9e6;
   const double tiles = dense_us(m, n, k, fp4, gated), read = bytes / 4.8e6 + 3;
-  return (fp4 ? 2 : 3) + passes * pass <= (tiles > read ? tiles : read);
+  return 3 + passes * pass <= (tiles > read ? tiles : read);
 }
 
 namespace {
@@ -221,11 +222,9 @@ namespace {
 // grow with R, so 2 and 8 rows have forms of their own (n = 4096, k = 4096,
 // 4-bit: 3.3, 3.9, 4.7 us for 1, 8, 16 rows; 8 rows in the 16-row form 4.6).  Two
 // buffers everywhere: more workgroups on a CU gain more than deeper ones.
-template <bool FP4, bool GATED, int RT2, int NW2, int RT8, int NW8, int RT16, int NW16>
-hipError_t run_rows(const StreamArgs& a, hipStream_t stream) {
-  if (a.m <= 2) return run_stream<FP4, GATED, RT2, 2, NW2, 2>(a, stream);
-  if (a.m <= 8) return run_stream<FP4, GATED, RT8, 8, NW8, 2>(a, stream);
-  return run_stream<FP4, GATED, RT16, 16, NW16, 2>(a, stream);
+template <bool GATED, int RT, int R, int NW>
+hipError_t run_fp4(const StreamArgs& a, hipStream_t stream) {
+  return run_stream<true, GATED, RT, R, NW, 2>(a, stream);
 }
 
 // A bf16 weight, read once, is loaded non-temporally (k = 4096, f = 14336: one
@@ -241,13 +240,32 @@ hipError_t run_bf16(const StreamArgs& a, hipStream_t stream) {
 
 }  // namespace
 
+// Row tiles and wavefronts of a workgroup by the number of (pairs of) row
+// tiles: as many wavefronts per tile as fit where each CU has one workgroup at
+// most, else fewer of them, so that two or three workgroups fit on a CU, and two
+// tiles to share an activation's loads.  Measured, us, the first form against
+// the one taken: linear n = 28672, k = 4096: 1 row 12.8, 11.2; 8 rows 20.9, 13.8;
+// 16 rows 25.3, 18.1;  n = 8192, k = 4096: 8 rows 12.3, 8.2 (n = 16384); 16 rows
+// 8.3, 6.3, 32 rows 15.0, 9.7;  n = 4096: 8 rows 4.0 against 4.9, 16 rows 4.7
+// against 5.7;  gated k = 4096, 16 rows: f = 4096 6.4 against 9.2, f = 8192 10.4, 10.0;
+// k = 704, f = 9248: 8.5, 5.4;  k = 4096, f = 4096, 64 rows: 19.4, 15.5.
 hipError_t launch_stream(const StreamArgs& a, hipStream_t stream) {
   if (!a.w_scale) return run_bf16(a, stream);
-  if (!a.gated) return run_rows<true, false, 1, 8, 1, 8, 1, 4>(a, stream);
-  // 64 weight rows share an activation's loads where their workgroups still
-  // cover 256 CUs (16 rows, k = 4096: f = 14336 17.0 against 20.8 us; f = 4096 8.2 against 6.4)
-  if (a.rows >= 8192) return run_rows<true, true, 2, 4, 2, 4, 4, 4>(a, stream);
-  return run_rows<true, true, 2, 4, 2, 4, 2, 4>(a, stream);
+  const int64_t tiles = a.rows / 16 * ((a.m + 15) / 16);
+  if (a.gated) {
+    if (a.m <= 2) return run_fp4<true, 2, 2, 4>(a, stream);
+    if (a.m <= 8) return run_fp4<true, 2, 8, 4>(a, stream);
+    if (tiles <= 256) return run_fp4<true, 2, 16, 4>(a, stream);
+    if (tiles <= 512) return run_fp4<true, 4, 16, 3>(a, stream);
+    if (tiles <= 768) return run_fp4<true, 2, 16, 2>(a, stream);
+    return run_fp4<true, 4, 16, 2>(a, stream);
+  }
+  if (a.m <= 2) return tiles <= 256 ? run_fp4<false, 1, 2, 8>(a, stream) : run_fp4<false, 1, 2, 4>(a, stream);
+  if (a.m <= 8) return tiles <= 256 ? run_fp4<false, 1, 8, 8>(a, stream) : run_fp4<false, 2, 8, 4>(a, stream);
+  if (tiles <= 256) return run_fp4<false, 1, 16, 4>(a, stream);
+  if (tiles <= 512) return run_fp4<false, 2, 16, 4>(a, stream);
+  if (tiles <= 1024) return run_fp4<false, 2, 16, 3>(a, stream);
+  return run_fp4<false, 2, 16, 2>(a, stream);
 }
 
 }  // namespace sfr

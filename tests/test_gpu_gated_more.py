@@ -57,7 +57,7 @@ def test_forward_tiles(sfr, m, k, f):
                                    (130, 4128, 4128), (130, 32, 32), (65, 4128, 4128), (1001, 288, 3104),
                                    (65, 4128, 6176), (385, 1056, 4128), (65, 8224, 2080), (130, 96, 48),
                                    (3000, 288, 4128), (2049, 288, 4128), (4097, 288, 4128), (130, 8224, 6176),
-                                   (385, 4128, 1056)])
+                                   (385, 4128, 1056), (4097, 8224, 32)])
 def test_mxfp4_linear_tiles(sfr, m, k, n):
     x, w = inputs(m + n, m, k, n)
     q = sfr.quantize_mx(w, FP4)
@@ -87,6 +87,22 @@ def test_backward_tiles(sfr, m, k, f):
         rx, bx, rw, bw = gated_grad64(dh.double(), xd, gd[:, :f], gd[:, f:], w.double(), "silu")
         check(dx, rx, bx, "dx")
         check(dw, rw, bw, "dw")
+
+
+# The streamed 4-bit forms: up to 2, 8, 16 rows and more passes, each with few
+# and many tiles of 16 weight rows (n / 16 an odd number of them, too).
+@pytest.mark.parametrize("m,k,n", [(1, 96, 4112), (2, 1056, 8224), (5, 96, 4112), (8, 544, 16), (16, 1056, 4112),
+                                   (9, 1056, 8208), (16, 1056, 16400), (27, 2080, 4112), (48, 4128, 8208), (100, 32, 32)])
+def test_mxfp4_streamed(sfr, m, k, n):
+    x, w = inputs(m + n, m, k, n)
+    q = sfr.quantize_mx(w, FP4)
+    ref, e = products64(x.double(), mx_values(q))
+    check(sfr.mxfp4_linear(x, q, out_dtype=torch.float32), ref, e, "out")
+    f = (n + 31) // 32 * 32
+    x, w = inputs(m + f, m, k, 2 * f)
+    q = sfr.quantize_mx(w, FP4)
+    h, bound, _ = gated64(x.double(), mx_values(q), "relu")
+    check(sfr.mxfp4_gated_linear(x, q, "relu"), h, bound, "h")
 
 
 def padded(rows, cols, dtype, fill, before=3, after=5):
