@@ -42,7 +42,7 @@ struct GradParams {
 };
 
 // dgu[m] = [dh u act'(g) | dh act(g)] from the saved g and u: one pass, memory
-// bound (per f: 2 bytes of dh, two saved values, 4 bytes written; 6.3 TB/s at m =
+// bound (per f: 2 bytes of dh, two saved values, 4 bytes written; 6.1 TB/s at m =
 // 8192, f = 14336).  A lane holds 8 f.  The gradients are formed in binary32
 // and rounded once to bf16, the type in which the two products read them.  An
 // 8-bit x is decoded by the same threads first (a launch of its own cost the

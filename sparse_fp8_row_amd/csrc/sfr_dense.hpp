@@ -518,7 +518,9 @@ __device__ __forceinline__ void plain_epilogue(v4f (&acc)[4][FM], const PlainOut
 // Slice and tile of workgroup `id` of 8 * ceil(slices * T / 8): XCD id % 8 (each
 // has its own L2) owns a contiguous run of them, slice by slice, the tiles of a
 // slice in groups of `group` n tiles.  False past the last.  (32-bit: the
-// launchers bound slices * T by 2^23.)
+// launchers bound slices * T by 2^23.)  With every slice over all XCDs, each of
+// which then reads most of both operands: dx of m = 73, k = 1408, f = 11584 42.8
+// us against 21.3.
 __device__ __forceinline__ bool tile_of(uint32_t id, uint32_t slices, uint32_t tiles_m, uint32_t tiles_n,
                                         uint32_t group, uint32_t& slice, int64_t& tm, int64_t& tn) {
   const uint32_t T = tiles_m * tiles_n, items = slices * T, per = (items + 7) / 8;
