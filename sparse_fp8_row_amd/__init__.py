@@ -482,9 +482,15 @@ def bsr_linear(x: torch.Tensor, w: BsrWeight, bias: Optional[torch.Tensor] = Non
 # --------------------------------------------------------------------------
 MX_BLOCK = 32
 SFR_ACT = {"silu": 0, "gelu_tanh": 1, "relu": 2}
-_BF16, _E2M1, _E8M0 = torch.bfloat16, torch.float4_e2m1fn_x2, torch.float8_e8m0fnu
-_MX = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1, _E2M1: 2}
-_SAVE = {torch.bfloat16: 1, torch.float8_e4m3fn: 2, torch.float8_e5m2: 3}
+_BF16 = torch.bfloat16
+# None on a torch without these types: the MX formats (scales are E8M0 bytes),
+# or their 4-bit form, are then refused as unsupported element types, and
+# everything else works.
+_E2M1, _E8M0 = getattr(torch, "float4_e2m1fn_x2", None), getattr(torch, "float8_e8m0fnu", None)
+_MX = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1} if _E8M0 is not None else {}
+_SAVE = {_BF16: 1, **{t: e + 2 for t, e in _MX.items()}}
+if _MX and _E2M1 is not None:
+    _MX[_E2M1] = 2
 
 
 @dataclass
@@ -740,7 +746,7 @@ def gated_linear_backward(dh: torch.Tensor, w: torch.Tensor, saved: GatedCheckpo
     return dx, dw
 
 
-_FP4 = (_E2M1,)
+_FP4 = tuple(t for t, e in _MX.items() if e == 2)
 
 
 @functools.lru_cache(maxsize=4096)
