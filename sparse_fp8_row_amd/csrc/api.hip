@@ -285,7 +285,7 @@ sfr_status gated_linear_bf16_backward(const uint16_t* dh, int64_t m, int64_t k, 
 
 int64_t sfr_mxfp4_workspace_bytes(int64_t m, int64_t n, int64_t k) {
   if (m <= 0 || m > SFR_MAX_DIM || !block_dim(n, 16) || !block_dim(k, 32) || !dense_ok(m, n)) return 0;
-  return sfr::mxfp4_workspace_bytes(m, n, k, false);
+  return sfr::mxfp4_workspace_bytes(m, n, k);
 }
 
 sfr_status mxfp4_linear(const uint16_t* x, int64_t m, int64_t k, const uint8_t* wq, const uint8_t* ws, int64_t n,
@@ -295,7 +295,7 @@ sfr_status mxfp4_linear(const uint16_t* x, int64_t m, int64_t k, const uint8_t* 
   if (m < 0 || m > SFR_MAX_DIM || (n != 0 && !block_dim(n, 16)) || !block_dim(k, 32) || !dense_ok(m, n))
     return SFR_ERR_SHAPE;
   if (m == 0 || n == 0) return SFR_OK;
-  const int64_t need = sfr::mxfp4_workspace_bytes(m, n, k, false);
+  const int64_t need = sfr::mxfp4_workspace_bytes(m, n, k);
   if (workspace_bytes < need) return SFR_ERR_SHAPE;
   if (!x || !wq || !ws || !out || (need > 0 && !workspace)) return SFR_ERR_NULL;
   if (!aligned16(x) || !aligned16(wq) || !aligned16(ws) || !aligned16(out) || (bias && !aligned16(bias)) ||

@@ -145,8 +145,8 @@ hipError_t launch_gated_backward(const GatedBackwardArgs& a, void* workspace, hi
   return e;
 }
 
-int64_t mxfp4_workspace_bytes(int64_t m, int64_t n, int64_t k, bool gated) {
-  return gated || stream_rows(m, n, k, true, false) ? 0 : align256(dense_nt_workspace_bytes(m, n, k));
+int64_t mxfp4_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  return stream_rows(m, n, k, true, false) ? 0 : align256(dense_nt_workspace_bytes(m, n, k));
 }
 
 hipError_t launch_mxfp4(const StreamArgs& a, void* workspace, hipStream_t stream) {

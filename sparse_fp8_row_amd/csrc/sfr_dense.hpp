@@ -303,28 +303,24 @@ struct Reader {
       }
     }
   }
-  // The same of two tiles, `apart` bytes apart, in one block.
+  // COLS: the same of two tiles, `apart` bytes apart, in one block.
   __device__ __forceinline__ void read2(v8bf (&o0)[2][NF], v8bf (&o1)[2][NF], const uint8_t* tile, int apart) const {
-    if constexpr (L == ROWS) {
-      read(o0, tile);
-      read(o1, tile + apart);
-    } else {
-      const uint32_t base = (uint32_t)(uintptr_t)(lds_void_t)tile;
-      uint32_t a[2 * NF];
-      v2u r[2 * NF][4];
+    static_assert(L == COLS, "transposing reads");
+    const uint32_t base = (uint32_t)(uintptr_t)(lds_void_t)tile;
+    uint32_t a[2 * NF];
+    v2u r[2 * NF][4];
 #pragma unroll
-      for (int i = 0; i < NF; ++i) {
-        a[i] = base + at[i];
-        a[NF + i] = a[i] + apart;
-      }
-      read_tr<2 * NF, 0, HI, KK, KK + HI>(r, a);
+    for (int i = 0; i < NF; ++i) {
+      a[i] = base + at[i];
+      a[NF + i] = a[i] + apart;
+    }
+    read_tr<2 * NF, 0, HI, KK, KK + HI>(r, a);
 #pragma unroll
-      for (int i = 0; i < NF; ++i) {
-        o0[0][i] = join8(r[i][0], r[i][1]);
-        o0[1][i] = join8(r[i][2], r[i][3]);
-        o1[0][i] = join8(r[NF + i][0], r[NF + i][1]);
-        o1[1][i] = join8(r[NF + i][2], r[NF + i][3]);
-      }
+    for (int i = 0; i < NF; ++i) {
+      o0[0][i] = join8(r[i][0], r[i][1]);
+      o0[1][i] = join8(r[i][2], r[i][3]);
+      o1[0][i] = join8(r[NF + i][0], r[NF + i][1]);
+      o1[1][i] = join8(r[NF + i][2], r[NF + i][3]);
     }
   }
 };

@@ -141,7 +141,7 @@ double dense_us(int64_t m, int64_t n, int64_t k, bool fp4, bool gated);
 // The matrix-core form of the 4-bit linear layer (not gated), any m.
 int64_t dense_nt_workspace_bytes(int64_t m, int64_t n, int64_t k);
 hipError_t launch_mxfp4_dense(const StreamArgs& a, void* workspace, hipStream_t stream);
-int64_t mxfp4_workspace_bytes(int64_t m, int64_t n, int64_t k, bool gated);
+int64_t mxfp4_workspace_bytes(int64_t m, int64_t n, int64_t k);  // of the linear layer; the gated block needs none
 hipError_t launch_mxfp4(const StreamArgs& a, void* workspace, hipStream_t stream);
 
 }  // namespace sfr
