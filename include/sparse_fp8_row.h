@@ -526,6 +526,25 @@ sfr_status mxfp4_gated_linear(const uint16_t* x, int64_t m, int64_t k, const uin
 /* Workspace bytes of mxfp4_linear; 0 for sizes it rejects. */
 int64_t sfr_mxfp4_workspace_bytes(int64_t m, int64_t n, int64_t k);
 
+/* The matrix products of the calls above, by what decides their kernel: the
+ * forward pass without and with a checkpoint, dx, dw, and the two 4-bit calls. */
+typedef enum {
+    SFR_PRODUCT_GATED = 0,
+    SFR_PRODUCT_GATED_SAVING = 1,
+    SFR_PRODUCT_DX = 2,
+    SFR_PRODUCT_DW = 3,
+    SFR_PRODUCT_MXFP4 = 4,
+    SFR_PRODUCT_MXFP4_GATED = 5
+} sfr_product_t;
+
+/*
+ * sfr_block_kernel -- name of the kernel that a product takes (a static string;
+ * for profiles and tests), NULL for sizes its call rejects and for a call
+ * without rows.  f: n for SFR_PRODUCT_MXFP4.  slices (may be NULL) receives the
+ * number of slices of its sum, 1 for an unsliced one.
+ */
+const char* sfr_block_kernel(sfr_product_t product, int64_t m, int64_t k, int64_t f, int32_t* slices);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* sfr_status_string(sfr_status s);
 

@@ -48,7 +48,8 @@ EXPORTED = ("quantize_rowwise_fp8", "quantize_tensorwise_fp8", "sfr_quantize_ten
             "sfr_linear_algo_name", "sfr_linear_algo_supported", "sfr_linear_default_algo",
             "bsr_count_bf16", "bsr_fill_bf16", "bsr_linear_bf16", "sfr_status_string", "sfr_format_version",
             "quantize_mx", "dequantize_mx", "gated_linear_bf16", "gated_linear_bf16_backward",
-            "sfr_gated_backward_workspace_bytes", "mxfp4_linear", "mxfp4_gated_linear", "sfr_mxfp4_workspace_bytes")
+            "sfr_gated_backward_workspace_bytes", "mxfp4_linear", "mxfp4_gated_linear", "sfr_mxfp4_workspace_bytes",
+            "sfr_block_kernel")
 
 _FP8 = {torch.float8_e4m3fn: SFR_E4M3, torch.float8_e5m2: SFR_E5M2}
 _lib = None
@@ -104,6 +105,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sfr_gated_backward_workspace_bytes.restype = I64
     lib.sfr_mxfp4_workspace_bytes.argtypes = [I64, I64, I64]
     lib.sfr_mxfp4_workspace_bytes.restype = I64
+    lib.sfr_block_kernel.argtypes = [I, I64, I64, I64, ctypes.POINTER(ctypes.c_int32)]
+    lib.sfr_block_kernel.restype = ctypes.c_char_p
     for fn in (lib.quantize_mx, lib.dequantize_mx, lib.gated_linear_bf16, lib.gated_linear_bf16_backward,
                lib.mxfp4_linear, lib.mxfp4_gated_linear):
         fn.restype = I
@@ -808,3 +811,18 @@ def mxfp4_gated_linear(x: torch.Tensor, w: MxTensor, activation: str = "silu", o
     _check(load().mxfp4_gated_linear(px, m, k, pq, ps, n // 2, act, out.data_ptr(), _raw_stream(device)),
            "mxfp4_gated_linear")
     return out
+
+
+_PRODUCTS = {"gated": 0, "gated_saving": 1, "dx": 2, "dw": 3, "mxfp4": 4, "mxfp4_gated": 5}
+
+
+def block_kernel(product: str, m: int, k: int, f: int):
+    """(name, slices of the sum) of the kernel that a product of the block takes:
+    "gated" (gated_linear), "gated_saving" (gated_linear_checkpointed), "dx" and
+    "dw" (gated_linear_backward), "mxfp4_gated", or "mxfp4" (mxfp4_linear, f its
+    n).  None for sizes that the call rejects and for a call without rows."""
+    if product not in _PRODUCTS:
+        raise ValueError(f"product must be one of {sorted(_PRODUCTS)}")
+    slices = ctypes.c_int32()
+    name = load().sfr_block_kernel(_PRODUCTS[product], m, k, f, ctypes.byref(slices))
+    return None if name is None else (name.decode(), slices.value)

@@ -317,6 +317,20 @@ sfr_status mxfp4_gated_linear(const uint16_t* x, int64_t m, int64_t k, const uin
   return launch_status(sfr::launch_mxfp4(a, nullptr, static_cast<hipStream_t>(stream)));
 }
 
+const char* sfr_block_kernel(sfr_product_t product, int64_t m, int64_t k, int64_t f, int32_t* slices) {
+  static_assert((int)SFR_PRODUCT_GATED == sfr::PRODUCT_GATED &&
+                    (int)SFR_PRODUCT_MXFP4_GATED == sfr::PRODUCT_MXFP4_GATED,
+                "the same numbers");
+  if (product < SFR_PRODUCT_GATED || product > SFR_PRODUCT_MXFP4_GATED || m <= 0 || m > SFR_MAX_DIM) return nullptr;
+  if (product == SFR_PRODUCT_MXFP4       ? !block_dim(f, 16) || !block_dim(k, 32) || !dense_ok(m, f)
+      : product == SFR_PRODUCT_MXFP4_GATED ? !gated_dim(f) || !block_dim(k, 32) || !dense_ok(m, 2 * f)
+                                         : !gated_shape(m, k, f))
+    return nullptr;
+  const sfr::DenseKernel c = sfr::block_kernel((int)product, m, k, f);
+  if (slices) *slices = c.slices;
+  return c.name;
+}
+
 const char* sfr_status_string(sfr_status s) {
   switch (s) {
     case SFR_OK: return "ok";

@@ -476,16 +476,21 @@ enum {
   CFG_COUNT
 };
 struct Config {
+  const char* name;
   int bn, bm, per_cu;
   bool rows_x;  // built for X by rows only
   double one, all, full, lasting, fixed, cols;
 };
 constexpr Config kConfigs[CFG_COUNT] = {
-    {256, 256, 1, false, 0.95, 1.37, 1.37, 1.66, 5.6, 1.0}, {256, 192, 1, true, 0.80, 1.06, 1.06, 1.34, 5.0, 1.06},
-    {384, 192, 1, true, 1.16, 1.60, 1.60, 2.06, 7.0, 1.04}, {128, 128, 2, false, 0.58, 0.76, 1.05, 1.05, 3.7, 1.0},
-    {128, 64, 2, false, 0.45, 0.51, 0.67, 0.67, 3.8, 1.0},  {64, 64, 3, false, 0.36, 0.40, 0.59, 0.59, 3.0, 1.0},
-    {128, 128, 1, true, 0.45, 0.58, 0.58, 0.58, 4.0, 1.0},  {128, 64, 1, true, 0.30, 0.34, 0.34, 0.34, 4.0, 1.0},
-    {64, 64, 2, true, 0.23, 0.32, 0.42, 0.42, 3.0, 1.0}};
+    {"wide_256x256", 256, 256, 1, false, 0.95, 1.37, 1.37, 1.66, 5.6, 1.0},
+    {"wide_256x192", 256, 192, 1, true, 0.80, 1.06, 1.06, 1.34, 5.0, 1.06},
+    {"wide_384x192", 384, 192, 1, true, 1.16, 1.60, 1.60, 2.06, 7.0, 1.04},
+    {"tile_128x128", 128, 128, 2, false, 0.58, 0.76, 1.05, 1.05, 3.7, 1.0},
+    {"tile_128x64", 128, 64, 2, false, 0.45, 0.51, 0.67, 0.67, 3.8, 1.0},
+    {"tile_64x64", 64, 64, 3, false, 0.36, 0.40, 0.59, 0.59, 3.0, 1.0},
+    {"tile_128x128_k2", 128, 128, 1, true, 0.45, 0.58, 0.58, 0.58, 4.0, 1.0},
+    {"tile_128x64_k2", 128, 64, 1, true, 0.30, 0.34, 0.34, 0.34, 4.0, 1.0},
+    {"tile_64x64_k2", 64, 64, 2, true, 0.23, 0.32, 0.42, 0.42, 3.0, 1.0}};
 struct Choice {
   int config, slices;
   int64_t k_per_split;
@@ -569,20 +574,30 @@ hipError_t run_dense(DenseParams p, const Choice& c, void* workspace, hipStream_
   return hipGetLastError();
 }
 
-int64_t slice_bytes(int64_t m, int64_t n, int64_t k, int lw) {
-  const Choice c = choose(m, n, k, ROWS, lw, true);
-  return c.slices > 1 ? c.slices * m * n * 4 : 0;
-}
+// The choice of each product, for its launch, its workspace and its name.
+Choice choose_gated(int64_t m, int64_t k, int64_t f) { return choose(m, 2 * f, k, ROWS, ROWS, false); }
+Choice choose_mxfp4(int64_t m, int64_t n, int64_t k) { return choose(m, n, k, ROWS, CODES, true); }
+Choice choose_dx(int64_t m, int64_t k, int64_t f2) { return choose(m, k, f2, ROWS, COLS, true); }
+Choice choose_dw(int64_t m, int64_t k, int64_t f2) { return choose(f2, k, m, COLS, COLS, false); }
+
+int64_t slice_bytes(const Choice& c, int64_t m, int64_t n) { return c.slices > 1 ? c.slices * m * n * 4 : 0; }
+
+DenseKernel named(const Choice& c) { return {kConfigs[c.config].name, c.slices}; }
 
 }  // namespace
+
+DenseKernel dense_gated_kernel(int64_t m, int64_t k, int64_t f) { return named(choose_gated(m, k, f)); }
+DenseKernel dense_mxfp4_kernel(int64_t m, int64_t n, int64_t k) { return named(choose_mxfp4(m, n, k)); }
+DenseKernel dense_dx_kernel(int64_t m, int64_t k, int64_t f2) { return named(choose_dx(m, k, f2)); }
+DenseKernel dense_dw_kernel(int64_t m, int64_t k, int64_t f2) { return named(choose_dw(m, k, f2)); }
 
 double dense_us(int64_t m, int64_t n, int64_t k, bool fp4, bool gated) {
   return choose(m, n, k, ROWS, fp4 ? CODES : ROWS, !gated).us;
 }
 
 // Workspace: the slices' partial sums.
-int64_t dense_nt_workspace_bytes(int64_t m, int64_t n, int64_t k) { return slice_bytes(m, n, k, CODES); }
-int64_t dense_dx_workspace_bytes(int64_t m, int64_t k, int64_t f2) { return slice_bytes(m, k, f2, COLS); }
+int64_t dense_nt_workspace_bytes(int64_t m, int64_t n, int64_t k) { return slice_bytes(choose_mxfp4(m, n, k), m, n); }
+int64_t dense_dx_workspace_bytes(int64_t m, int64_t k, int64_t f2) { return slice_bytes(choose_dx(m, k, f2), m, k); }
 
 hipError_t launch_gated_dense(const GatedArgs& a, hipStream_t stream) {
   DenseParams p{};
@@ -594,7 +609,7 @@ hipError_t launch_gated_dense(const GatedArgs& a, hipStream_t stream) {
   p.rows_n = a.f;
   p.k = a.k;
   p.gated = GatedOut{a.h, a.gu, a.gu_scale, a.m, a.f, a.act, a.gu_fmt};
-  const Choice c = choose(a.m, 2 * a.f, a.k, ROWS, ROWS, false);
+  const Choice c = choose_gated(a.m, a.k, a.f);
   return a.w_scale ? run_dense<ROWS, CODES, EPI_GATED>(p, c, nullptr, stream)
                    : run_dense<ROWS, ROWS, EPI_GATED>(p, c, nullptr, stream);
 }
@@ -609,7 +624,7 @@ hipError_t launch_mxfp4_dense(const StreamArgs& a, void* workspace, hipStream_t 
   p.rows_n = a.rows;
   p.k = a.k;
   p.plain = PlainOut{a.out, a.bias, a.m, a.rows, a.out_fmt};
-  return run_dense<ROWS, CODES, EPI_PLAIN>(p, choose(a.m, a.rows, a.k, ROWS, CODES, true), workspace, stream);
+  return run_dense<ROWS, CODES, EPI_PLAIN>(p, choose_mxfp4(a.m, a.rows, a.k), workspace, stream);
 }
 
 hipError_t launch_dense_dx(const uint16_t* dgu, const uint16_t* w, int64_t m, int64_t k, int64_t f2, uint16_t* dx,
@@ -623,7 +638,7 @@ hipError_t launch_dense_dx(const uint16_t* dgu, const uint16_t* w, int64_t m, in
   p.rows_n = k;
   p.k = f2;
   p.plain = PlainOut{dx, nullptr, m, k, OUT_BF16};
-  return run_dense<ROWS, COLS, EPI_PLAIN>(p, choose(m, k, f2, ROWS, COLS, true), workspace, stream);
+  return run_dense<ROWS, COLS, EPI_PLAIN>(p, choose_dx(m, k, f2), workspace, stream);
 }
 
 hipError_t launch_dense_dw(const uint16_t* dgu, const uint16_t* x, int64_t m, int64_t k, int64_t f2, uint16_t* dw,
@@ -637,7 +652,7 @@ hipError_t launch_dense_dw(const uint16_t* dgu, const uint16_t* x, int64_t m, in
   p.rows_n = k;
   p.k = m;
   p.plain = PlainOut{dw, nullptr, f2, k, OUT_BF16};
-  return run_dense<COLS, COLS, EPI_PLAIN>(p, choose(f2, k, m, COLS, COLS, false), nullptr, stream);
+  return run_dense<COLS, COLS, EPI_PLAIN>(p, choose_dw(m, k, f2), nullptr, stream);
 }
 
 }  // namespace sfr

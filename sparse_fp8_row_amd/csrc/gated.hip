@@ -165,4 +165,21 @@ hipError_t launch_mxfp4(const StreamArgs& a, void* workspace, hipStream_t stream
   return launch_gated_dense(g, stream);
 }
 
+DenseKernel block_kernel(int product, int64_t m, int64_t k, int64_t f) {
+  if (product == PRODUCT_GATED_SAVING) return dense_gated_kernel(m, k, f);
+  if (product == PRODUCT_DX) return dense_dx_kernel(m, k, 2 * f);
+  if (product == PRODUCT_DW) return dense_dw_kernel(m, k, 2 * f);
+  const bool fp4 = product != PRODUCT_GATED, gated = product != PRODUCT_MXFP4;
+  if (!stream_rows(m, gated ? 2 * f : f, k, fp4, gated))
+    return gated ? dense_gated_kernel(m, k, f) : dense_mxfp4_kernel(m, f, k);
+  static const uint8_t some = 0;  // w_scale: tells a 4-bit weight from a bf16 one, not read
+  StreamArgs a{};
+  a.w_scale = fp4 ? &some : nullptr;
+  a.m = m;
+  a.k = k;
+  a.rows = f;
+  a.gated = gated;
+  return {stream_name(a), 1};
+}
+
 }  // namespace sfr

@@ -136,11 +136,26 @@ struct StreamArgs {
 };
 bool stream_rows(int64_t m, int64_t n, int64_t k, bool fp4, bool gated);  // n: weight rows (2 f when gated)
 hipError_t launch_stream(const StreamArgs& a, hipStream_t stream);
+const char* stream_name(const StreamArgs& a);  // of the form that launch_stream takes
 // Modelled time of the matrix-core form, us.
 double dense_us(int64_t m, int64_t n, int64_t k, bool fp4, bool gated);
 // The matrix-core form of the 4-bit linear layer (not gated), any m.
 int64_t dense_nt_workspace_bytes(int64_t m, int64_t n, int64_t k);
 hipError_t launch_mxfp4_dense(const StreamArgs& a, void* workspace, hipStream_t stream);
+
+// The matrix-core kernel that a product takes: its name and the slices of its sum.
+struct DenseKernel {
+  const char* name;
+  int slices;
+};
+DenseKernel dense_gated_kernel(int64_t m, int64_t k, int64_t f);
+DenseKernel dense_mxfp4_kernel(int64_t m, int64_t n, int64_t k);
+DenseKernel dense_dx_kernel(int64_t m, int64_t k, int64_t f2);
+DenseKernel dense_dw_kernel(int64_t m, int64_t k, int64_t f2);
+// The same of any product of the block, streamed forms among them (f: n for PRODUCT_MXFP4).
+enum { PRODUCT_GATED = 0, PRODUCT_GATED_SAVING, PRODUCT_DX, PRODUCT_DW, PRODUCT_MXFP4, PRODUCT_MXFP4_GATED };
+DenseKernel block_kernel(int product, int64_t m, int64_t k, int64_t f);
+
 int64_t mxfp4_workspace_bytes(int64_t m, int64_t n, int64_t k);  // of the linear layer; the gated block needs none
 hipError_t launch_mxfp4(const StreamArgs& a, void* workspace, hipStream_t stream);
 

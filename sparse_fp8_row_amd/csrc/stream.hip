@@ -218,54 +218,71 @@ bool stream_rows(int64_t m, int64_t n, int64_t k, bool fp4, bool gated) {
 
 namespace {
 
+// One form of the kernel, with its name.
+struct Form {
+  const char* name;
+  hipError_t (*run)(const StreamArgs&, hipStream_t);
+};
+
+// Two buffers everywhere: more workgroups on a CU gain more than deeper ones.
+constexpr Form kBf16R2{"stream_bf16_r2", run_stream<false, true, 2, 2, 3, 2, true>};
+constexpr Form kBf16R8{"stream_bf16_r8", run_stream<false, true, 2, 8, 3, 2, true>};
+constexpr Form kBf16R16{"stream_bf16_r16", run_stream<false, true, 2, 16, 3, 2, true>};
+constexpr Form kBf16Passes{"stream_bf16_passes", run_stream<false, true, 2, 16, 3, 2>};
+constexpr Form kGatedR2{"stream_4bit_gated_r2", run_stream<true, true, 2, 2, 4, 2>};
+constexpr Form kGatedR8{"stream_4bit_gated_r8", run_stream<true, true, 2, 8, 4, 2>};
+constexpr Form kGatedT2W4{"stream_4bit_gated_t2w4", run_stream<true, true, 2, 16, 4, 2>};
+constexpr Form kGatedT4W3{"stream_4bit_gated_t4w3", run_stream<true, true, 4, 16, 3, 2>};
+constexpr Form kGatedT2W2{"stream_4bit_gated_t2w2", run_stream<true, true, 2, 16, 2, 2>};
+constexpr Form kGatedT4W2{"stream_4bit_gated_t4w2", run_stream<true, true, 4, 16, 2, 2>};
+constexpr Form kR2T1W8{"stream_4bit_r2_t1w8", run_stream<true, false, 1, 2, 8, 2>};
+constexpr Form kR2T1W4{"stream_4bit_r2_t1w4", run_stream<true, false, 1, 2, 4, 2>};
+constexpr Form kR8T1W8{"stream_4bit_r8_t1w8", run_stream<true, false, 1, 8, 8, 2>};
+constexpr Form kR8T2W4{"stream_4bit_r8_t2w4", run_stream<true, false, 2, 8, 4, 2>};
+constexpr Form kT1W4{"stream_4bit_t1w4", run_stream<true, false, 1, 16, 4, 2>};
+constexpr Form kT2W4{"stream_4bit_t2w4", run_stream<true, false, 2, 16, 4, 2>};
+constexpr Form kT2W3{"stream_4bit_t2w3", run_stream<true, false, 2, 16, 3, 2>};
+constexpr Form kT2W2{"stream_4bit_t2w2", run_stream<true, false, 2, 16, 2, 2>};
+
+// The form of a call.
+//
 // R by the rows of a workgroup: the activation's share of LDS and its loads
 // grow with R, so 2 and 8 rows have forms of their own (n = 4096, k = 4096,
-// 4-bit: 3.3, 3.9, 4.7 us for 1, 8, 16 rows; 8 rows in the 16-row form 4.6).  Two
-// buffers everywhere: more workgroups on a CU gain more than deeper ones.
-template <bool GATED, int RT, int R, int NW>
-hipError_t run_fp4(const StreamArgs& a, hipStream_t stream) {
-  return run_stream<true, GATED, RT, R, NW, 2>(a, stream);
-}
-
+// 4-bit: 3.3, 3.9, 4.7 us for 1, 8, 16 rows; 8 rows in the 16-row form 4.6).
+//
 // A bf16 weight, read once, is loaded non-temporally (k = 4096, f = 14336: one
 // row 41.5 -> 38.3 us, 16 rows 44.4 -> 39.6; with more rows later passes find
 // it in the caches).  A 4-bit weight is not: 16 rows 16.9 -> 18.8 us where the
 // caches hold it, 20.6 -> 20.1 where they do not.
-hipError_t run_bf16(const StreamArgs& a, hipStream_t stream) {
-  if (a.m <= 2) return run_stream<false, true, 2, 2, 3, 2, true>(a, stream);
-  if (a.m <= 8) return run_stream<false, true, 2, 8, 3, 2, true>(a, stream);
-  if (a.m <= 16) return run_stream<false, true, 2, 16, 3, 2, true>(a, stream);
-  return run_stream<false, true, 2, 16, 3, 2>(a, stream);
+//
+// Row tiles and wavefronts of a workgroup for a 4-bit weight by the number of
+// (pairs of) row tiles: as many wavefronts per tile as fit where each CU has one
+// workgroup at most, else fewer of them, so that two or three workgroups fit on
+// a CU, and two tiles to share an activation's loads.  (The gated forms of up
+// to 8 rows and the bf16 forms are one for every number of tiles: they were
+// timed at k = 4096, f = 14336 alone.)  Measured, us, the first form against the
+// one taken: linear n = 28672, k = 4096: 1 row 12.8, 11.2; 8 rows 20.9, 13.8; 16
+// rows 25.3, 18.1;  n = 8192, k = 4096: 8 rows 12.3, 8.2 (n = 16384); 16 rows
+// 8.3, 6.3, 32 rows 15.0, 9.7;  n = 4096: 8 rows 4.0 against 4.9, 16 rows 4.7
+// against 5.7;  gated k = 4096, 16 rows: f = 4096 6.4 against 9.2, f = 8192 10.4, 10.0;
+// k = 704, f = 9248: 8.5, 5.4;  k = 4096, f = 4096, 64 rows: 19.4, 15.5.
+const Form& stream_form(const StreamArgs& a) {
+  if (!a.w_scale) return a.m <= 2 ? kBf16R2 : a.m <= 8 ? kBf16R8 : a.m <= 16 ? kBf16R16 : kBf16Passes;
+  const int64_t tiles = a.rows / 16 * ((a.m + 15) / 16);
+  if (a.gated) {
+    if (a.m <= 2) return kGatedR2;
+    if (a.m <= 8) return kGatedR8;
+    return tiles <= 256 ? kGatedT2W4 : tiles <= 512 ? kGatedT4W3 : tiles <= 768 ? kGatedT2W2 : kGatedT4W2;
+  }
+  if (a.m <= 2) return tiles <= 256 ? kR2T1W8 : kR2T1W4;
+  if (a.m <= 8) return tiles <= 256 ? kR8T1W8 : kR8T2W4;
+  return tiles <= 256 ? kT1W4 : tiles <= 512 ? kT2W4 : tiles <= 1024 ? kT2W3 : kT2W2;
 }
 
 }  // namespace
 
-// Row tiles and wavefronts of a workgroup by the number of (pairs of) row
-// tiles: as many wavefronts per tile as fit where each CU has one workgroup at
-// most, else fewer of them, so that two or three workgroups fit on a CU, and two
-// tiles to share an activation's loads.  Measured, us, the first form against
-// the one taken: linear n = 28672, k = 4096: 1 row 12.8, 11.2; 8 rows 20.9, 13.8;
-// 16 rows 25.3, 18.1;  n = 8192, k = 4096: 8 rows 12.3, 8.2 (n = 16384); 16 rows
-// 8.3, 6.3, 32 rows 15.0, 9.7;  n = 4096: 8 rows 4.0 against 4.9, 16 rows 4.7
-// against 5.7;  gated k = 4096, 16 rows: f = 4096 6.4 against 9.2, f = 8192 10.4, 10.0;
-// k = 704, f = 9248: 8.5, 5.4;  k = 4096, f = 4096, 64 rows: 19.4, 15.5.
-hipError_t launch_stream(const StreamArgs& a, hipStream_t stream) {
-  if (!a.w_scale) return run_bf16(a, stream);
-  const int64_t tiles = a.rows / 16 * ((a.m + 15) / 16);
-  if (a.gated) {
-    if (a.m <= 2) return run_fp4<true, 2, 2, 4>(a, stream);
-    if (a.m <= 8) return run_fp4<true, 2, 8, 4>(a, stream);
-    if (tiles <= 256) return run_fp4<true, 2, 16, 4>(a, stream);
-    if (tiles <= 512) return run_fp4<true, 4, 16, 3>(a, stream);
-    if (tiles <= 768) return run_fp4<true, 2, 16, 2>(a, stream);
-    return run_fp4<true, 4, 16, 2>(a, stream);
-  }
-  if (a.m <= 2) return tiles <= 256 ? run_fp4<false, 1, 2, 8>(a, stream) : run_fp4<false, 1, 2, 4>(a, stream);
-  if (a.m <= 8) return tiles <= 256 ? run_fp4<false, 1, 8, 8>(a, stream) : run_fp4<false, 2, 8, 4>(a, stream);
-  if (tiles <= 256) return run_fp4<false, 1, 16, 4>(a, stream);
-  if (tiles <= 512) return run_fp4<false, 2, 16, 4>(a, stream);
-  if (tiles <= 1024) return run_fp4<false, 2, 16, 3>(a, stream);
-  return run_fp4<false, 2, 16, 2>(a, stream);
-}
+const char* stream_name(const StreamArgs& a) { return stream_form(a).name; }
+
+hipError_t launch_stream(const StreamArgs& a, hipStream_t stream) { return stream_form(a).run(a, stream); }
 
 }  // namespace sfr

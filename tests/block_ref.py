@@ -143,3 +143,11 @@ def inputs(seed, m, k, rows, device="cuda", scale=0.05):
     x = torch.randn(m, k, generator=g).bfloat16()
     w = (scale * torch.randn(rows, k, generator=g)).bfloat16()
     return x.to(device), w.to(device)
+
+
+def shapes_of(test):
+    """The sizes that a test is parametrized over."""
+    for mark in test.pytestmark:
+        if mark.name == "parametrize" and mark.args[0].startswith("m,k,"):
+            return list(mark.args[1])
+    raise AssertionError(f"{test.__name__} has no sizes")
