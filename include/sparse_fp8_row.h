@@ -446,6 +446,11 @@ typedef enum { SFR_SAVE_NONE = 0, SFR_SAVE_BF16 = 1, SFR_SAVE_E4M3 = 2, SFR_SAVE
  * A block with a NaN or an infinity gets scale 255 and zero codes.
  * dequantize_mx writes q * 2^e, exactly (every such value is a bf16 number),
  * and NaN for a block of scale 255.  Deterministic, bit-exact.
+ * Blocks from elsewhere may have any scale byte s and element code: one stands
+ * for q * 2^(s - 127), rounded to the nearest bf16 number, ties to even (inexact
+ * only for e4m3 elements below s = 3 and e5m2 elements below s = 10, which reach
+ * under bf16's smallest step; infinite from 2^128 on), NaN and infinity codes
+ * for themselves.  Every call that reads MX blocks takes them so.
  *
  *   x, out  [rows, cols] bf16 bits.
  *   q       [rows, cols] bytes, or [rows, cols / 2] for SFR_MX_E2M1.
@@ -505,8 +510,9 @@ int64_t sfr_gated_backward_workspace_bytes(int64_t m, int64_t k, int64_t f, sfr_
  * mxfp4_linear -- the linear layer for a 4-bit weight with one scale per 32
  * values, as quantize_mx(SFR_MX_E2M1) writes it:
  *     out[m, n] = sum_k x[m, k] wq[n, k] (+ bias[n])
- * The weight's values are exact in bf16; sums are binary32, rounded once to
- * bf16 or returned in binary32.
+ * The weight's values are exact in bf16 (those of 2^128 and more, scale bytes
+ * 253 and 254, are infinities); sums are binary32, rounded once to bf16 or
+ * returned in binary32.
  * mxfp4_gated_linear -- the gated block for such a weight [2 f, k]; h bf16.
  *
  *   x   [m, k] bf16 bits.

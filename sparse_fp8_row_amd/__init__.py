@@ -649,7 +649,8 @@ def quantize_mx(x: torch.Tensor, dtype=torch.float8_e4m3fn, *, stream=None) -> M
 
 
 def dequantize_mx(t: MxTensor, out: Optional[torch.Tensor] = None, *, stream=None) -> torch.Tensor:
-    """MxTensor -> the bf16 values it stands for (exact)."""
+    """MxTensor -> the bf16 values it stands for (exact for every block that
+    quantize_mx writes; the header says what others give)."""
     if not isinstance(t, MxTensor):
         raise ValueError("t must be an MxTensor")
     codes = t.codes

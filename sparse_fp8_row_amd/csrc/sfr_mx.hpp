@@ -57,8 +57,9 @@ __device__ __forceinline__ float mx_scaled(float v, float inv, float limit) {
   return limit == 0.0f ? 0.0f : __builtin_amdgcn_fmed3f(v * inv, -limit, limit);
 }
 
-// The scale as a binary32 operand of the hardware converters: byte 255 gives
-// the exponent of infinities, with which they return NaN.
+// The scale as a binary32 operand of the hardware converters, which take its
+// exponent field: byte 0 is 2^-127, and with byte 255, the exponent of
+// infinities, they return NaN.
 __device__ __forceinline__ float mx_scale_value(uint32_t code) { return __uint_as_float(code << 23); }
 
 // Four scaled values (|v| <= fmax) -> four FP8 bytes, nearest even.
