@@ -429,7 +429,8 @@ sfr_status bsr_linear_bf16(const uint16_t* x, int64_t m, int64_t k, const int32_
  * their negatives) packs two values a byte, the even column in the low half. */
 typedef enum { SFR_MX_E4M3 = 0, SFR_MX_E5M2 = 1, SFR_MX_E2M1 = 2 } sfr_mx_t;
 
-/* Activation of the gated block: x s(x), the tanh form of GELU, max(x, 0). */
+/* Activation of the gated block: x s(x), the tanh form of GELU, max(x, 0).  The
+ * logistic factor s may be 0 where it lies below 2^-126 (SiLU: x < -87.3). */
 typedef enum { SFR_ACT_SILU = 0, SFR_ACT_GELU_TANH = 1, SFR_ACT_RELU = 2 } sfr_act_t;
 
 /* How an activation is saved for the backward pass. */
@@ -484,7 +485,10 @@ sfr_status gated_linear_bf16(const uint16_t* x, int64_t m, int64_t k, const uint
  *     dg = dh * u * act'(g),  du = dh * act(g)        (binary32, rounded to bf16)
  *     dx[m, k] = sum_j dg[m, j] w[j, k] + du[m, j] w[f + j, k]
  *     dw[j, k] = sum_m dg[m, j] x[m, k],  dw[f + j, k] = sum_m du[m, j] x[m, k]
- * (binary32 sums, rounded once to bf16).  relu'(0) = 0.
+ * (binary32 sums, rounded once to bf16).  relu' is 1 above 0 and 0 elsewhere, at
+ * NaN too.  The rounding of dg and du, which the matrix instructions read in
+ * bf16, makes the gradients' relative error 0.0024 (root mean square) where
+ * the last rounding alone would leave 0.0017.
  *
  *   dh        [m, f] bf16 bits.
  *   gu, gu_scale, gu_save   as gated_linear_bf16 wrote them.

@@ -678,7 +678,10 @@ def _gated_operands(x: torch.Tensor, w: torch.Tensor, device: int):
 
 def gated_linear(x: torch.Tensor, w: torch.Tensor, activation: str = "silu", out: Optional[torch.Tensor] = None, *,
                  stream=None) -> torch.Tensor:
-    """h [m, f] = act(x @ w[:f].T) * (x @ w[f:].T) for bf16 x [m, k], w [2 f, k]."""
+    """h [m, f] = act(x @ w[:f].T) * (x @ w[f:].T) for bf16 x [m, k], w [2 f, k].
+
+    The result has no autograd graph, also where x or w require grad; for
+    gradients call gated_linear_checkpointed and gated_linear_backward."""
     device = x.get_device()
     if stream is not None or device < 0 or device != _current_device():
         return _elsewhere(gated_linear, stream, x, w, activation, out)
@@ -697,7 +700,9 @@ def gated_linear_checkpointed(x: torch.Tensor, w: torch.Tensor, activation: str 
                               checkpoint=torch.float8_e4m3fn, *, stream=None):
     """(h, GatedCheckpoint): gated_linear, keeping for the backward pass x and
     the projections in 8 bits (checkpoint float8_e4m3fn or float8_e5m2: MX
-    blocks), or x itself and the projections in bf16 (torch.bfloat16)."""
+    blocks), or x itself and the projections in bf16 (torch.bfloat16).
+
+    h has no autograd graph: hand its gradient to gated_linear_backward."""
     device = x.get_device()
     if stream is not None or device < 0 or device != _current_device():
         return _elsewhere(gated_linear_checkpointed, stream, x, w, activation, checkpoint)
@@ -727,7 +732,8 @@ def _saved_parts(t, name: str, device: int):
 def gated_linear_backward(dh: torch.Tensor, w: torch.Tensor, saved: GatedCheckpoint, need_dx: bool = True,
                           need_dw: bool = True, *, stream=None):
     """(dx [m, k], dw [2 f, k]) in bf16 from dh [m, f], w and what
-    gated_linear_checkpointed kept; None in place of one that is not needed."""
+    gated_linear_checkpointed kept; None in place of one that is not needed.
+    Returned, not added to any .grad."""
     device = dh.get_device()
     if stream is not None or device < 0 or device != _current_device():
         return _elsewhere(gated_linear_backward, stream, dh, w, saved, need_dx, need_dw)
@@ -770,7 +776,8 @@ def _mxfp4_operands(x: torch.Tensor, w: MxTensor, device: int):
 def mxfp4_linear(x: torch.Tensor, w: MxTensor, bias: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
                  out: Optional[torch.Tensor] = None, *, stream=None) -> torch.Tensor:
     """bf16 x [m, k] -> out [m, n] = x @ W.T (+ bias) for a 4-bit weight W [n, k]
-    with one scale per 32 values, from quantize_mx(w, torch.float4_e2m1fn_x2)."""
+    with one scale per 32 values, from quantize_mx(w, torch.float4_e2m1fn_x2).
+    The result has no autograd graph."""
     device = x.get_device()
     if stream is not None or device < 0 or device != _current_device():
         return _elsewhere(mxfp4_linear, stream, x, w, bias, out_dtype, out)
@@ -797,7 +804,8 @@ def mxfp4_linear(x: torch.Tensor, w: MxTensor, bias: Optional[torch.Tensor] = No
 
 def mxfp4_gated_linear(x: torch.Tensor, w: MxTensor, activation: str = "silu", out: Optional[torch.Tensor] = None, *,
                        stream=None) -> torch.Tensor:
-    """gated_linear for a 4-bit weight [2 f, k] from quantize_mx(w, torch.float4_e2m1fn_x2)."""
+    """gated_linear for a 4-bit weight [2 f, k] from quantize_mx(w, torch.float4_e2m1fn_x2).
+    The result has no autograd graph."""
     device = x.get_device()
     if stream is not None or device < 0 or device != _current_device():
         return _elsewhere(mxfp4_gated_linear, stream, x, w, activation, out)
