@@ -198,11 +198,11 @@ __global__ __launch_bounds__(64 * WN * WM * KS) void dense_tile_kernel(DensePara
 // when a phase waits.  Loads past the last step read zeros (they are masked)
 // and keep the counts.
 //
-// Measured at m = 8192, k = 4096, f = 14336 (256 x 256): 1.29 - 1.45 PFLOP/s
-// forward, 1.46 dx, 1.35 dW, with the matrix units busy 80% of the cycles at a clock
-// that power holds near 1.5 GHz; without the global loads it would be 1.51
-// PFLOP/s, without the LDS reads 1.31.  Phases of 16 instructions took 1693
-// us forward in place of 1485.
+// Measured at m = 8192, k = 4096, f = 14336 (256 x 256): 1.37 - 1.45 PFLOP/s
+// forward, 1.50 dx, 1.38 dW (median of a run, the best 2 - 6% higher), with the matrix
+// units busy 80% of the cycles at a clock that power holds near 1.5 GHz.  On one
+// box, where the forward pass took 1485 us (1.30): without the global loads 1272,
+// without the LDS reads 1470, with phases of 16 instructions 1693.
 // ---------------------------------------------------------------------------
 template <int LX, int LW, int EPI, int WH, int XF>
 __global__ __launch_bounds__(512, 2) void dense_wide_kernel(DenseParams p) {
@@ -457,7 +457,9 @@ hipError_t run_wide(DenseParams p, int slices, hipStream_t stream) {
 //   m = 128, f = 14336: 128x64 48, 128x128 49 (KS = 2: 44), 256x256 76
 //   m = 140, f = 4096: 64x64 30 (KS = 2: 25), 128x64 32 (25), 128x128 41 (35)
 //   m = 33, k = f = 512: 64x64 5.3 (KS = 2: 4.6), 128x64 6.6 (5.8)
-//   m = 8192, f = 14336: 256x256 1485, 256x192 1618, 384x192 1662, 128x128 1868
+//   m = 8192, f = 14336: 256x256 1485, 256x192 1618, 384x192 1662, 128x128 1868 (one
+//     box; the clock decides: others run the first in 1310 - 1410, and the model,
+//     which only has to rank them, gives it 1566)
 //   dx m = 1000, k = 2048, f = 5632: 128x128 in 1, 2, 4, 8 slices 118, 73, 55, 67,
 //     256x256 211, 122, 76, 59;  m = 4096, k = f = 2048: 128x128 63, 256x192 85
 // Slices (plain outputs only) add a pass over their binary32 partial sums.
