@@ -70,3 +70,57 @@ def test_far_below_zero(sfr, m, act):
     h, bound, (g, u, _, _) = gated64(x.double(), w.double(), act)
     assert bool((h.abs() > 1e-6).any())
     check(sfr.gated_linear(x, w, act), h, bound + (g * u).abs() * 2.0 ** -126, "h")
+
+
+def calls(sfr, x, w, q, dh, **kw):
+    """One call of each operator, with `kw`, and of those with `out` into one."""
+    m, f = dh.shape
+    h, saved = sfr.gated_linear_checkpointed(x, w, **kw)
+    dx, dw = sfr.gated_linear_backward(dh, w, saved, **kw)
+    outs = [torch.empty(m, n, dtype=torch.bfloat16, device="cuda") for n in (f, f, 2 * f, x.shape[1])]
+    return [h, dx, dw, sfr.gated_linear(x, w, out=outs[0], **kw), sfr.mxfp4_gated_linear(x, q, out=outs[1], **kw),
+            sfr.mxfp4_linear(x, q, out=outs[2], **kw), sfr.dequantize_mx(saved.x, out=outs[3], **kw), *outs]
+
+
+@pytest.mark.parametrize("m,k,f", [(3, 4128, 1056), (130, 4128, 2080)])
+def test_explicit_stream_in_a_graph(sfr, m, k, f):
+    """Calls with an explicit stream captured into a graph: the capturing stream
+    named, and a side stream that the capture forks into and joins again.
+    Replayed with new inputs and eager work between, and after the inputs'
+    neighbours in memory were freed."""
+    x, w = inputs(3, m, k, 2 * f)
+    q, dh = sfr.quantize_mx(w, torch.float4_e2m1fn_x2), inputs(4, m, f, 16)[0]
+    calls(sfr, x, w, q, dh)
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        first = calls(sfr, x, w, q, dh, stream=here)
+        side.wait_stream(here)
+        second = calls(sfr, x, w, q, dh, stream=side)
+        here.wait_stream(side)
+    for i in range(3):
+        nx, nw = inputs(10 + i, m, k, 2 * f)
+        nq = sfr.quantize_mx(nw, torch.float4_e2m1fn_x2)
+        x.copy_(nx)
+        w.copy_(nw)
+        dh.copy_(inputs(20 + i, m, f, 16)[0])
+        q.codes.view(torch.uint8).copy_(nq.codes.view(torch.uint8))
+        q.scale.view(torch.uint8).copy_(nq.scale.view(torch.uint8))
+        del nx, nw, nq
+        graph.replay()
+        want = calls(sfr, x, w, q, dh)
+        torch.cuda.synchronize()
+        for a, b, c in zip(first, second, want):
+            assert torch.equal(a, c) and torch.equal(b, c), i
+
+
+def test_inputs_that_are_one_tensor(sfr):
+    """The same tensor as activation and weight, and h as its own gradient."""
+    w = inputs(5, 16, 96, 128)[1]
+    copy = w.clone()
+    h, saved = sfr.gated_linear_checkpointed(w, w, checkpoint=torch.bfloat16)
+    hp, sp = sfr.gated_linear_checkpointed(copy, w, checkpoint=torch.bfloat16)
+    assert torch.equal(h, hp) and torch.equal(w, copy)
+    for a, b in zip(sfr.gated_linear_backward(h, w, saved), sfr.gated_linear_backward(hp.clone(), copy, sp)):
+        assert torch.equal(a, b)
