@@ -555,6 +555,147 @@ typedef enum {
  */
 const char* sfr_block_kernel(sfr_product_t product, int64_t m, int64_t k, int64_t f, int32_t* slices);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The linear layer in 8-bit integers, one scale per activation row (token) and
+ * weight row (output channel):
+ *
+ *     out[m, n] = xs[m] ws[n] sum_k xq[m, k] wq[n, k]  (+ bias[n])
+ *
+ * The sum is exact in 32 bits, so results depend on nothing but the arguments:
+ * not on the kernel, on the other rows of a batch, nor on whether x was quantized
+ * before the call or in it.  It is rounded to binary32; a fused multiply-add with
+ * the binary32 product xs[m] ws[n] and the bias rounds once more, and the result is
+ * rounded once to bf16 or returned in binary32.
+ *
+ * Sizes: 0 <= m <= SFR_MAX_DIM; 0 < k <= SFR_MAX_INT8_K (the largest sum of products
+ * of any 8-bit codes then fits 32 bits); 0 <= n <= SFR_MAX_BLOCK_DIM; k % 16 == 0,
+ * n % 16 == 0; a call with more than 2^21 tiles of 128 x 128 outputs (64 x 64 up to
+ * 64 rows) is SFR_ERR_SHAPE.
+ * ---------------------------------------------------------------------------
+ */
+#define SFR_MAX_INT8_K ((int64_t)131056)
+
+/*
+ * quantize_rowwise_int8 -- bf16 rows to 8-bit integers, activations by token or a
+ * weight by output channel:
+ *     amax  = max |x[r, :]|                                    (exact)
+ *     q     = the whole number nearest to 127 x / amax, ties to even (exactly so:
+ *             no rounding of the quotient shows)
+ *     scale = amax / 127                                       (binary32)
+ * A row of zeros gets scale 0 and zero codes; a row that holds a NaN or an infinity
+ * gets scale NaN and zero codes, so that its products are NaN and no other row's
+ * are.  Deterministic, bit-exact.
+ *
+ *   x [rows, cols] bf16 bits, q [rows, cols] bytes, scale [rows] binary32.
+ * Sizes: 0 <= rows <= SFR_MAX_DIM, 0 < cols <= SFR_MAX_DIM, cols % 8 == 0.
+ * rows == 0 is a no-op.
+ */
+sfr_status quantize_rowwise_int8(const uint16_t* x, int64_t rows, int64_t cols, int8_t* q, float* scale,
+                                 void* stream);
+
+/*
+ * int8_scaled_linear -- the layer on quantized x [m, k].
+ * int8_linear_dynamic -- the same from a bf16 x: quantize_rowwise_int8, then the layer.
+ *
+ *   xq [m, k], wq [n, k]: codes;  xs [m], ws [n]: binary32 scales.
+ *   x   [m, k] bf16 bits.
+ *   bias [n] bf16 bits or NULL;  out [m, n] bf16 bits or binary32.
+ *   workspace  device scratch of at least sfr_int8_workspace_bytes(m, n, k, dynamic)
+ *              bytes (0 for many sizes of the first form; then it may be NULL),
+ *              overwritten; calls that may run at the same time need distinct
+ *              workspaces.
+ * m == 0 or n == 0 is a no-op; a small workspace is SFR_ERR_SHAPE.
+ */
+sfr_status int8_scaled_linear(const int8_t* xq, const float* xs, int64_t m, int64_t k, const int8_t* wq,
+                              const float* ws, int64_t n, const uint16_t* bias, void* out, sfr_out_t out_dt,
+                              void* workspace, int64_t workspace_bytes, void* stream);
+sfr_status int8_linear_dynamic(const uint16_t* x, int64_t m, int64_t k, const int8_t* wq, const float* ws, int64_t n,
+                               const uint16_t* bias, void* out, sfr_out_t out_dt, void* workspace,
+                               int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of int8_linear_dynamic (dynamic != 0) or int8_scaled_linear; 0 for sizes they reject. */
+int64_t sfr_int8_workspace_bytes(int64_t m, int64_t n, int64_t k, int dynamic);
+
+/* The product's kernel, as sfr_block_kernel gives it for the block's products. */
+const char* sfr_int8_kernel(int64_t m, int64_t n, int64_t k, int dynamic, int32_t* slices);
+
+/*
+ * ---------------------------------------------------------------------------
+ * A mixture of gated feed-forward blocks ("experts") for a few tokens: the router,
+ * and the whole layer in two launches.
+ * ---------------------------------------------------------------------------
+ */
+#define SFR_MAX_EXPERTS 1024
+#define SFR_MAX_TOP 16
+
+/* How the router's weights are formed from its logits: exp(l) over the sum of all
+ * experts' exp, or 1 / (1 + exp(-l)). */
+typedef enum { SFR_ROUTE_SOFTMAX = 0, SFR_ROUTE_SIGMOID = 1 } sfr_route_t;
+
+/*
+ * moe_route -- the router: for every token its `top` best experts, best first.
+ *     logits[t, e]  = sum_k x[t, k] w[e, k] (+ bias[e])
+ *     ids[t, :]     = the experts with the largest logits; of equal logits (as
+ *                     rounded; -0 equals 0) the lowest expert comes first
+ *     weights[t, s] = score of logits[t, ids[t, s]], divided by the sum of the
+ *                     chosen experts' scores where renormalize is not 0
+ * The sum is formed in binary64 and rounded once to binary32, so that the choice
+ * does not depend on the other tokens of a call.  An expert with logit -infinity (a
+ * bias of -infinity shuts it off) is never chosen: a slot left over has id -1 and
+ * weight 0.  NaN counts as larger than everything else and makes the weights NaN.
+ *
+ *   x [m, k], w [experts, k]: bf16 bits;  bias [experts] binary32 or NULL.
+ *   logits [m, experts] binary32, ids [m, top] int32, weights [m, top] binary32: written.
+ * Sizes: 0 <= m <= SFR_MAX_DIM; 0 < k <= SFR_MAX_BLOCK_DIM, k % 32 == 0;
+ * 0 < experts <= SFR_MAX_EXPERTS; 0 < top <= min(experts, SFR_MAX_TOP).
+ * m == 0 is a no-op.
+ */
+sfr_status moe_route(const uint16_t* x, int64_t m, int64_t k, const uint16_t* w, int64_t experts, const float* bias,
+                     int64_t top, sfr_route_t score, int renormalize, float* logits, int32_t* ids, float* weights,
+                     void* stream);
+
+/* Form of the experts' weights: bf16; 8-bit integers with a scale per row (as
+ * quantize_rowwise_int8 writes them; the activation stays bf16); 4-bit blocks (as
+ * quantize_mx writes SFR_MX_E2M1). */
+typedef enum { SFR_EXPERT_BF16 = 0, SFR_EXPERT_INT8 = 1, SFR_EXPERT_MXFP4 = 2 } sfr_expert_t;
+
+/*
+ * moe_layer -- the layer on the router's choice:
+ *     h[t, s]  = act(x[t] Wg[e]^T) * (x[t] Wu[e]^T),  e = ids[t, s]
+ *     out[t]   = sum_s weights[t, s] h[t, s] Wd[e]^T
+ * Sums are binary32; h is rounded once to bf16, the type in which the second
+ * product reads it, and out once to bf16.  ids outside [0, experts) are no choice
+ * (padding, or experts held elsewhere: out is then this device's share); a token
+ * without a choice gets zeros.  An expert named twice counts with the sum of its
+ * weights.  A token's result depends on no other token's values, and infinities and
+ * NaN in an expert reach only the tokens that chose it; the order of a token's
+ * sums depends on which experts the call's tokens chose.  No atomics on results.
+ *
+ *   x [m, k], out [m, k]: bf16 bits.  ids [m, top] int32, weights [m, top] binary32.
+ *   w_gate_up  [experts, 2 f, k]: every expert's gate rows, then its up rows.
+ *   w_down     [experts, k, f].
+ *     SFR_EXPERT_BF16   bf16 bits; the scales are not used (NULL).
+ *     SFR_EXPERT_INT8   codes; scales binary32 [experts, 2 f] and [experts, k].
+ *     SFR_EXPERT_MXFP4  two codes a byte; scales bytes [experts, 2 f, k / 32] and
+ *                       [experts, k, f / 32].
+ *   workspace  device scratch of at least sfr_moe_workspace_bytes(m, f, top) bytes,
+ *              overwritten; calls that may run at the same time need distinct
+ *              workspaces.
+ * Sizes: 0 <= m <= SFR_MAX_DIM (taken 64 tokens at a time, each reading the weights
+ * of the experts that they chose); 0 < k, 2 f <= SFR_MAX_BLOCK_DIM, k % 32 == 0,
+ * f % 32 == 0; 0 < experts <= SFR_MAX_EXPERTS; 0 < top <= SFR_MAX_TOP.
+ * Alignment: 16 bytes, ids and weights 4.  m == 0 is a no-op; a small workspace is
+ * SFR_ERR_SHAPE.
+ */
+sfr_status moe_layer(const uint16_t* x, int64_t m, int64_t k, const int32_t* ids, const float* weights, int64_t top,
+                     int64_t experts, int64_t f, sfr_expert_t form, const void* w_gate_up, const void* gate_up_scale,
+                     const void* w_down, const void* down_scale, sfr_act_t act, uint16_t* out, void* workspace,
+                     int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of moe_layer; 0 for sizes it rejects. */
+int64_t sfr_moe_workspace_bytes(int64_t m, int64_t f, int64_t top);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* sfr_status_string(sfr_status s);
 

@@ -13,8 +13,10 @@ Tensor-wise scaling (one scale per operand): ``quantize_tensorwise_fp8``,
 ``prepare_weight(..., scaling="tensor")`` and ``sparse_fp8_scaled_linear``.
 
 The gated feed-forward block (``gated_linear``, its gradients from 8-bit
-activations, its 4-bit form) and the MX block formats are at the end of this
-module.  None of these calls builds an autograd graph: the gradient is
+activations, its 4-bit form) and the MX block formats, the linear layer in
+8-bit integers (``int8_linear``) and the mixture of gated blocks for a few
+tokens (``moe_route``, ``moe_layer``) are at the end of this module.  None of
+these calls builds an autograd graph: the gated block's gradient is
 ``gated_linear_backward``.
 
 The operator follows pytorch/ao PR #1671 ("Add CUTLASS-based row-wise scaled
@@ -49,7 +51,9 @@ EXPORTED = ("quantize_rowwise_fp8", "quantize_tensorwise_fp8", "sfr_quantize_ten
             "bsr_count_bf16", "bsr_fill_bf16", "bsr_linear_bf16", "sfr_status_string", "sfr_format_version",
             "quantize_mx", "dequantize_mx", "gated_linear_bf16", "gated_linear_bf16_backward",
             "sfr_gated_backward_workspace_bytes", "mxfp4_linear", "mxfp4_gated_linear", "sfr_mxfp4_workspace_bytes",
-            "sfr_block_kernel")
+            "sfr_block_kernel",
+            "quantize_rowwise_int8", "int8_scaled_linear", "int8_linear_dynamic", "sfr_int8_workspace_bytes",
+            "sfr_int8_kernel", "moe_route", "moe_layer", "sfr_moe_workspace_bytes")
 
 _FP8 = {torch.float8_e4m3fn: SFR_E4M3, torch.float8_e5m2: SFR_E5M2}
 _lib = None
@@ -107,6 +111,20 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sfr_mxfp4_workspace_bytes.restype = I64
     lib.sfr_block_kernel.argtypes = [I, I64, I64, I64, ctypes.POINTER(ctypes.c_int32)]
     lib.sfr_block_kernel.restype = ctypes.c_char_p
+    lib.quantize_rowwise_int8.argtypes = [P, I64, I64, P, P, P]
+    lib.int8_scaled_linear.argtypes = [P, P, I64, I64, P, P, I64, P, P, I, P, I64, P]
+    lib.int8_linear_dynamic.argtypes = [P, I64, I64, P, P, I64, P, P, I, P, I64, P]
+    lib.sfr_int8_workspace_bytes.argtypes = [I64, I64, I64, I]
+    lib.sfr_int8_workspace_bytes.restype = I64
+    lib.sfr_int8_kernel.argtypes = [I64, I64, I64, I, ctypes.POINTER(ctypes.c_int32)]
+    lib.sfr_int8_kernel.restype = ctypes.c_char_p
+    lib.moe_route.argtypes = [P, I64, I64, P, I64, P, I64, I, I, P, P, P, P]
+    lib.moe_layer.argtypes = [P, I64, I64, P, P, I64, I64, I64, I, P, P, P, P, I, P, P, I64, P]
+    lib.sfr_moe_workspace_bytes.argtypes = [I64, I64, I64]
+    lib.sfr_moe_workspace_bytes.restype = I64
+    for fn in (lib.quantize_rowwise_int8, lib.int8_scaled_linear, lib.int8_linear_dynamic, lib.moe_route,
+               lib.moe_layer):
+        fn.restype = I
     for fn in (lib.quantize_mx, lib.dequantize_mx, lib.gated_linear_bf16, lib.gated_linear_bf16_backward,
                lib.mxfp4_linear, lib.mxfp4_gated_linear):
         fn.restype = I
@@ -513,6 +531,28 @@ class MxTensor:
 
 
 @dataclass
+class Int8Tensor:
+    """Rows of 8-bit integers with one scale each: codes int8 [rows, cols],
+    scale float32 [rows]; a value is scale * code."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+
+    @property
+    def shape(self):
+        return tuple(self.codes.shape)
+
+
+@dataclass
+class MoeRoute:
+    """A router's choice: ids int32 [m, top] (the experts of every token, best
+    first; values outside [0, experts) are no choice), their weights float32
+    [m, top], and the logits float32 [m, experts] where moe_route formed them."""
+    ids: torch.Tensor
+    weights: torch.Tensor
+    logits: Optional[torch.Tensor] = None
+
+
+@dataclass
 class GatedCheckpoint:
     """What gated_linear_checkpointed keeps for gated_linear_backward: the
     input x [m, k] and the projections gu = [g | u] [m, 2 f], each a bf16 tensor
@@ -536,7 +576,7 @@ def _elsewhere(fn, stream, first, *args):
     the stream its kernels run on, and the memory of its arguments is not used
     again before that stream is done with them (the stream has to be ordered
     after what produced them, as for any work)."""
-    t = first.codes if isinstance(first, MxTensor) else first
+    t = first.codes if isinstance(first, (MxTensor, Int8Tensor)) else first
     device = t.get_device()
     if device < 0:
         raise ValueError("the arguments must be GPU tensors")
@@ -555,9 +595,12 @@ def _keep(a, stream):
     if isinstance(a, torch.Tensor):
         if a.is_cuda:
             a.record_stream(stream)
-    elif isinstance(a, MxTensor):
+    elif isinstance(a, (MxTensor, Int8Tensor)):
         _keep(a.codes, stream)
         _keep(a.scale, stream)
+    elif isinstance(a, MoeRoute):
+        _keep(a.ids, stream)
+        _keep(a.weights, stream)
     elif isinstance(a, GatedCheckpoint):
         _keep(a.x, stream)
         _keep(a.gu, stream)
@@ -835,3 +878,204 @@ def block_kernel(product: str, m: int, k: int, f: int):
     slices = ctypes.c_int32()
     name = load().sfr_block_kernel(_PRODUCTS[product], m, k, f, ctypes.byref(slices))
     return None if name is None else (name.decode(), slices.value)
+
+
+# --------------------------------------------------------------------------
+# Linear layer in 8-bit integers
+# --------------------------------------------------------------------------
+_INT8, _F32, _I32 = torch.int8, torch.float32, torch.int32
+
+
+def _int8_parts(t, name: str, device: int):
+    """(rows, cols, address of the codes, of the scales) of an Int8Tensor, checked."""
+    if not isinstance(t, Int8Tensor):
+        raise ValueError(f"{name} must be an Int8Tensor")
+    codes, scale = t.codes, t.scale
+    if codes.dtype is not _INT8 or codes.dim() != 2 or scale.dtype is not _F32:
+        raise ValueError(f"{name}: codes must be 2-D int8 and scale float32")
+    rows, cols = codes.shape
+    if scale.shape != (rows,):
+        raise ValueError(f"{name}: scale must have one entry per row")
+    if codes.get_device() != device or scale.get_device() != device or device < 0 or not codes.is_contiguous() or \
+            not scale.is_contiguous():
+        _refuse(codes, f"{name}.codes", device)
+        _refuse(scale, f"{name}.scale", device)
+    return rows, cols, codes.data_ptr(), scale.data_ptr()
+
+
+def quantize_rowwise_int8(x: torch.Tensor, *, stream=None) -> Int8Tensor:
+    """bf16 [rows, cols] -> Int8Tensor, scale = amax / 127 for every row: an
+    activation by token, or a weight [n, k] by output channel (cols a multiple of 8)."""
+    device = x.get_device()
+    if stream is not None or device < 0 or device != _current_device():
+        return _elsewhere(quantize_rowwise_int8, stream, x)
+    px = _bf16_2d(x, "x", device)
+    rows, cols = x.shape
+    codes = torch.empty_like(x, dtype=_INT8)
+    scale = x.new_empty((rows,), dtype=_F32)
+    _check(load().quantize_rowwise_int8(px, rows, cols, codes.data_ptr(), scale.data_ptr(), _raw_stream(device)),
+           "quantize_rowwise_int8")
+    return Int8Tensor(codes, scale)
+
+
+@functools.lru_cache(maxsize=4096)
+def _int8_workspace_bytes(m: int, n: int, k: int, dynamic: bool) -> int:
+    return load().sfr_int8_workspace_bytes(m, n, k, dynamic)
+
+
+def int8_linear(x, w: Int8Tensor, bias: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
+                out: Optional[torch.Tensor] = None, *, stream=None) -> torch.Tensor:
+    """x [m, k] -> out [m, n] = x @ W.T (+ bias) in 8-bit integers for a weight W
+    [n, k] from quantize_rowwise_int8.  x: bf16, quantized by token in the call,
+    or an Int8Tensor (one quantization for several products); both give the same
+    bits.  The result has no autograd graph."""
+    dynamic = not isinstance(x, Int8Tensor)
+    first = x if dynamic else x.codes
+    device = first.get_device()
+    if stream is not None or device < 0 or device != _current_device():
+        return _elsewhere(int8_linear, stream, x, w, bias, out_dtype, out)
+    if dynamic:
+        px = _bf16_2d(x, "x", device)
+        m, k = x.shape
+    else:
+        m, k, px, pxs = _int8_parts(x, "x", device)
+    n, wk, pw, pws = _int8_parts(w, "w", device)
+    if wk != k:
+        raise ValueError("operand shapes do not match")
+    pb = None
+    if bias is not None:
+        if bias.dtype is not _BF16 or bias.shape != (n,):
+            raise ValueError("bias must be bfloat16 [n]")
+        _refuse(bias, "bias", device)
+        pb = bias.data_ptr()
+    if out_dtype is not _BF16 and out_dtype is not _F32:
+        raise ValueError("out_dtype must be bfloat16 or float32")
+    if out is not None:
+        _check_out(out, m, n, out_dtype, first, w.codes, w.scale, *(() if dynamic else (x.scale,)),
+                   *(() if bias is None else (bias,)))
+    else:
+        out = w.scale.new_empty((m, n), dtype=out_dtype)
+    od = SFR_OUT_BF16 if out_dtype is _BF16 else SFR_OUT_F32
+    nbytes = _int8_workspace_bytes(m, n, k, dynamic)
+    work = w.codes.new_empty((nbytes,)) if nbytes else None
+    pwork = work.data_ptr() if nbytes else None
+    if dynamic:
+        _check(load().int8_linear_dynamic(px, m, k, pw, pws, n, pb, out.data_ptr(), od, pwork, nbytes,
+                                          _raw_stream(device)), "int8_linear")
+    else:
+        _check(load().int8_scaled_linear(px, pxs, m, k, pw, pws, n, pb, out.data_ptr(), od, pwork, nbytes,
+                                         _raw_stream(device)), "int8_linear")
+    return out
+
+
+def int8_kernel(m: int, n: int, k: int, dynamic: bool = True):
+    """(name, slices of the sum) of the kernel that int8_linear's product takes, as
+    block_kernel gives it; None for sizes that the call rejects or that leave nothing to do."""
+    slices = ctypes.c_int32()
+    name = load().sfr_int8_kernel(m, n, k, dynamic, ctypes.byref(slices))
+    return None if name is None else (name.decode(), slices.value)
+
+
+# --------------------------------------------------------------------------
+# Mixture of gated feed-forward blocks for a few tokens
+# --------------------------------------------------------------------------
+SFR_ROUTE = {"softmax": 0, "sigmoid": 1}
+
+
+def moe_route(x: torch.Tensor, w: torch.Tensor, top: int, bias: Optional[torch.Tensor] = None,
+              score: str = "softmax", renormalize: bool = True, *, stream=None) -> MoeRoute:
+    """The `top` best experts of every token: logits = x @ w.T (+ bias) for bf16 x
+    [m, k], w [experts, k] and float32 bias [experts]; weights from their softmax
+    over all experts or their sigmoid, divided by the chosen ones' sum with
+    `renormalize`.  Of equal logits the lowest expert comes first; an expert whose
+    bias is -inf is never chosen (a slot left over: id -1, weight 0).  The logits'
+    sum is formed in binary64, so the choice does not depend on the rest of the
+    batch.  The results have no autograd graph."""
+    device = x.get_device()
+    if stream is not None or device < 0 or device != _current_device():
+        return _elsewhere(moe_route, stream, x, w, top, bias, score, renormalize)
+    px, pw = _bf16_2d(x, "x", device), _bf16_2d(w, "w", device)
+    m, k = x.shape
+    experts, wk = w.shape
+    if wk != k:
+        raise ValueError("operand shapes do not match")
+    if score not in SFR_ROUTE:
+        raise ValueError(f"score must be one of {sorted(SFR_ROUTE)}")
+    pb = None
+    if bias is not None:
+        if bias.dtype is not _F32 or bias.shape != (experts,):
+            raise ValueError("bias must be float32 [experts]")
+        _refuse(bias, "bias", device)
+        pb = bias.data_ptr()
+    if not 0 < top <= experts:
+        raise ValueError("top must be between 1 and the number of experts")
+    logits = x.new_empty((m, experts), dtype=_F32)
+    ids = x.new_empty((m, top), dtype=_I32)
+    weights = x.new_empty((m, top), dtype=_F32)
+    _check(load().moe_route(px, m, k, pw, experts, pb, top, SFR_ROUTE[score], renormalize, logits.data_ptr(),
+                            ids.data_ptr(), weights.data_ptr(), _raw_stream(device)), "moe_route")
+    return MoeRoute(ids, weights, logits)
+
+
+def _expert_parts(t, name: str, device: int):
+    """(form, rows, cols, address of the weights, of the scales or None) of the
+    experts' stacked weight rows, checked."""
+    if isinstance(t, Int8Tensor):
+        return (1, *_int8_parts(t, name, device))
+    if isinstance(t, MxTensor):
+        return (2, *_mx_parts(t, name, device, _FP4))
+    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.dim() != 3:
+        raise ValueError(f"{name} must be a 3-D bfloat16 tensor, an Int8Tensor or a 4-bit MxTensor")
+    if t.get_device() != device or device < 0 or not t.is_contiguous():
+        _refuse(t, name, device)
+    a, b, c = t.shape
+    return 0, a * b, c, t.data_ptr(), None
+
+
+def moe_layer(x: torch.Tensor, route: MoeRoute, w_gate_up, w_down, activation: str = "silu",
+              out: Optional[torch.Tensor] = None, *, stream=None) -> torch.Tensor:
+    """The whole mixture of gated feed-forward blocks for a few tokens, in two
+    launches: out[t] = sum_s weights[t, s] * (act(x[t] @ Wg[e].T) * (x[t] @ Wu[e].T)) @ Wd[e].T,
+    e = ids[t, s], for bf16 x [m, k].
+
+    w_gate_up: bf16 [experts, 2 f, k], every expert's gate rows and then its up
+    rows; or those rows stacked [experts * 2 f, k] in 8 bits
+    (quantize_rowwise_int8) or 4 bits (quantize_mx(w, torch.float4_e2m1fn_x2)).
+    w_down: bf16 [experts, k, f], or stacked [experts * k, f] in the same form.
+    Tokens are taken 64 at a time, each time reading the chosen experts' weights
+    once.  ids outside [0, experts) are no choice; a token without one gets zeros.
+    The result has no autograd graph."""
+    device = x.get_device()
+    if stream is not None or device < 0 or device != _current_device():
+        return _elsewhere(moe_layer, stream, x, route, w_gate_up, w_down, activation, out)
+    px = _bf16_2d(x, "x", device)
+    m, k = x.shape
+    ids, weights = route.ids, route.weights
+    if ids.dtype is not _I32 or weights.dtype is not _F32 or ids.dim() != 2 or ids.shape[0] != m or \
+            weights.shape != ids.shape:
+        raise ValueError("route must hold ids int32 [m, top] and weights float32 [m, top]")
+    if ids.get_device() != device or weights.get_device() != device or not ids.is_contiguous() or \
+            not weights.is_contiguous():
+        _refuse(ids, "route.ids", device)
+        _refuse(weights, "route.weights", device)
+    form, rows, wk, pg, pgs = _expert_parts(w_gate_up, "w_gate_up", device)
+    dform, drows, f, pd, pds = _expert_parts(w_down, "w_down", device)
+    experts = drows // k if k else 0
+    if dform != form:
+        raise ValueError("w_gate_up and w_down must be of the same form")
+    if wk != k or experts * k != drows or experts * 2 * f != rows or \
+            form == 0 and not (w_gate_up.shape[0] == w_down.shape[0] == experts):
+        raise ValueError("operand shapes do not match: w_gate_up [experts, 2 f, k], w_down [experts, k, f]")
+    act = _act_enum(activation)
+    if out is not None:
+        parts = [t for w in (w_gate_up, w_down) for t in ((w,) if form == 0 else (w.codes, w.scale))]
+        _check_out(out, m, k, _BF16, x, ids, weights, *parts)
+    else:
+        out = torch.empty_like(x)
+    top = ids.shape[1]
+    lib = load()
+    nbytes = lib.sfr_moe_workspace_bytes(m, f, top)
+    work = x.new_empty((max(nbytes, 16),), dtype=torch.uint8)
+    _check(lib.moe_layer(px, m, k, ids.data_ptr(), weights.data_ptr(), top, experts, f, form, pg, pgs, pd, pds, act,
+                         out.data_ptr(), work.data_ptr(), nbytes, _raw_stream(device)), "moe_layer")
+    return out

@@ -17,7 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsparse_fp8_row.so")
 SOURCES = ["api.hip", "quantize.hip", "compress.hip", "gemm.hip", "bsr.hip",
-           "mx.hip", "dense.hip", "stream.hip", "gated.hip"]
+           "mx.hip", "dense.hip", "stream.hip", "gated.hip", "int8.hip", "moe.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -8,6 +8,7 @@
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool fp8_ok(int dt) { return dt == SFR_E4M3 || dt == SFR_E5M2; }
 bool scale_ok(int kind) { return kind == SFR_SCALE_ROW || kind == SFR_SCALE_TENSOR; }
 // Bound on rows * cols of any one tensor, keeping every grid within HIP's limits.
@@ -27,6 +28,14 @@ bool dense_ok(int64_t rows, int64_t cols) {
 bool gated_shape(int64_t m, int64_t k, int64_t f) {
   return m >= 0 && m <= SFR_MAX_DIM && block_dim(k, 32) && gated_dim(f) && dense_ok(m, 2 * f) &&
          dense_ok(m, k) && dense_ok(2 * f, k);
+}
+
+bool int8_shape(int64_t m, int64_t n, int64_t k) {
+  return m >= 0 && m <= SFR_MAX_DIM && (n == 0 || block_dim(n, 16)) && k > 0 && k <= SFR_MAX_INT8_K && k % 16 == 0 &&
+         dense_ok(m, n);
+}
+bool moe_sizes(int64_t m, int64_t experts, int64_t top) {
+  return m >= 0 && m <= SFR_MAX_DIM && experts > 0 && experts <= SFR_MAX_EXPERTS && top > 0 && top <= SFR_MAX_TOP;
 }
 
 sfr_status launch_status(hipError_t e) { return e == hipSuccess ? SFR_OK : SFR_ERR_LAUNCH; }
@@ -329,6 +338,118 @@ const char* sfr_block_kernel(sfr_product_t product, int64_t m, int64_t k, int64_
   const sfr::DenseKernel c = sfr::block_kernel((int)product, m, k, f);
   if (slices) *slices = c.slices;
   return c.name;
+}
+
+sfr_status quantize_rowwise_int8(const uint16_t* x, int64_t rows, int64_t cols, int8_t* q, float* scale,
+                                 void* stream) {
+  if (rows < 0 || rows > SFR_MAX_DIM || cols <= 0 || cols > SFR_MAX_DIM || cols % 8 != 0 || rows * cols > kMaxElems)
+    return SFR_ERR_SHAPE;
+  if (rows == 0) return SFR_OK;
+  if (!x || !q || !scale) return SFR_ERR_NULL;
+  if (!aligned16(x) || !aligned16(q) || !aligned16(scale)) return SFR_ERR_ALIGN;
+  return launch_status(sfr::launch_quantize_int8(x, rows, cols, q, scale, static_cast<hipStream_t>(stream)));
+}
+
+int64_t sfr_int8_workspace_bytes(int64_t m, int64_t n, int64_t k, int dynamic) {
+  if (!int8_shape(m, n, k) || m == 0 || n == 0) return 0;
+  return sfr::int8_workspace_bytes(m, n, k, dynamic != 0);
+}
+
+const char* sfr_int8_kernel(int64_t m, int64_t n, int64_t k, int dynamic, int32_t* slices) {
+  if (!int8_shape(m, n, k) || m == 0 || n == 0) return nullptr;
+  const sfr::DenseKernel c = sfr::int8_kernel(m, n, k, dynamic != 0);
+  if (slices) *slices = c.slices;
+  return c.name;
+}
+
+sfr_status int8_scaled_linear(const int8_t* xq, const float* xs, int64_t m, int64_t k, const int8_t* wq,
+                              const float* ws, int64_t n, const uint16_t* bias, void* out, sfr_out_t out_dt,
+                              void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!out_ok(out_dt)) return SFR_ERR_DTYPE;
+  if (!int8_shape(m, n, k)) return SFR_ERR_SHAPE;
+  if (m == 0 || n == 0) return SFR_OK;
+  const int64_t need = sfr::int8_workspace_bytes(m, n, k, false);
+  if (workspace_bytes < need) return SFR_ERR_SHAPE;
+  if (!xq || !xs || !wq || !ws || !out || (need > 0 && !workspace)) return SFR_ERR_NULL;
+  if (!aligned16(xq) || !aligned16(xs) || !aligned16(wq) || !aligned16(ws) || !aligned16(out) ||
+      (bias && !aligned16(bias)) || (need > 0 && !aligned16(workspace)))
+    return SFR_ERR_ALIGN;
+  const sfr::Int8Args a{nullptr, xq, xs, wq, ws, bias, out, m, n, k, (int)out_dt};
+  return launch_status(sfr::launch_int8(a, workspace, static_cast<hipStream_t>(stream)));
+}
+
+sfr_status int8_linear_dynamic(const uint16_t* x, int64_t m, int64_t k, const int8_t* wq, const float* ws, int64_t n,
+                               const uint16_t* bias, void* out, sfr_out_t out_dt, void* workspace,
+                               int64_t workspace_bytes, void* stream) {
+  if (!out_ok(out_dt)) return SFR_ERR_DTYPE;
+  if (!int8_shape(m, n, k)) return SFR_ERR_SHAPE;
+  if (m == 0 || n == 0) return SFR_OK;
+  const int64_t need = sfr::int8_workspace_bytes(m, n, k, true);
+  if (workspace_bytes < need) return SFR_ERR_SHAPE;
+  if (!x || !wq || !ws || !out || (need > 0 && !workspace)) return SFR_ERR_NULL;
+  if (!aligned16(x) || !aligned16(wq) || !aligned16(ws) || !aligned16(out) || (bias && !aligned16(bias)) ||
+      (need > 0 && !aligned16(workspace)))
+    return SFR_ERR_ALIGN;
+  const sfr::Int8Args a{x, nullptr, nullptr, wq, ws, bias, out, m, n, k, (int)out_dt};
+  return launch_status(sfr::launch_int8(a, workspace, static_cast<hipStream_t>(stream)));
+}
+
+sfr_status moe_route(const uint16_t* x, int64_t m, int64_t k, const uint16_t* w, int64_t experts, const float* bias,
+                     int64_t top, sfr_route_t score, int renormalize, float* logits, int32_t* ids, float* weights,
+                     void* stream) {
+  if (score != SFR_ROUTE_SOFTMAX && score != SFR_ROUTE_SIGMOID) return SFR_ERR_DTYPE;
+  if (!moe_sizes(m, experts, top) || top > experts || !block_dim(k, 32)) return SFR_ERR_SHAPE;
+  if (m == 0) return SFR_OK;
+  if (!x || !w || !logits || !ids || !weights) return SFR_ERR_NULL;
+  if (!aligned16(x) || !aligned16(w) || !aligned16(bias) || !aligned16(logits) || !aligned16(ids) ||
+      !aligned16(weights))
+    return SFR_ERR_ALIGN;
+  const sfr::RouteArgs a{x,         w,      m,   (int)k, (int)experts, bias, (int)top, (int)score, renormalize != 0,
+                         logits,    ids,    weights};
+  return launch_status(sfr::launch_moe_route(a, static_cast<hipStream_t>(stream)));
+}
+
+int64_t sfr_moe_workspace_bytes(int64_t m, int64_t f, int64_t top) {
+  if (!moe_sizes(m, 1, top) || !gated_dim(f)) return 0;
+  return sfr::moe_workspace_bytes(m, f, (int)top);
+}
+
+sfr_status moe_layer(const uint16_t* x, int64_t m, int64_t k, const int32_t* ids, const float* weights, int64_t top,
+                     int64_t experts, int64_t f, sfr_expert_t form, const void* w_gate_up, const void* gate_up_scale,
+                     const void* w_down, const void* down_scale, sfr_act_t act, uint16_t* out, void* workspace,
+                     int64_t workspace_bytes, void* stream) {
+  static_assert(SFR_MAX_EXPERTS == sfr::kMoeExperts && SFR_MAX_TOP == sfr::kMoeTop, "the same limits");
+  static_assert((int)SFR_EXPERT_INT8 == sfr::EXPERT_INT8 && (int)SFR_EXPERT_MXFP4 == sfr::EXPERT_FP4 &&
+                    (int)SFR_ROUTE_SIGMOID == sfr::ROUTE_SIGMOID,
+                "the same numbers");
+  if (!act_ok(act) || form < SFR_EXPERT_BF16 || form > SFR_EXPERT_MXFP4) return SFR_ERR_DTYPE;
+  if (!moe_sizes(m, experts, top) || !block_dim(k, 32) || !gated_dim(f)) return SFR_ERR_SHAPE;
+  if (m == 0) return SFR_OK;
+  if (workspace_bytes < sfr::moe_workspace_bytes(m, f, (int)top)) return SFR_ERR_SHAPE;
+  const bool scaled = form != SFR_EXPERT_BF16;
+  if (!x || !ids || !weights || !w_gate_up || !w_down || !out || !workspace ||
+      (scaled && (!gate_up_scale || !down_scale)))
+    return SFR_ERR_NULL;
+  if (!aligned16(x) || !aligned4(ids) || !aligned4(weights) || !aligned16(w_gate_up) || !aligned16(w_down) ||
+      !aligned16(out) || !aligned16(workspace) || (scaled && (!aligned16(gate_up_scale) || !aligned16(down_scale))))
+    return SFR_ERR_ALIGN;
+  sfr::MoeArgs a{};
+  a.x = x;
+  a.k = (int)k;
+  a.f = (int)f;
+  a.experts = (int)experts;
+  a.top = (int)top;
+  a.ids = ids;
+  a.weights = weights;
+  a.form = (int)form;
+  a.w_gu = w_gate_up;
+  a.s_gu = gate_up_scale;
+  a.w_down = w_down;
+  a.s_down = down_scale;
+  a.act = (int)act;
+  a.h = static_cast<uint16_t*>(workspace);
+  a.out = out;
+  return launch_status(sfr::launch_moe_layer(a, m, static_cast<hipStream_t>(stream)));
 }
 
 const char* sfr_status_string(sfr_status s) {

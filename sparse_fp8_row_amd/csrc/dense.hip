@@ -3,7 +3,7 @@
 //                g, u) formed from the accumulators;
 //   input grad   dx = [dg du] [Wg; Wu];
 //   weight grad  dW = [dg du]^T x;
-// and the product with a decoded 4-bit weight.  Bound by the matrix cores for
+// and the products with a decoded 4-bit weight and of 8-bit integers.  Bound by the matrix cores for
 // many rows (4 m k f operations forward, twice that backward), by reading the
 // weight for few.
 #include <type_traits>
@@ -13,7 +13,10 @@
 namespace sfr {
 namespace {
 
-enum { EPI_PLAIN = 0, EPI_GATED = 1 };
+enum { EPI_PLAIN = 0, EPI_GATED = 1, EPI_INT8 = 2 };
+
+template <int EPI>
+using Sum = std::conditional_t<EPI == EPI_INT8, v4i, v4f>;
 
 struct DenseParams {
   const uint16_t *x, *w;
@@ -26,6 +29,7 @@ struct DenseParams {
   float* partial;  // with several slices: binary32 [slices, m, n], summed by dense_reduce_kernel
   PlainOut plain;
   GatedOut gated;
+  Int8Scales scales;  // EPI_INT8: x, w and every count of k stand for pairs of 8-bit integers
 };
 
 // Where this workgroup's outputs go: the output, or its slice's partial sums.
@@ -37,6 +41,9 @@ __device__ __forceinline__ PlainOut plain_of(const DenseParams& p, uint32_t slic
     o.out_fmt = OUT_F32;
   }
   return o;
+}
+__device__ __forceinline__ Int8Scales scales_of(const DenseParams& p) {
+  return p.partial ? Int8Scales{nullptr, nullptr} : p.scales;
 }
 
 // The W operand's loader in the three forms.
@@ -105,11 +112,11 @@ __global__ __launch_bounds__(64 * WN * WM * KS) void dense_tile_kernel(DensePara
       lw.rows.stage(s, kdim - kt * BK);
     }
   };
-  v4f acc[FN][FM];
+  Sum<EPI> acc[FN][FM];
 #pragma unroll
   for (int i = 0; i < FN; ++i)
 #pragma unroll
-    for (int j = 0; j < FM; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < FM; ++j) acc[i][j] = Sum<EPI>{};
 
   if constexpr (FP4) lw.codes.template fetch<0>(kdim);
 #pragma unroll
@@ -139,7 +146,7 @@ __global__ __launch_bounds__(64 * WN * WM * KS) void dense_tile_kernel(DensePara
   wg_barrier();  // every wavefront is done with the stages: their LDS becomes the epilogue's
 
   if constexpr (KS == 2) {
-    v4f* const sums = reinterpret_cast<v4f*>(all_smem + S * STAGE) + wave * (FN * FM * 64) + lane;
+    Sum<EPI>* const sums = reinterpret_cast<Sum<EPI>*>(all_smem + S * STAGE) + wave * (FN * FM * 64) + lane;
     if (kg == 1) {
 #pragma unroll
       for (int i = 0; i < FN; ++i)
@@ -168,6 +175,8 @@ __global__ __launch_bounds__(64 * WN * WM * KS) void dense_tile_kernel(DensePara
       u[1][j] = u1[j];
     }
     gated_epilogue<FM>(g, u, p.gated, mb, n0 + wn * 32, lane, region);
+  } else if constexpr (EPI == EPI_INT8) {
+    int8_epilogue<FM>(acc, scales_of(p), plain_of(p, slice), mb, n0 + wn * 64, lane, region);
   } else {
     plain_epilogue<FM>(acc, plain_of(p, slice), mb, n0 + wn * 64, lane, region);
   }
@@ -238,7 +247,7 @@ __global__ __launch_bounds__(512, 2) void dense_wide_kernel(DenseParams p) {
   const Reader<FP4 ? ROWS : LW, 128, 4> rw(wn * 4, lane);
   const Reader<LX, XR, XFT> rx(wm * XFT, lane);
 
-  v4f acc[WH][XT][4][XFT];
+  Sum<EPI> acc[WH][XT][4][XFT];
 #pragma unroll
   for (int h = 0; h < WH; ++h)
 #pragma unroll
@@ -246,7 +255,7 @@ __global__ __launch_bounds__(512, 2) void dense_wide_kernel(DenseParams p) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < XFT; ++j) acc[h][q][i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < XFT; ++j) acc[h][q][i][j] = Sum<EPI>{};
 
   auto load_x = [&](int t) __attribute__((always_inline)) {
     uint8_t* s = smem + (t & 1) * STAGE + WH * WPART;
@@ -294,7 +303,7 @@ __global__ __launch_bounds__(512, 2) void dense_wide_kernel(DenseParams p) {
   if (wn == 1) wg_barrier();
 
   v8bf w[2][4], x[XT][2][XFT];
-  auto multiply = [&](auto pending, v4f(&c)[XT][4][XFT]) __attribute__((always_inline)) {
+  auto multiply = [&](auto pending, Sum<EPI>(&c)[XT][4][XFT]) __attribute__((always_inline)) {
     wait_vm<pending.value>();
     wait_lds();
     wg_barrier();
@@ -354,7 +363,7 @@ __global__ __launch_bounds__(512, 2) void dense_wide_kernel(DenseParams p) {
 #pragma unroll
     for (int q = 0; q < XT; ++q) {
       const int64_t mb = m0 + q * XR + wm * (XFT * 16);
-      v4f(&a)[4][XFT] = acc[h][q];
+      Sum<EPI>(&a)[4][XFT] = acc[h][q];
       if constexpr (EPI == EPI_GATED) {
         v4f g[2][XFT], u[2][XFT];
 #pragma unroll
@@ -365,30 +374,43 @@ __global__ __launch_bounds__(512, 2) void dense_wide_kernel(DenseParams p) {
           u[1][j] = a[3][j];
         }
         gated_epilogue<XFT>(g, u, p.gated, mb, n0 + h * 64 + wn * 32, lane, region);
+      } else if constexpr (EPI == EPI_INT8) {
+        int8_epilogue<XFT>(a, scales_of(p), plain_of(p, slice), mb, n0 + h * 128 + wn * 64, lane, region);
       } else {
         plain_epilogue<XFT>(a, plain_of(p, slice), mb, n0 + h * 128 + wn * 64, lane, region);
       }
     }
 }
 
-// Sums the slices in order, adds the bias, rounds once.
-__global__ __launch_bounds__(256) void dense_reduce_kernel(const float* __restrict__ partial, int slices, PlainOut o) {
+// Sums the slices in order (V = v4i: exactly, then the scales), adds the bias, rounds once.
+template <class V>
+__global__ __launch_bounds__(256) void dense_reduce_kernel(const float* __restrict__ partial, int slices, PlainOut o,
+                                                           Int8Scales sc) {
   const int64_t quads = o.m * o.n / 4;
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (at >= quads) return;
-  const v4f* p = reinterpret_cast<const v4f*>(partial);
-  v4f s = p[at];
+  const V* p = reinterpret_cast<const V*>(partial);
+  V total = p[at];
   int i = 1;
   for (; i + 4 <= slices; i += 4) {  // four loads in flight
-    const v4f a = p[at + i * quads], b = p[at + (i + 1) * quads], c = p[at + (i + 2) * quads],
+    const V a = p[at + i * quads], b = p[at + (i + 1) * quads], c = p[at + (i + 2) * quads],
               d = p[at + (i + 3) * quads];
-    s += a;
-    s += b;
-    s += c;
-    s += d;
+    total += a;
+    total += b;
+    total += c;
+    total += d;
   }
-  for (; i < slices; ++i) s += p[at + i * quads];
-  if (o.bias) {
+  for (; i < slices; ++i) total += p[at + i * quads];
+  v4f s;
+  if constexpr (std::is_same_v<V, v4i>) {
+    const float xs = sc.x[at * 4 / o.n];
+    const v4f ws = *reinterpret_cast<const v4f*>(sc.w + at * 4 % o.n), bias = bias4(o.bias, at * 4 % o.n);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = int8_value(total[j], xs, ws[j], bias[j]);
+  } else {
+    s = total;
+  }
+  if (std::is_same_v<V, v4f> && o.bias) {
     const uint2 b = *reinterpret_cast<const uint2*>(o.bias + at * 4 % o.n);
     s[0] += bf16_to_f32(b.x & 0xFFFFu);
     s[1] += bf16_to_f32(b.x >> 16);
@@ -572,13 +594,15 @@ hipError_t run_dense(DenseParams p, const Choice& c, void* workspace, hipStream_
   }
   if (e != hipSuccess || c.slices == 1) return e;
   const int64_t quads = p.plain.m * p.plain.n / 4;
-  dense_reduce_kernel<<<dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream>>>(p.partial, c.slices, p.plain);
+  dense_reduce_kernel<Sum<EPI>>
+      <<<dim3((unsigned)((quads + 255) / 256)), dim3(256), 0, stream>>>(p.partial, c.slices, p.plain, p.scales);
   return hipGetLastError();
 }
 
 // The choice of each product, for its launch, its workspace and its name.
 Choice choose_gated(int64_t m, int64_t k, int64_t f) { return choose(m, 2 * f, k, ROWS, ROWS, false); }
 Choice choose_mxfp4(int64_t m, int64_t n, int64_t k) { return choose(m, n, k, ROWS, CODES, true); }
+Choice choose_int8(int64_t m, int64_t n, int64_t k) { return choose(m, n, k / 2, ROWS, ROWS, true); }
 Choice choose_dx(int64_t m, int64_t k, int64_t f2) { return choose(m, k, f2, ROWS, COLS, true); }
 Choice choose_dw(int64_t m, int64_t k, int64_t f2) { return choose(f2, k, m, COLS, COLS, false); }
 
@@ -593,13 +617,19 @@ DenseKernel dense_mxfp4_kernel(int64_t m, int64_t n, int64_t k) { return named(c
 DenseKernel dense_dx_kernel(int64_t m, int64_t k, int64_t f2) { return named(choose_dx(m, k, f2)); }
 DenseKernel dense_dw_kernel(int64_t m, int64_t k, int64_t f2) { return named(choose_dw(m, k, f2)); }
 
+DenseKernel dense_int8_kernel(int64_t m, int64_t n, int64_t k) { return named(choose_int8(m, n, k)); }
+
 double dense_us(int64_t m, int64_t n, int64_t k, bool fp4, bool gated) {
   return choose(m, n, k, ROWS, fp4 ? CODES : ROWS, !gated).us;
 }
 
+double dense_int8_us(int64_t m, int64_t n, int64_t k) { return choose_int8(m, n, k).us; }
+
 // Workspace: the slices' partial sums.
 int64_t dense_nt_workspace_bytes(int64_t m, int64_t n, int64_t k) { return slice_bytes(choose_mxfp4(m, n, k), m, n); }
 int64_t dense_dx_workspace_bytes(int64_t m, int64_t k, int64_t f2) { return slice_bytes(choose_dx(m, k, f2), m, k); }
+
+int64_t dense_int8_workspace_bytes(int64_t m, int64_t n, int64_t k) { return slice_bytes(choose_int8(m, n, k), m, n); }
 
 hipError_t launch_gated_dense(const GatedArgs& a, hipStream_t stream) {
   DenseParams p{};
@@ -627,6 +657,19 @@ hipError_t launch_mxfp4_dense(const StreamArgs& a, void* workspace, hipStream_t 
   p.k = a.k;
   p.plain = PlainOut{a.out, a.bias, a.m, a.rows, a.out_fmt};
   return run_dense<ROWS, CODES, EPI_PLAIN>(p, choose_mxfp4(a.m, a.rows, a.k), workspace, stream);
+}
+
+hipError_t launch_int8_dense(const Int8Args& a, void* workspace, hipStream_t stream) {
+  DenseParams p{};
+  p.x = reinterpret_cast<const uint16_t*>(a.xq);
+  p.w = reinterpret_cast<const uint16_t*>(a.wq);
+  p.ldx = p.ldw = a.k / 2;
+  p.rows_m = a.m;
+  p.rows_n = a.n;
+  p.k = a.k / 2;
+  p.plain = PlainOut{a.out, a.bias, a.m, a.n, a.out_fmt};
+  p.scales = Int8Scales{a.xs, a.ws};
+  return run_dense<ROWS, ROWS, EPI_INT8>(p, choose_int8(a.m, a.n, a.k), workspace, stream);
 }
 
 hipError_t launch_dense_dx(const uint16_t* dgu, const uint16_t* w, int64_t m, int64_t k, int64_t f2, uint16_t* dx,

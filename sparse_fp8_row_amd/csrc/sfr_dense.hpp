@@ -38,6 +38,11 @@ __device__ __forceinline__ void buf_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* ld
   const uint32_t a = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void_t)lds);
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t)(uintptr_t)a, 16, voff, 0, 0, NT ? 2 : 0);
 }
+// One byte per active lane -> one dword in LDS at lds + 4 lane.
+__device__ __forceinline__ void buf_byte_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* lds, int voff) {
+  const uint32_t a = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void_t)lds);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t)(uintptr_t)a, 1, voff, 0, 0, 0);
+}
 constexpr int kPastRange = 0x7FFFFFF0;  // an offset past every descriptor's range
 
 // s_waitcnt with only the vector-memory counter constrained.
@@ -328,6 +333,13 @@ struct Reader {
 __device__ __forceinline__ v4f mfma16(v8bf a, v8bf b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
+// The same 16 bytes per lane as sixteen 8-bit integers, summed exactly: twice
+// the k (64) in the same time.  The kernels that stage bf16 operands carry 8-bit
+// rows as rows of half as many bf16 elements; only this product and the
+// epilogue know the difference.
+__device__ __forceinline__ v4i mfma16(v8bf a, v8bf b, v4i c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(v4i, a), __builtin_bit_cast(v4i, b), c, 0, 0, 0);
+}
 
 // ---------------------------------------------------------------------------
 // Epilogues of a wavefront's block, FM x 16 rows m.  `region`: LDS of its own,
@@ -509,6 +521,57 @@ __device__ __forceinline__ void plain_epilogue(v4f (&acc)[4][FM], const PlainOut
     const int64_t m = m0 + row, n = col + 8 * c;
     if (m < o.m && n < o.n) *reinterpret_cast<uint4*>(out + m * o.n + n) = v;
   }
+}
+
+// Scales of an 8-bit integer product: one per activation row and weight row.
+struct Int8Scales {
+  const float *x, *w;
+};
+
+// An output of an 8-bit integer product from its exact sum, by the same four
+// roundings in every kernel: the sum to binary32, the scales' product, the fused
+// multiply-add with the bias, and the caller's to the output type.
+__device__ __forceinline__ float int8_value(int sum, float xs, float ws, float bias) {
+  return __builtin_fmaf((float)sum, xs * ws, bias);
+}
+
+// Four biases from column n on (n a multiple of 4); zeros (-0, which leaves a
+// product as it is) without one.
+__device__ __forceinline__ v4f bias4(const uint16_t* bias, int64_t n) {
+  if (!bias) return v4f{-0.f, -0.f, -0.f, -0.f};
+  const uint2 b = *reinterpret_cast<const uint2*>(bias + n);
+  return v4f{bf16_to_f32(b.x & 0xFFFFu), bf16_to_f32(b.x >> 16), bf16_to_f32(b.y & 0xFFFFu), bf16_to_f32(b.y >> 16)};
+}
+
+// Columns col .. col + 63 of rows m0 .. from their exact sums.  Rows and columns
+// past the ends take the last one's scales and are not stored.
+template <int FM>
+__device__ __forceinline__ void int8_epilogue(const v4i (&acc)[4][FM], const Int8Scales& sc, PlainOut o, int64_t m0,
+                                              int64_t col, int lane, uint8_t* region) {
+  const int r16 = lane & 15, lg = lane >> 4;
+  if (col >= o.n) return;
+  v4f y[4][FM];
+  if (!sc.x) {  // a slice's partial sums, kept as integers
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int fm = 0; fm < FM; ++fm) y[j][fm] = __builtin_bit_cast(v4f, acc[j][fm]);
+  } else {
+    float xs[FM];
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm) xs[fm] = sc.x[min(m0 + fm * 16 + r16, o.m - 1)];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t n = min(col + 16 * j + 4 * lg, o.n - 4);
+      const v4f ws = *reinterpret_cast<const v4f*>(sc.w + n), b = bias4(o.bias, n);
+#pragma unroll
+      for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[j][fm][i] = int8_value(acc[j][fm][i], xs[fm], ws[i], b[i]);
+    }
+    o.bias = nullptr;
+  }
+  plain_epilogue<FM>(y, o, m0, col, lane, region);
 }
 
 // Slice and tile of workgroup `id` of 8 * ceil(slices * T / 8): XCD id % 8 (each

@@ -133,6 +133,7 @@ struct StreamArgs {
   const uint16_t* bias;
   void* out;
   int out_fmt;
+  const float *xs, *ws;  // ws not null: x and w are 8-bit integers with these scales
 };
 bool stream_rows(int64_t m, int64_t n, int64_t k, bool fp4, bool gated);  // n: weight rows (2 f when gated)
 hipError_t launch_stream(const StreamArgs& a, hipStream_t stream);
@@ -156,7 +157,61 @@ DenseKernel dense_dw_kernel(int64_t m, int64_t k, int64_t f2);
 enum { PRODUCT_GATED = 0, PRODUCT_GATED_SAVING, PRODUCT_DX, PRODUCT_DW, PRODUCT_MXFP4, PRODUCT_MXFP4_GATED };
 DenseKernel block_kernel(int product, int64_t m, int64_t k, int64_t f);
 
+// 8-bit integers with a scale per row: the quantizer, and the product of two
+// quantized matrices (or of a bf16 x, quantized into the workspace first).
+hipError_t launch_quantize_int8(const uint16_t* x, int64_t rows, int64_t cols, int8_t* q, float* scale,
+                                hipStream_t stream);
+struct Int8Args {
+  const uint16_t* x;  // bf16, or null where xq and xs are given
+  const int8_t* xq;
+  const float* xs;
+  const int8_t* wq;
+  const float* ws;
+  const uint16_t* bias;  // may be null
+  void* out;
+  int64_t m, n, k;
+  int out_fmt;
+};
+bool stream_rows_int8(int64_t m, int64_t n, int64_t k);
+double dense_int8_us(int64_t m, int64_t n, int64_t k);
+int64_t dense_int8_workspace_bytes(int64_t m, int64_t n, int64_t k);
+hipError_t launch_int8_dense(const Int8Args& a, void* workspace, hipStream_t stream);
+DenseKernel dense_int8_kernel(int64_t m, int64_t n, int64_t k);
+int64_t int8_workspace_bytes(int64_t m, int64_t n, int64_t k, bool dynamic);
+hipError_t launch_int8(const Int8Args& a, void* workspace, hipStream_t stream);
+DenseKernel int8_kernel(int64_t m, int64_t n, int64_t k, bool dynamic);
+
 int64_t mxfp4_workspace_bytes(int64_t m, int64_t n, int64_t k);  // of the linear layer; the gated block needs none
 hipError_t launch_mxfp4(const StreamArgs& a, void* workspace, hipStream_t stream);
+
+// The mixture of gated feed-forward blocks.
+enum { ROUTE_SOFTMAX = 0, ROUTE_SIGMOID = 1 };
+enum { EXPERT_BF16 = 0, EXPERT_INT8 = 1, EXPERT_FP4 = 2 };
+constexpr int kMoeExperts = 1024, kMoeTop = 16, kMoeTokens = 64;  // most experts, choices; tokens of one pass
+struct RouteArgs {
+  const uint16_t *x, *w;
+  int64_t m;
+  int k, experts;
+  const float* bias;  // may be null
+  int top, score, renormalize;
+  float* logits;   // [m, experts]
+  int32_t* ids;    // [m, top]
+  float* weights;  // [m, top]
+};
+hipError_t launch_moe_route(const RouteArgs& a, hipStream_t stream);
+struct MoeArgs {
+  const uint16_t* x;
+  int m, k, f, experts, top;  // m: tokens of one pass
+  const int32_t* ids;
+  const float* weights;
+  int form;
+  const void *w_gu, *s_gu;      // [experts, 2 f, k]; scales: a float per row (INT8), a byte per 32 (FP4)
+  const void *w_down, *s_down;  // [experts, k, f]
+  int act;
+  uint16_t* h;  // workspace [m, top, f]
+  uint16_t* out;
+};
+int64_t moe_workspace_bytes(int64_t m, int64_t f, int top);
+hipError_t launch_moe_layer(const MoeArgs& a, int64_t m, hipStream_t stream);
 
 }  // namespace sfr

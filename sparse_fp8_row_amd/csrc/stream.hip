@@ -1,6 +1,6 @@
 // Products of a few activation rows with a weight that is read once: the
 // decode forms of the gated block (bf16 or 4-bit weight) and of the 4-bit
-// linear layer.  Bound by reading the weight.
+// linear layer, and the linear layer in 8-bit integers.  Bound by reading the weight.
 //
 // A workgroup owns 16 RT weight rows and up to 16 activation rows (grid y).
 // Its wavefronts take units of UK k in turn and add their binary32 sums in a
@@ -19,18 +19,15 @@
 //     takes codes 8 j .. 8 j + 7, decoded (exactly) to bf16 with the scale applied
 //     by the converter: k = 32 (l / 16) + 8 j ..;
 //   bf16: k = 32 j + 8 (l / 16) ..
+//   8-bit integers (weight and activation): as bf16 rows of half as many elements.
 // Gated: row tiles alternate between gate and up rows, so act(g) * u is
 // formed from the sums before anything is rounded.
+#include <type_traits>
+
 #include "sfr_dense.hpp"
 
 namespace sfr {
 namespace {
-
-// One byte per active lane -> one dword in LDS at lds + 4 lane.
-__device__ __forceinline__ void buf_byte_to_lds(__amdgpu_buffer_rsrc_t r, uint8_t* lds, int voff) {
-  const uint32_t a = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void_t)lds);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_t)(uintptr_t)a, 1, voff, 0, 0, 0);
-}
 
 // R: activation rows in LDS (a power of two, at least the workgroup's).
 template <bool FP4, int RT, int R, int NW, int D>
@@ -47,16 +44,19 @@ struct Stream {
   static_assert((D - 1) * LOADS < 64, "wait counts");
 };
 
-template <bool FP4, bool GATED, int RT, int R, int NW, int D, bool NT>
+template <bool FP4, bool GATED, int RT, int R, int NW, int D, bool NT, bool I8>
 __global__ __launch_bounds__(64 * NW) void stream_kernel(StreamArgs p) {
   using S = Stream<FP4, RT, R, NW, D>;
+  using Sum = std::conditional_t<I8, v4i, v4f>;
+  using Part = std::conditional_t<I8, int, float>;
+  static_assert(!I8 || (!FP4 && !GATED), "8-bit integers: the linear layer");
   static_assert(!GATED || RT % 2 == 0, "row tiles come in pairs");
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, lg = lane >> 4;
   const int64_t m0 = (int64_t)blockIdx.y * 16;
   const int mr = (int)min(p.m - m0, (int64_t)16);
-  const int K = (int)p.k, wrow = FP4 ? K / 2 : K * 2;
+  const int K = (int)(I8 ? p.k / 2 : p.k), wrow = FP4 ? K / 2 : K * 2;
   const int64_t tile0 = (int64_t)blockIdx.x * (GATED ? RT / 2 : RT), tiles = p.rows / 16;
 
   // tiles past the last one read the last one (and are not stored)
@@ -99,9 +99,9 @@ __global__ __launch_bounds__(64 * NW) void stream_kernel(StreamArgs p) {
     }
   };
 
-  v4f acc[RT];
+  Sum acc[RT];
 #pragma unroll
-  for (int t = 0; t < RT; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < RT; ++t) acc[t] = Sum{};
 
   const int units = (K + S::UK - 1) / S::UK;
 #pragma unroll
@@ -147,29 +147,32 @@ __global__ __launch_bounds__(64 * NW) void stream_kernel(StreamArgs p) {
   wait_lds();
   wg_barrier();  // no load in flight, no read pending: the buffers become the sums'
 
-  float* const red = reinterpret_cast<float*>(smem);  // [NW][RT][R][16]
+  Part* const red = reinterpret_cast<Part*>(smem);  // [NW][RT][R][16]
 #pragma unroll
   for (int t = 0; t < RT; ++t)
-    if (r16 < mr) *reinterpret_cast<v4f*>(red + ((wave * RT + t) * R + r16) * 16 + 4 * lg) = acc[t];
+    if (r16 < mr) *reinterpret_cast<Sum*>(red + ((wave * RT + t) * R + r16) * 16 + 4 * lg) = acc[t];
   wait_lds();
   wg_barrier();
   constexpr int OT = GATED ? RT / 2 : RT;
   for (int i = threadIdx.x; i < OT * 16 * mr; i += 64 * NW) {
     const int n = i % 16, t = i / 16 % OT, m = i / (16 * OT);
     const int64_t col = (tile0 + t) * 16 + n;
-    float y = 0.f, u = 0.f;
+    Part sum = 0;
+    float u = 0.f;
 #pragma unroll
     for (int v = 0; v < NW; ++v) {
-      y += red[((v * RT + (GATED ? 2 * t : t)) * R + m) * 16 + n];
+      sum += red[((v * RT + (GATED ? 2 * t : t)) * R + m) * 16 + n];
       if constexpr (GATED) u += red[((v * RT + 2 * t + 1) * R + m) * 16 + n];
     }
+    float y = (float)sum;
     if constexpr (GATED) {
       y = u * (p.act == ACT_SILU        ? act_value<ACT_SILU>(y)
                : p.act == ACT_GELU_TANH ? act_value<ACT_GELU_TANH>(y)
                                         : act_value<ACT_RELU>(y));
     }
     if (col < p.rows) {
-      if (p.bias) y += bf16_to_f32(p.bias[col]);
+      if constexpr (I8) y = int8_value(sum, p.xs[m0 + m], p.ws[col], p.bias ? bf16_to_f32(p.bias[col]) : -0.f);
+      if (!I8 && p.bias) y += bf16_to_f32(p.bias[col]);
       const int64_t at = (m0 + m) * p.rows + col;
       if (p.out_fmt == OUT_F32) static_cast<float*>(p.out)[at] = y;
       else static_cast<uint16_t*>(p.out)[at] = (uint16_t)pack_bf16x2(y, 0.f);
@@ -177,11 +180,11 @@ __global__ __launch_bounds__(64 * NW) void stream_kernel(StreamArgs p) {
   }
 }
 
-template <bool FP4, bool GATED, int RT, int R, int NW, int D, bool NT = false>
+template <bool FP4, bool GATED, int RT, int R, int NW, int D, bool NT = false, bool I8 = false>
 hipError_t run_stream(const StreamArgs& a, hipStream_t stream) {
   constexpr int cover = (GATED ? RT / 2 : RT) * 16, bytes = Stream<FP4, RT, R, NW, D>::BYTES;
   static_assert(bytes <= 160 * 1024, "LDS of a CU");
-  auto* kernel = stream_kernel<FP4, GATED, RT, R, NW, D, NT>;
+  auto* kernel = stream_kernel<FP4, GATED, RT, R, NW, D, NT, I8>;
   if constexpr (bytes > 65536) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -216,6 +219,15 @@ bool stream_rows(int64_t m, int64_t n, int64_t k, bool fp4, bool gated) {
   return 3 + passes * pass <= (tiles > read ? tiles : read);
 }
 
+// The same for 8-bit integers, first taken as the bf16 product of half the k.
+bool stream_rows_int8(int64_t m, int64_t n, int64_t k) {
+  const int64_t passes = (m + 15) / 16;
+  if (m <= 8) return true;
+  if (passes > 8) return false;
+  const double bytes = (double)n * k, pass = bytes / 9e6, tiles = dense_int8_us(m, n, k), read = bytes / 4.8e6 + 3;
+  return 3 + passes * pass <= (tiles > read ? tiles : read);
+}
+
 namespace {
 
 // One form of the kernel, with its name.
@@ -243,6 +255,12 @@ constexpr Form kT1W4{"stream_4bit_t1w4", run_stream<true, false, 1, 16, 4, 2>};
 constexpr Form kT2W4{"stream_4bit_t2w4", run_stream<true, false, 2, 16, 4, 2>};
 constexpr Form kT2W3{"stream_4bit_t2w3", run_stream<true, false, 2, 16, 3, 2>};
 constexpr Form kT2W2{"stream_4bit_t2w2", run_stream<true, false, 2, 16, 2, 2>};
+constexpr Form kI8R2T1W8{"stream_int8_r2_t1w8", run_stream<false, false, 1, 2, 8, 2, false, true>};
+constexpr Form kI8R2T2W4{"stream_int8_r2_t2w4", run_stream<false, false, 2, 2, 4, 2, false, true>};
+constexpr Form kI8R8T1W8{"stream_int8_r8_t1w8", run_stream<false, false, 1, 8, 8, 2, false, true>};
+constexpr Form kI8R8T2W4{"stream_int8_r8_t2w4", run_stream<false, false, 2, 8, 4, 2, false, true>};
+constexpr Form kI8T1W8{"stream_int8_t1w8", run_stream<false, false, 1, 16, 8, 2, false, true>};
+constexpr Form kI8T2W4{"stream_int8_t2w4", run_stream<false, false, 2, 16, 4, 2, false, true>};
 
 // The form of a call.
 //
@@ -267,6 +285,10 @@ constexpr Form kT2W2{"stream_4bit_t2w2", run_stream<true, false, 2, 16, 2, 2>};
 // against 5.7;  gated k = 4096, 16 rows: f = 4096 6.4 against 9.2, f = 8192 10.4, 10.0;
 // k = 704, f = 9248: 8.5, 5.4;  k = 4096, f = 4096, 64 rows: 19.4, 15.5.
 const Form& stream_form(const StreamArgs& a) {
+  if (a.ws) {
+    const bool few = a.rows / 16 * ((a.m + 15) / 16) <= 256;
+    return a.m <= 2 ? (few ? kI8R2T1W8 : kI8R2T2W4) : a.m <= 8 ? (few ? kI8R8T1W8 : kI8R8T2W4) : few ? kI8T1W8 : kI8T2W4;
+  }
   if (!a.w_scale) return a.m <= 2 ? kBf16R2 : a.m <= 8 ? kBf16R8 : a.m <= 16 ? kBf16R16 : kBf16Passes;
   const int64_t tiles = a.rows / 16 * ((a.m + 15) / 16);
   if (a.gated) {
