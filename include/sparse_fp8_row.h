@@ -679,7 +679,7 @@ typedef enum { SFR_EXPERT_BF16 = 0, SFR_EXPERT_INT8 = 1, SFR_EXPERT_MXFP4 = 2 } 
  *     SFR_EXPERT_INT8   codes; scales binary32 [experts, 2 f] and [experts, k].
  *     SFR_EXPERT_MXFP4  two codes a byte; scales bytes [experts, 2 f, k / 32] and
  *                       [experts, k, f / 32].
- *   workspace  device scratch of at least sfr_moe_workspace_bytes(m, f, top) bytes,
+ *   workspace  device scratch of at least sfr_moe_workspace_bytes(m, k, f, top) bytes,
  *              overwritten; calls that may run at the same time need distinct
  *              workspaces.
  * Sizes: 0 <= m <= SFR_MAX_DIM (taken 64 tokens at a time, each reading the weights
@@ -694,7 +694,7 @@ sfr_status moe_layer(const uint16_t* x, int64_t m, int64_t k, const int32_t* ids
                      int64_t workspace_bytes, void* stream);
 
 /* Workspace bytes of moe_layer; 0 for sizes it rejects. */
-int64_t sfr_moe_workspace_bytes(int64_t m, int64_t f, int64_t top);
+int64_t sfr_moe_workspace_bytes(int64_t m, int64_t k, int64_t f, int64_t top);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* sfr_status_string(sfr_status s);

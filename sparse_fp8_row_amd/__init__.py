@@ -120,7 +120,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sfr_int8_kernel.restype = ctypes.c_char_p
     lib.moe_route.argtypes = [P, I64, I64, P, I64, P, I64, I, I, P, P, P, P]
     lib.moe_layer.argtypes = [P, I64, I64, P, P, I64, I64, I64, I, P, P, P, P, I, P, P, I64, P]
-    lib.sfr_moe_workspace_bytes.argtypes = [I64, I64, I64]
+    lib.sfr_moe_workspace_bytes.argtypes = [I64, I64, I64, I64]
     lib.sfr_moe_workspace_bytes.restype = I64
     for fn in (lib.quantize_rowwise_int8, lib.int8_scaled_linear, lib.int8_linear_dynamic, lib.moe_route,
                lib.moe_layer):
@@ -1074,7 +1074,7 @@ def moe_layer(x: torch.Tensor, route: MoeRoute, w_gate_up, w_down, activation: s
         out = torch.empty_like(x)
     top = ids.shape[1]
     lib = load()
-    nbytes = lib.sfr_moe_workspace_bytes(m, f, top)
+    nbytes = lib.sfr_moe_workspace_bytes(m, k, f, top)
     work = x.new_empty((max(nbytes, 16),), dtype=torch.uint8)
     _check(lib.moe_layer(px, m, k, ids.data_ptr(), weights.data_ptr(), top, experts, f, form, pg, pgs, pd, pds, act,
                          out.data_ptr(), work.data_ptr(), nbytes, _raw_stream(device)), "moe_layer")

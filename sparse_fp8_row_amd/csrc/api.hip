@@ -409,9 +409,9 @@ sfr_status moe_route(const uint16_t* x, int64_t m, int64_t k, const uint16_t* w,
   return launch_status(sfr::launch_moe_route(a, static_cast<hipStream_t>(stream)));
 }
 
-int64_t sfr_moe_workspace_bytes(int64_t m, int64_t f, int64_t top) {
-  if (!moe_sizes(m, 1, top) || !gated_dim(f)) return 0;
-  return sfr::moe_workspace_bytes(m, f, (int)top);
+int64_t sfr_moe_workspace_bytes(int64_t m, int64_t k, int64_t f, int64_t top) {
+  if (!moe_sizes(m, 1, top) || !block_dim(k, 32) || !gated_dim(f)) return 0;
+  return sfr::moe_workspace_bytes(m, k, f, (int)top);
 }
 
 sfr_status moe_layer(const uint16_t* x, int64_t m, int64_t k, const int32_t* ids, const float* weights, int64_t top,
@@ -425,7 +425,7 @@ sfr_status moe_layer(const uint16_t* x, int64_t m, int64_t k, const int32_t* ids
   if (!act_ok(act) || form < SFR_EXPERT_BF16 || form > SFR_EXPERT_MXFP4) return SFR_ERR_DTYPE;
   if (!moe_sizes(m, experts, top) || !block_dim(k, 32) || !gated_dim(f)) return SFR_ERR_SHAPE;
   if (m == 0) return SFR_OK;
-  if (workspace_bytes < sfr::moe_workspace_bytes(m, f, (int)top)) return SFR_ERR_SHAPE;
+  if (workspace_bytes < sfr::moe_workspace_bytes(m, k, f, (int)top)) return SFR_ERR_SHAPE;
   const bool scaled = form != SFR_EXPERT_BF16;
   if (!x || !ids || !weights || !w_gate_up || !w_down || !out || !workspace ||
       (scaled && (!gate_up_scale || !down_scale)))

@@ -2,7 +2,10 @@
 // layer
 //     out[t] = sum_s weights[t, s] (act(x[t] Wg[e]^T) * (x[t] Wu[e]^T)) Wd[e]^T,  e = ids[t, s]
 // in two launches.  Bound by reading the chosen experts' weights once.
+#include <type_traits>
+
 #include "sfr_dense.hpp"
+#include "sfr_quant.hpp"
 
 namespace sfr {
 namespace {
@@ -11,25 +14,27 @@ namespace {
 // Router
 // ---------------------------------------------------------------------------
 
-constexpr int kTokens = 4;  // of one workgroup of the logits
-
 // logits[t, e] = x[t] . w[e] + bias[e], summed in binary64 and rounded once to
 // binary32: every product of two bf16 values is exact in binary32, so the sum's
 // rounding (2^-53) is all there is before the last, and which of two nearly equal
 // experts a token takes does not depend on the batch, the tiling or the order.
-__global__ __launch_bounds__(256) void route_logits_kernel(const uint16_t* __restrict__ x, int64_t m, int k,
-                                                           const uint16_t* __restrict__ w, int experts,
-                                                           const float* __restrict__ bias, float* __restrict__ logits) {
-  __shared__ double red[4][kTokens];
+//
+// Few tokens: a workgroup per expert and T tokens, its threads share k.
+constexpr int kFewTokens = 4;
+
+__global__ __launch_bounds__(256) void route_few_kernel(RouteArgs p) {
+  constexpr int T = kFewTokens;
+  __shared__ double red[4][T];
   const int tid = threadIdx.x, e = blockIdx.x;
-  const int64_t t0 = (int64_t)blockIdx.y * kTokens;
-  double sum[kTokens] = {};
-  for (int c = tid; c < k / 8; c += 256) {
-    const uint4 b = reinterpret_cast<const uint4*>(w + (int64_t)e * k)[c];
+  const int64_t t0 = (int64_t)blockIdx.y * T;
+  double sum[T] = {};
+  for (int c = tid; c < p.k / 8; c += 256) {
+    const uint4 b = reinterpret_cast<const uint4*>(p.w + (int64_t)e * p.k)[c];
     const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int t = 0; t < kTokens; ++t) {
-      const uint4 a = reinterpret_cast<const uint4*>(x + min(t0 + t, m - 1) * k)[c];
+    for (int t = 0; t < T; ++t) {
+      if (t0 + t >= p.m) continue;
+      const uint4 a = reinterpret_cast<const uint4*>(p.x + (t0 + t) * p.k)[c];
       const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -39,16 +44,114 @@ __global__ __launch_bounds__(256) void route_logits_kernel(const uint16_t* __res
     }
   }
 #pragma unroll
-  for (int t = 0; t < kTokens; ++t) {
+  for (int t = 0; t < T; ++t) {
 #pragma unroll
     for (int d = 32; d >= 1; d /= 2) sum[t] += __shfl_xor(sum[t], d);
     if ((tid & 63) == 0) red[tid >> 6][t] = sum[t];
   }
   __syncthreads();
-  if (tid < kTokens && t0 + tid < m) {
+  if (tid < T && t0 + tid < p.m) {
     double s = ((red[0][tid] + red[1][tid]) + red[2][tid]) + red[3][tid];
-    if (bias) s += (double)bias[e];
-    logits[(t0 + tid) * experts + e] = (float)s;
+    if (p.bias) s += (double)p.bias[e];
+    p.logits[(t0 + tid) * p.experts + e] = (float)s;
+  }
+}
+
+// More tokens: on v_mfma_f64_16x16x4_f64 (lane l holds A row and B column l % 16 at
+// k l / 16, and rows 4 i + l / 16 of D's column l % 16).  A workgroup owns 16 TB tokens
+// x 16 EB experts and its eight wavefronts an eighth of k each, in steps of 32: a lane
+// loads eight values of each operand, whose j-th go into the j-th instruction (any
+// order of k serves, the same for both).  Bound by the binary64 rate (64 cycles an
+// instruction) and, at a third of that again, by the conversions of its operands.
+// One block a workgroup fills the CUs evenly; from 1024 blocks on 2 x 2, which halves
+// the conversions (k = 4096, logits and choice in a graph, us: 1000 tokens, 161
+// experts 39.6, in 2 x 2 44.0; 1024, 256 49.8, 44.8; 4096, 128 89.9, 78.9).  Up to
+// kFewLogits the form above is faster (96 x 128 16.2, 17.4; 128 x 128 19.1, 17.3; 64 x 128
+// 13.6, 17.3).
+constexpr int64_t kFewLogits = 12288;
+typedef double v4d __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ double bf16_to_f64(const uint4& v, int i) {
+  const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+  return (double)(i & 1 ? __uint_as_float(w & 0xFFFF0000u) : bf16_to_f32(w & 0xFFFFu));
+}
+
+template <int TB, int EB, int NW>  // blocks of 16 tokens and experts, wavefronts
+__global__ __launch_bounds__(64 * NW) void route_many_kernel(RouteArgs p) {
+  constexpr int H = NW / 2;
+  __shared__ v4d red[H][TB * EB][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, lg = lane >> 4;
+  const int e0 = blockIdx.x * 16 * EB;
+  const int64_t t0 = (int64_t)blockIdx.y * 16 * TB;
+  // rows past the ends read the last one (and are not stored)
+  const uint16_t *px[TB], *pw[EB];
+#pragma unroll
+  for (int i = 0; i < TB; ++i) px[i] = p.x + min(t0 + 16 * i + r16, p.m - 1) * p.k + 8 * lg;
+#pragma unroll
+  for (int i = 0; i < EB; ++i) pw[i] = p.w + (int64_t)min(e0 + 16 * i + r16, p.experts - 1) * p.k + 8 * lg;
+  v4d acc[TB][EB];
+#pragma unroll
+  for (int i = 0; i < TB; ++i)
+#pragma unroll
+    for (int j = 0; j < EB; ++j) acc[i][j] = v4d{0, 0, 0, 0};
+  const int steps = p.k / 32;
+  uint4 x[TB], w[EB];
+  auto load = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < TB; ++i) x[i] = *reinterpret_cast<const uint4*>(px[i] + s * 32);
+#pragma unroll
+    for (int i = 0; i < EB; ++i) w[i] = *reinterpret_cast<const uint4*>(pw[i] + s * 32);
+  };
+  if (wave < steps) load(wave);
+  for (int s = wave; s < steps; s += NW) {
+    uint4 a[TB], b[EB];
+#pragma unroll
+    for (int i = 0; i < TB; ++i) a[i] = x[i];
+#pragma unroll
+    for (int i = 0; i < EB; ++i) b[i] = w[i];
+    if (s + NW < steps) load(s + NW);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      double xa[TB], wb[EB];
+#pragma unroll
+      for (int i = 0; i < TB; ++i) xa[i] = bf16_to_f64(a[i], k);
+#pragma unroll
+      for (int i = 0; i < EB; ++i) wb[i] = bf16_to_f64(b[i], k);
+#pragma unroll
+      for (int i = 0; i < TB; ++i)
+#pragma unroll
+        for (int j = 0; j < EB; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f64_16x16x4f64(xa[i], wb[j], acc[i][j], 0, 0, 0);
+    }
+  }
+  // the wavefronts' sums join in a fixed order: w, w + H; then 0 .. H - 1
+  if (wave >= H) {
+#pragma unroll
+    for (int i = 0; i < TB; ++i)
+#pragma unroll
+      for (int j = 0; j < EB; ++j) red[wave - H][i * EB + j][lane] = acc[i][j];
+  }
+  __syncthreads();
+  if (wave < H) {
+#pragma unroll
+    for (int i = 0; i < TB; ++i)
+#pragma unroll
+      for (int j = 0; j < EB; ++j) red[wave][i * EB + j][lane] += acc[i][j];
+  }
+  __syncthreads();
+  for (int b = wave; b < TB * EB; b += NW) {
+    v4d s = red[0][b][lane];
+#pragma unroll
+    for (int h = 1; h < H; ++h) s += red[h][b][lane];
+    const int e = e0 + 16 * (b % EB) + r16;
+    if (e >= p.experts) continue;
+    const double bias = p.bias ? (double)p.bias[e] : -0.0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t t = t0 + 16 * (b / EB) + 4 * i + lg;
+      if (t < p.m) p.logits[t * p.experts + e] = (float)(s[i] + bias);
+    }
   }
 }
 
@@ -61,47 +164,47 @@ __device__ __forceinline__ uint32_t order_of(float v) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// A wavefront per token: `top` rounds of a wavefront-wide maximum over (value,
-// lower index first); lane j then holds the j-th choice.  The weights are formed
-// relative to the best, so no exponential overflows.
+// A wavefront per token: `top` rounds of a wavefront-wide maximum, of whose lanes
+// the lowest expert is taken; lane j then holds the j-th choice.  The weights are
+// formed relative to the best, so no exponential overflows.
 template <int PER>  // experts per lane
-__global__ __launch_bounds__(256) void route_select_kernel(const float* __restrict__ logits, int64_t m, int experts,
-                                                           int top, int score, int renormalize, int32_t* __restrict__ ids,
-                                                           float* __restrict__ weights) {
+__global__ __launch_bounds__(256) void route_select_kernel(RouteArgs a) {
   const int lane = threadIdx.x & 63;
   const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= m) return;
+  if (t >= a.m) return;
+  const int top = a.top, score = a.score;
+  const bool renormalize = a.renormalize;
   float v[PER];
-  uint64_t key[PER];  // order of the value, then of the lower index
+  uint32_t key[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = lane + 64 * i;
-    v[i] = e < experts ? logits[t * experts + e] : -__builtin_inff();
-    const uint32_t o = order_of(v[i]);
-    key[i] = o ? (uint64_t)o << 32 | (uint32_t)~e : 0;
+    v[i] = e < a.experts ? a.logits[t * a.experts + e] : -__builtin_inff();
+    key[i] = order_of(v[i]);
   }
   float chosen = -__builtin_inff(), best = 0.0f;
   int id = -1;
   for (int j = 0; j < top; ++j) {
-    uint64_t k = 0;
+    uint32_t k = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) k = max(k, key[i]);
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) k = max(k, (uint64_t)__shfl_xor((unsigned long long)k, d));
+    k = wave_max(k);
     if (k == 0) break;  // nothing left: lanes j .. keep id -1
-    const int e = (int)~(uint32_t)k;
-    float mine = 0.0f;
+    bool found = false;
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (key[i] == k) {
-        key[i] = 0;
-        mine = v[i];
+    for (int i = 0; i < PER; ++i) {
+      const uint64_t at = __ballot(key[i] == k);
+      if (!found && at != 0) {
+        found = true;
+        const int l = __builtin_ctzll(at);
+        const float value = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v[i]), l));
+        if (lane == l) key[i] = 0;
+        if (j == 0) best = value;
+        if (lane == j) {
+          id = l + 64 * i;
+          chosen = value;
+        }
       }
-    const float value = __shfl(mine, e & 63);
-    if (j == 0) best = value;
-    if (lane == j) {
-      id = e;
-      chosen = value;
     }
   }
   float p = 0.0f, total = 0.0f;
@@ -125,8 +228,8 @@ __global__ __launch_bounds__(256) void route_select_kernel(const float* __restri
     p = id >= 0 ? p / total : 0.0f;
   }
   if (lane < top) {
-    ids[t * top + lane] = id;
-    weights[t * top + lane] = p;
+    a.ids[t * top + lane] = id;
+    a.weights[t * top + lane] = p;
   }
 }
 
@@ -150,31 +253,87 @@ __global__ __launch_bounds__(256) void route_select_kernel(const float* __restri
 //   stays with the tokens that met it.
 // ---------------------------------------------------------------------------
 
-struct Choices {
-  int ids[kMoeTokens * kMoeTop];
-  uint32_t bits[kMoeExperts / 32];  // chosen experts
+// What a workgroup knows of the tokens' choices, in two forms with the same calls.
+// ids outside [0, experts) are no choice.
+//   count          chosen experts
+//   expert(i)      the i-th of them (uniform)
+//   slot(e)        in lane t: token t's first slot with expert e, or -1
+//   weight(e)      in lane t: the sum of its weights over its slots with e
+// Shared is the LDS that a form takes.
+
+// Up to 64 slots in all: a lane holds one (lane = t * top + s), and ballots do the
+// rest, without LDS or a barrier.  Experts in the order of their first slots.
+struct FewChoices {
+  struct Shared {};
+  const MoeArgs& p;
+  int id;
+  float w;
+  uint64_t firsts;  // slots that name an expert first
+  int count;
+  template <bool WEIGHTS>
+  __device__ __forceinline__ FewChoices(const MoeArgs& p_, Shared&, int lane, std::bool_constant<WEIGHTS>)
+      : p(p_), id(-1), w(0.f), firsts(0) {
+    if (lane < p.m * p.top) {
+      const int v = p.ids[lane];
+      if constexpr (WEIGHTS) w = p.weights[lane];
+      if (v >= 0 && v < p.experts) id = v;
+    }
+    for (uint64_t rest = __ballot(id >= 0); rest != 0;) {
+      const int first = __builtin_ctzll(rest);
+      firsts |= (uint64_t)1 << first;
+      rest &= ~__ballot(id == __builtin_amdgcn_readlane(id, first));
+    }
+    count = __popcll(firsts);
+  }
+  __device__ __forceinline__ int expert(int i) const {
+    uint64_t f = firsts;
+    for (; i > 0; --i) f &= f - 1;
+    return __builtin_amdgcn_readlane(id, __builtin_ctzll(f));
+  }
+  // token t's bits of a mask over slots, for lane t
+  __device__ __forceinline__ uint32_t mine(uint64_t slots, int lane) const {
+    return lane < p.m ? (uint32_t)(slots >> (lane * p.top)) & ((1u << p.top) - 1) : 0;
+  }
+  __device__ __forceinline__ int slot(int e, int lane) const {
+    const uint32_t s = mine(__ballot(id == e), lane);
+    return s ? __builtin_ctz(s) : -1;
+  }
+  __device__ __forceinline__ float weight(int e, int lane) const {
+    const uint32_t slots = mine(__ballot(id == e), lane);
+    float sum = 0.f;
+    for (int s = 0; s < p.top; ++s) {
+      const float v = __shfl(w, lane * p.top + s & 63);
+      sum += slots >> s & 1 ? v : 0.f;
+    }
+    return sum;
+  }
 };
 
-// Reads ids: values outside [0, experts) are no choice (-1).
-__device__ __forceinline__ void read_choices(Choices& c, const MoeArgs& p) {
-  for (int i = threadIdx.x; i < kMoeExperts / 32; i += blockDim.x) c.bits[i] = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < p.m * p.top; i += blockDim.x) {
-    const int id = p.ids[i];
-    const bool in = id >= 0 && id < p.experts;
-    c.ids[i] = in ? id : -1;
-    if (in) atomicOr(&c.bits[id / 32], 1u << (id & 31));
-  }
-  __syncthreads();
-}
-
-// The chosen experts in ascending order, found by a wavefront.
-struct Chosen {
+// Any number: ids in LDS, and a bit per chosen expert, whose words a wavefront's
+// lanes then hold.  Experts in ascending order.
+struct ManyChoices {
+  struct Shared {
+    int ids[kMoeTokens * kMoeTop];
+    uint32_t bits[kMoeExperts / 32];
+  };
+  const MoeArgs& p;
+  const int* ids;
   uint32_t word;  // lane l < 32: bits of experts 32 l ..
   int upto;       // chosen experts up to this word's end
   int count;
-  __device__ __forceinline__ Chosen(const Choices& c, int lane) {
+  template <bool WEIGHTS>
+  __device__ __forceinline__ ManyChoices(const MoeArgs& p_, Shared& c, int lane, std::bool_constant<WEIGHTS>)
+      : p(p_), ids(c.ids) {
     static_assert(kMoeExperts <= 64 * 32, "a word per lane");
+    for (int i = threadIdx.x; i < kMoeExperts / 32; i += blockDim.x) c.bits[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.m * p.top; i += blockDim.x) {
+      const int id = p.ids[i];
+      const bool in = id >= 0 && id < p.experts;
+      c.ids[i] = in ? id : -1;
+      if (in) atomicOr(&c.bits[id / 32], 1u << (id & 31));
+    }
+    __syncthreads();
     word = lane < kMoeExperts / 32 ? c.bits[lane] : 0;
     upto = __popc(word);
 #pragma unroll
@@ -184,38 +343,41 @@ struct Chosen {
     }
     count = __builtin_amdgcn_readlane(upto, 63);
   }
-  // The i-th (i < count), uniform.
   __device__ __forceinline__ int expert(int i) const {
-    const uint64_t past = __ballot(upto > i);
-    const int l = __builtin_ctzll(past);
+    const int l = __builtin_ctzll(__ballot(upto > i));
     uint32_t w = (uint32_t)__builtin_amdgcn_readlane((int)word, l);
-    int skip = i - (__builtin_amdgcn_readlane(upto, l) - __popc(w));
-    for (; skip > 0; --skip) w &= w - 1;
+    for (int skip = i - (__builtin_amdgcn_readlane(upto, l) - __popc(w)); skip > 0; --skip) w &= w - 1;
     return 32 * l + __builtin_ctz(w);
+  }
+  __device__ __forceinline__ int slot(int e, int lane) const {
+    int found = -1;
+    if (lane < p.m)
+      for (int s = p.top - 1; s >= 0; --s) found = ids[lane * p.top + s] == e ? s : found;
+    return found;
+  }
+  __device__ __forceinline__ float weight(int e, int lane) const {
+    float sum = 0.f;
+    if (lane < p.m)
+      for (int s = 0; s < p.top; ++s)
+        if (ids[lane * p.top + s] == e) sum += p.weights[lane * p.top + s];
+    return sum;
   }
 };
 
-// Lane t's first slot with expert e, or -1.
-__device__ __forceinline__ int slot_of(const Choices& c, const MoeArgs& p, int e, int t) {
-  int slot = -1;
-  if (t < p.m)
-    for (int s = p.top - 1; s >= 0; --s) slot = c.ids[t * p.top + s] == e ? s : slot;
-  return slot;
-}
-
-// R: activation rows in LDS.
-template <int WF, int RT, int R, int NW, int D>
+// Sizes of a unit: UK_ k of RT weight tiles of 16 rows, and of R activation rows.
+template <int WF, int RT, int R, int UK_>
 struct Unit {
-  static constexpr int UK = WF == EXPERT_BF16 ? 128 : 256;
+  static constexpr int UK = UK_;
   static constexpr int WROW = WF == EXPERT_BF16 ? UK * 2 : WF == EXPERT_INT8 ? UK : UK / 2, XROW = UK * 2;
-  static constexpr int WL = 16 * WROW / 1024, SL = WF == EXPERT_FP4 ? 16 * (UK / 32) / 64 : 0;
+  static constexpr int WL = 16 * WROW / 1024, SL = WF == EXPERT_FP4 ? (16 * (UK / 32) + 63) / 64 : 0;  // loads
   static constexpr int XL = (R * XROW + 1023) / 1024;
-  static constexpr int LOADS = RT * (WL + SL) + XL;
-  static constexpr int TILE = WL * 1024 + SL * 256, BYTES = RT * TILE + XL * 1024;
-  static constexpr int RED = NW * RT * R * 16 * 4;
-  static constexpr int LDS = NW * D * BYTES > RED ? NW * D * BYTES : RED;
-  static_assert((D - 1) * LOADS < 64, "wait counts");
+  static constexpr int TILE = WL * 1024 + SL * 256, WBYTES = RT * TILE, XBYTES = XL * 1024;
+  // 16-byte chunk c of weight row r lies at chunk c ^ swizzle(r): eight rows of one
+  // chunk take the 128 bytes of an LDS cycle once
+  __device__ static __forceinline__ int swizzle(int r) { return WROW >= 128 ? r & 7 : r >> 1 & 3; }
 };
+// k of a unit where a wavefront streams both operands by itself
+constexpr int stream_k(int form) { return form == EXPERT_BF16 ? 128 : 256; }
 
 template <int WF>
 __device__ __forceinline__ int row_bytes(int k) {
@@ -230,13 +392,14 @@ __device__ __forceinline__ void issue_weight(__amdgpu_buffer_rsrc_t rw, __amdgpu
   constexpr int WC = U::WROW / 16, WPL = 64 / WC, PER = U::UK / WC;  // chunks per row, rows per load, k per chunk
 #pragma unroll
   for (int j = 0; j < U::WL; ++j) {
-    const int row = j * WPL + lane / WC, c = (lane % WC) ^ (row & 7);
+    const int row = j * WPL + lane / WC, c = (lane % WC) ^ U::swizzle(row);
     buf_to_lds<NT>(rw, b + j * 1024, c * PER < left ? row * row_bytes<WF>(k) + u * U::WROW + c * 16 : kPastRange);
   }
 #pragma unroll
   for (int j = 0; j < U::SL; ++j) {
-    const int row = j * 8 + (lane >> 3), c = lane & 7;
-    buf_byte_to_lds(rs, b + U::WL * 1024 + j * 256, c * 32 < left ? row * (k / 32) + u * 8 + c : kPastRange);
+    constexpr int BC = U::UK / 32;  // blocks per row
+    const int row = j * (64 / BC) + lane / BC, c = lane % BC;
+    buf_byte_to_lds(rs, b + U::WL * 1024 + j * 256, c * 32 < left ? row * (k / 32) + u * BC + c : kPastRange);
   }
 }
 
@@ -254,11 +417,10 @@ __device__ __forceinline__ v8bf widen8_int8(uint32_t lo, uint32_t hi) {
   return __builtin_bit_cast(v8bf, r);
 }
 
-// acc[t][b] += (weight tile t) (activation rows 16 b ..) over one unit.
+// acc[t][b] += (weight tile t, at w) (activation rows 16 b .., at xb) over one unit.
 template <int WF, int RT, int RB, int R, class U>
-__device__ __forceinline__ void multiply_unit(v4f (&acc)[RT][RB], const uint8_t* b, int lane) {
-  const int r16 = lane & 15, lg = lane >> 4;
-  const uint8_t* const xb = b + RT * U::TILE;
+__device__ __forceinline__ void multiply_unit(v4f (&acc)[RT][RB], const uint8_t* b, const uint8_t* xb, int lane) {
+  const int r16 = lane & 15, lg = lane >> 4, sw = U::swizzle(r16);
 #pragma unroll
   for (int s = 0; s < U::UK / 128; ++s) {
     v8bf x[RB][4];
@@ -277,27 +439,33 @@ __device__ __forceinline__ void multiply_unit(v4f (&acc)[RT][RB], const uint8_t*
       v8bf w[4];
       if constexpr (WF == EXPERT_BF16) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const v8bf*>(wb + 16 * ((4 * j + lg) ^ (r16 & 7)));
+        for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const v8bf*>(wb + 16 * ((4 * j + lg) ^ sw));
       } else if constexpr (WF == EXPERT_INT8) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const v4i q = *reinterpret_cast<const v4i*>(wb + 16 * ((8 * s + 2 * lg + h) ^ (r16 & 7)));
+          const v4i q = *reinterpret_cast<const v4i*>(wb + 16 * ((8 * s + 2 * lg + h) ^ sw));
           w[2 * h] = widen8_int8((uint32_t)q[0], (uint32_t)q[1]);
           w[2 * h + 1] = widen8_int8((uint32_t)q[2], (uint32_t)q[3]);
         }
       } else {
-        const v4i q = *reinterpret_cast<const v4i*>(wb + 16 * ((4 * s + lg) ^ (r16 & 7)));
+        const v4i q = *reinterpret_cast<const v4i*>(wb + 16 * ((4 * s + lg) ^ sw));
         const float f = mx_scale_value(
-            *reinterpret_cast<const uint32_t*>(b + t * U::TILE + U::WL * 1024 + 4 * (r16 * 8 + 4 * s + lg)));
+            *reinterpret_cast<const uint32_t*>(b + t * U::TILE + U::WL * 1024 + 4 * (r16 * (U::UK / 32) + 4 * s + lg)));
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j] = __builtin_bit_cast(v8bf, mx_widen8_e2m1((uint32_t)q[j], f));
       }
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb)
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[t][rb] = mfma16(w[j], x[rb][j], acc[t][rb]);
+        for (int rb = 0; rb < RB; ++rb) acc[t][rb] = mfma16(w[j], x[rb][j], acc[t][rb]);
     }
   }
+}
+
+__device__ __forceinline__ float gate_value(int act, float g) {
+  return act == ACT_SILU        ? act_value<ACT_SILU>(g)
+         : act == ACT_GELU_TANH ? act_value<ACT_GELU_TANH>(g)
+                                : act_value<ACT_RELU>(g);
 }
 
 // Row tile's descriptors: weight rows from `row` on of the stacked experts.
@@ -310,22 +478,31 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t scale_rows(const void* s, int6
   return buf_rsrc(static_cast<const uint8_t*>(s) + (WF == EXPERT_FP4 ? row * (k / 32) : 0), kPastRange);
 }
 
-template <int WF, int RT, int R, int NW, int D, bool NT>
+// LDS of the kernels whose wavefronts stream units by themselves.
+template <int WF, int RT, int R, int NW, int D>
+struct Streamed : Unit<WF, RT, R, stream_k(WF)> {
+  using U = Unit<WF, RT, R, stream_k(WF)>;
+  static constexpr int LOADS = RT * (U::WL + U::SL) + U::XL, BYTES = U::WBYTES + U::XBYTES;
+  static constexpr int RED = NW * RT * R * 16 * 4;
+  static constexpr int LDS = NW * D * BYTES > RED ? NW * D * BYTES : RED;
+  static_assert((D - 1) * LOADS < 64, "wait counts");
+};
+
+template <class C, int WF, int RT, int R, int NW, int D, bool NT>
 __global__ __launch_bounds__(64 * NW) void moe_up_kernel(MoeArgs p) {
-  using U = Unit<WF, RT, R, NW, D>;
+  using U = Unit<WF, RT, R, stream_k(WF)>;
+  using L = Streamed<WF, RT, R, NW, D>;
   static_assert(RT % 2 == 0, "row tiles come in pairs");
   constexpr int RB = (R + 15) / 16;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-  __shared__ Choices choices;
+  __shared__ typename C::Shared shared;
   __shared__ int rows[kMoeTokens], pairs[kMoeTokens];  // the expert's tokens, and their rows of h
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, lg = lane >> 4;
 
-  read_choices(choices, p);
-  const Chosen chosen(choices, lane);
+  const C chosen(p, shared, lane, std::false_type{});
   if ((int)blockIdx.y >= chosen.count) return;
-  const int e = chosen.expert(blockIdx.y);
-  const int slot = slot_of(choices, p, e, lane);
+  const int e = chosen.expert(blockIdx.y), slot = chosen.slot(e, lane);
   const uint64_t takers = __ballot(slot >= 0);
   const int count = __popcll(takers);
   if (wave == 0 && slot >= 0) {
@@ -345,7 +522,7 @@ __global__ __launch_bounds__(64 * NW) void moe_up_kernel(MoeArgs p) {
     rs[t] = scale_rows<WF>(p.s_gu, row, K);
   }
   const __amdgpu_buffer_rsrc_t rx = buf_rsrc(p.x, kPastRange);
-  uint8_t* const mine = smem + wave * (D * U::BYTES);
+  uint8_t* const mine = smem + wave * (D * L::BYTES);
   const int units = (K + U::UK - 1) / U::UK;
   constexpr int XC = U::XROW / 16, XPL = 64 / XC;
 
@@ -358,7 +535,7 @@ __global__ __launch_bounds__(64 * NW) void moe_up_kernel(MoeArgs p) {
       xoff[j] = row < mr ? rows[r0 + row] * (K * 2) + 16 * ((lane % XC) ^ (row & 7)) : kPastRange;
     }
     auto issue = [&](int at, int u) __attribute__((always_inline)) {
-      uint8_t* b = mine + at * U::BYTES;
+      uint8_t* b = mine + at * L::BYTES;
       const int left = K - u * U::UK;  // may be negative: every lane masked
 #pragma unroll
       for (int t = 0; t < RT; ++t) issue_weight<WF, NT, U>(rw[t], rs[t], b + t * U::TILE, u, left, K, lane);
@@ -366,7 +543,7 @@ __global__ __launch_bounds__(64 * NW) void moe_up_kernel(MoeArgs p) {
       for (int j = 0; j < U::XL; ++j) {
         const int c = (lane % XC) ^ ((j * XPL + lane / XC) & 7);
         const bool in = c * 8 < left && xoff[j] != kPastRange;
-        buf_to_lds(rx, b + RT * U::TILE + j * 1024, in ? xoff[j] + u * U::XROW : kPastRange);
+        buf_to_lds(rx, b + U::WBYTES + j * 1024, in ? xoff[j] + u * U::XROW : kPastRange);
       }
     };
     v4f acc[RT][RB];
@@ -380,9 +557,9 @@ __global__ __launch_bounds__(64 * NW) void moe_up_kernel(MoeArgs p) {
     for (int u = wave; u < units; u += NW) {
       wait_lds();  // the buffer to be refilled has been read
       issue(at == 0 ? D - 1 : at - 1, u + (D - 1) * NW);
-      wait_vm<(D - 1) * U::LOADS>();
+      wait_vm<(D - 1) * L::LOADS>();
       asm volatile("" ::: "memory");
-      multiply_unit<WF, RT, RB, R, U>(acc, mine + at * U::BYTES, lane);
+      multiply_unit<WF, RT, RB, R, U>(acc, mine + at * L::BYTES, mine + at * L::BYTES + U::WBYTES, lane);
       at = at == D - 1 ? 0 : at + 1;
     }
     wait_vm<0>();
@@ -414,9 +591,7 @@ __global__ __launch_bounds__(64 * NW) void moe_up_kernel(MoeArgs p) {
         g *= s[0];
         u *= s[p.f];
       }
-      const float h = u * (p.act == ACT_SILU        ? act_value<ACT_SILU>(g)
-                           : p.act == ACT_GELU_TANH ? act_value<ACT_GELU_TANH>(g)
-                                                    : act_value<ACT_RELU>(g));
+      const float h = u * gate_value(p.act, g);
       p.h[(int64_t)pairs[r0 + r] * p.f + col] = (uint16_t)pack_bf16x2(h, 0.f);
     }
     if (r0 + R < count) {
@@ -426,23 +601,23 @@ __global__ __launch_bounds__(64 * NW) void moe_up_kernel(MoeArgs p) {
   }
 }
 
-template <int WF, int RT, int R, int NW, int D, bool NT>
+template <class C, int WF, int RT, int R, int NW, int D, bool NT>
 __global__ __launch_bounds__(64 * NW) void moe_down_kernel(MoeArgs p) {
-  using U = Unit<WF, RT, R, NW, D>;
+  using U = Unit<WF, RT, R, stream_k(WF)>;
+  using L = Streamed<WF, RT, R, NW, D>;
   constexpr int RB = (R + 15) / 16;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-  __shared__ Choices choices;
+  __shared__ typename C::Shared shared;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, lg = lane >> 4;
   const int F = p.f, tile0 = blockIdx.x * RT, tiles = p.k / 16;
 
-  read_choices(choices, p);
-  const Chosen chosen(choices, lane);
+  const C chosen(p, shared, lane, std::true_type{});
   const int each = (F + U::UK - 1) / U::UK, units = chosen.count * each;
   const int share = (units + NW - 1) / NW, first = min(wave * share, units), last = min(first + share, units);
 
   const __amdgpu_buffer_rsrc_t rh = buf_rsrc(p.h, kPastRange);
-  uint8_t* const mine = smem + wave * (D * U::BYTES);
+  uint8_t* const mine = smem + wave * (D * L::BYTES);
   constexpr int XC = U::XROW / 16, XPL = 64 / XC;
   __amdgpu_buffer_rsrc_t rw[RT], rs[RT];
   int hoff[U::XL];
@@ -455,7 +630,7 @@ __global__ __launch_bounds__(64 * NW) void moe_down_kernel(MoeArgs p) {
       rw[t] = weight_rows<WF>(p.w_down, row, F);
       rs[t] = scale_rows<WF>(p.s_down, row, F);
     }
-    const int slot = slot_of(choices, p, e, lane);
+    const int slot = chosen.slot(e, lane);
     const int pair = slot < 0 ? -1 : lane * p.top + slot;
 #pragma unroll
     for (int j = 0; j < U::XL; ++j) {
@@ -471,7 +646,7 @@ __global__ __launch_bounds__(64 * NW) void moe_down_kernel(MoeArgs p) {
   }
   // Puts the next unit in flight; past the wavefront's last, loads that are all masked.
   auto issue = [&](int at) __attribute__((always_inline)) {
-    uint8_t* b = mine + at * U::BYTES;
+    uint8_t* b = mine + at * L::BYTES;
     if (next < last && unit_in == each) {
       ++expert_in;
       unit_in = 0;
@@ -484,7 +659,7 @@ __global__ __launch_bounds__(64 * NW) void moe_down_kernel(MoeArgs p) {
     for (int j = 0; j < U::XL; ++j) {
       const int c = (lane % XC) ^ ((j * XPL + lane / XC) & 7);
       const bool in = c * 8 < left && hoff[j] != kPastRange;
-      buf_to_lds(rh, b + RT * U::TILE + j * 1024, in ? hoff[j] + unit_in * U::XROW : kPastRange);
+      buf_to_lds(rh, b + U::WBYTES + j * 1024, in ? hoff[j] + unit_in * U::XROW : kPastRange);
     }
     ++next;
     ++unit_in;
@@ -503,21 +678,14 @@ __global__ __launch_bounds__(64 * NW) void moe_down_kernel(MoeArgs p) {
     for (int u = first; u < last; ++u) {
       wait_lds();  // the buffer to be refilled has been read
       issue(at == 0 ? D - 1 : at - 1);
-      wait_vm<(D - 1) * U::LOADS>();
+      wait_vm<(D - 1) * L::LOADS>();
       asm volatile("" ::: "memory");
-      multiply_unit<WF, RT, RB, R, U>(acc, mine + at * U::BYTES, lane);
+      multiply_unit<WF, RT, RB, R, U>(acc, mine + at * L::BYTES, mine + at * L::BYTES + U::WBYTES, lane);
       at = at == D - 1 ? 0 : at + 1;
       if (++unit_at == each || u + 1 == last) {  // the expert's end, or this share's
         const int e = chosen.expert(expert_at);
-        float weight = 0.f;  // lane t: token t's, over all its slots with this expert
-        bool taker = false;
-        if (lane < p.m)
-          for (int s = 0; s < p.top; ++s)
-            if (choices.ids[lane * p.top + s] == e) {
-              weight += p.weights[lane * p.top + s];
-              taker = true;
-            }
-        const uint64_t takers = __ballot(taker);
+        const float weight = chosen.weight(e, lane);
+        const uint64_t takers = __ballot(chosen.slot(e, lane) >= 0);
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
           const int col = 16 * b + r16;
@@ -564,6 +732,193 @@ __global__ __launch_bounds__(64 * NW) void moe_down_kernel(MoeArgs p) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// More tokens: a workgroup owns NW wavefronts' weight tiles of one expert and all
+// of k, and its wavefronts share the expert's activation rows, gathered: each
+// puts its own weight tiles and a share of the activation in flight, D - 1 units
+// ahead, and one barrier a unit publishes them.  The number of 16-row blocks of
+// the expert's tokens picks the loop (NB), and with it how many units fit LDS.
+// The groups of NW wavefronts' tiles of all chosen experts are split evenly, in
+// order, over as many workgroups as the CUs hold, which keep units in flight
+// from one group to the next.
+//
+// Up: RT / 2 pairs of gate and up tiles a wavefront; h as above.
+// Down: RT tiles of 16 columns; weight times the sums go to the workspace in
+//   binary32, a row per (token, first slot of the expert), which
+//   moe_combine_kernel adds in the order of the slots: a token's result then
+//   depends on nothing but the token.
+// ---------------------------------------------------------------------------
+struct TileShared {
+  int rows[kMoeTokens], pairs[kMoeTokens];  // the expert's tokens, and their rows of h
+  float weights[kMoeTokens];                // DOWN: over all the token's slots with the expert
+};
+
+template <int WF, bool DOWN, int RT, int NW, int UK, int POOL, int NB, bool NT>
+__device__ __forceinline__ void moe_tiles(const MoeArgs& p, const TileShared& sh, int e, int count, int g0, int g1,
+                                          uint8_t* smem, int lane, int wave) {
+  using U = Unit<WF, RT, 16 * NB, UK>;
+  // every wavefront the same number of the activation's loads; those past its end write zeros
+  constexpr int XL = (U::XL + NW - 1) / NW, LOADS = RT * (U::WL + U::SL) + XL, STAGE = NW * (U::WBYTES + XL * 1024);
+  constexpr int D = POOL / STAGE < 6 ? POOL / STAGE : 6;
+  static_assert(D >= 2 && (D - 2) * LOADS < 64, "units in LDS, wait counts");
+  const int r16 = lane & 15, lg = lane >> 4;
+  const int K = DOWN ? p.f : p.k, N = DOWN ? p.k : p.f;  // N: columns of the result
+  constexpr int CT = DOWN ? RT : RT / 2;                 // its tiles of a wavefront
+  const int tiles = N / 16;
+  __amdgpu_buffer_rsrc_t rw[RT], rs[RT];
+  // the tiles of group g; past the last one, the last one again (and not stored)
+  auto enter = [&](int g) __attribute__((always_inline)) {
+    const int tile0 = (g * NW + wave) * CT;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const int64_t row = DOWN ? (int64_t)e * N + min(tile0 + t, tiles - 1) * 16
+                               : (int64_t)e * 2 * N + min(tile0 + t / 2, tiles - 1) * 16 + (t & 1 ? N : 0);
+      rw[t] = weight_rows<WF>(DOWN ? p.w_down : p.w_gu, row, K);
+      rs[t] = scale_rows<WF>(DOWN ? p.s_down : p.s_gu, row, K);
+    }
+  };
+  const __amdgpu_buffer_rsrc_t rx = buf_rsrc(DOWN ? p.h : p.x, kPastRange);
+  const int units = (K + U::UK - 1) / U::UK;
+  constexpr int XC = U::XROW / 16, XPL = 64 / XC;
+  int xoff[XL];
+#pragma unroll
+  for (int j = 0; j < XL; ++j) {
+    const int row = (wave * XL + j) * XPL + lane / XC;
+    xoff[j] = row < count ? (DOWN ? sh.pairs : sh.rows)[row] * (K * 2) + 16 * ((lane % XC) ^ (row & 7)) : kPastRange;
+  }
+  int group_in = g0, unit_in = 0;  // what is put in flight next
+  enter(g0);
+  auto issue = [&](int at) __attribute__((always_inline)) {
+    if (unit_in == units && group_in + 1 < g1) {
+      ++group_in;
+      unit_in = 0;
+      enter(group_in);
+    }
+    uint8_t* const b = smem + at * STAGE;
+    const int left = K - unit_in * U::UK;  // not positive past the last unit: every lane masked
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+      issue_weight<WF, NT, U>(rw[t], rs[t], b + wave * U::WBYTES + t * U::TILE, unit_in, left, K, lane);
+#pragma unroll
+    for (int j = 0; j < XL; ++j) {
+      const int row = (wave * XL + j) * XPL + lane / XC, c = (lane % XC) ^ (row & 7);
+      const bool in = c * 8 < left && xoff[j] != kPastRange;
+      buf_to_lds(rx, b + NW * U::WBYTES + (wave * XL + j) * 1024, in ? xoff[j] + unit_in * U::XROW : kPastRange);
+    }
+    ++unit_in;
+  };
+#pragma unroll
+  for (int i = 0; i < D - 1; ++i) issue(i);
+  int at = 0;
+  for (int g = g0; g < g1; ++g) {
+    v4f acc[RT][NB];
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) acc[t][b] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int u = 0; u < units; ++u) {
+      wait_vm<(D - 2) * LOADS>();  // the oldest unit of this wavefront in flight has landed
+      wait_lds();                  // and its reads of the stage to be refilled are done
+      wg_barrier();
+      issue(at == 0 ? D - 1 : at - 1);
+      const uint8_t* const b = smem + at * STAGE;
+      multiply_unit<WF, RT, NB, 16 * NB, U>(acc, b + wave * U::WBYTES, b + NW * U::WBYTES, lane);
+      at = at == D - 1 ? 0 : at + 1;
+    }
+    // rows of the result: lane r16 of block b, four columns from 4 lg on
+    const int tile0 = (g * NW + wave) * CT;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int r = 16 * b + r16;
+      if (r >= count) continue;
+      const int64_t pair = sh.pairs[r];
+#pragma unroll
+      for (int t = 0; t < CT; ++t) {
+        if (tile0 + t >= tiles) continue;
+        const int col = (tile0 + t) * 16 + 4 * lg;
+        if constexpr (DOWN) {
+          v4f y = acc[t][b];
+          if constexpr (WF == EXPERT_INT8)
+            y *= *reinterpret_cast<const v4f*>(static_cast<const float*>(p.s_down) + (int64_t)e * N + col);
+          *reinterpret_cast<v4f*>(p.y + pair * N + col) = y * sh.weights[r];
+        } else {
+          v4f g4 = acc[2 * t][b], v = acc[2 * t + 1][b];
+          if constexpr (WF == EXPERT_INT8) {
+            const float* s = static_cast<const float*>(p.s_gu) + (int64_t)e * 2 * N + col;
+            g4 *= *reinterpret_cast<const v4f*>(s);
+            v *= *reinterpret_cast<const v4f*>(s + N);
+          }
+          float h[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[i] = gate_value(p.act, g4[i]) * v[i];
+          *reinterpret_cast<uint2*>(p.h + pair * N + col) =
+              make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
+        }
+      }
+    }
+  }
+  wait_vm<0>();  // the loads past the last unit (zeros) end before the LDS is used for anything else
+}
+
+template <int WF, bool DOWN, int RT, int NW, int UK, int POOL, bool NT>
+__global__ __launch_bounds__(64 * NW) void moe_tile_kernel(MoeArgs p) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  __shared__ ManyChoices::Shared shared;
+  __shared__ TileShared sh;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const ManyChoices chosen(p, shared, lane, std::bool_constant<DOWN>{});
+  constexpr int cover = NW * (DOWN ? RT : RT / 2) * 16;
+  const int groups = ((DOWN ? p.k : p.f) + cover - 1) / cover, tasks = chosen.count * groups;
+  const int share = (tasks + gridDim.x - 1) / gridDim.x, last = min((int)(blockIdx.x + 1) * share, tasks);
+  for (int task = blockIdx.x * share; task < last;) {
+    const int i = task / groups, g0 = task - i * groups, g1 = min(groups, g0 + last - task);
+    task += g1 - g0;
+    const int e = chosen.expert(i), slot = chosen.slot(e, lane);
+    const uint64_t takers = __ballot(slot >= 0);
+    __syncthreads();  // the expert before is done with its lists and the stages
+    if (wave == 0) {
+      const float w = DOWN ? chosen.weight(e, lane) : 0.f;
+      if (slot >= 0) {
+        const int r = __popcll(takers & (((uint64_t)1 << lane) - 1));
+        sh.rows[r] = lane;
+        sh.pairs[r] = lane * p.top + slot;
+        sh.weights[r] = w;
+      }
+    }
+    __syncthreads();
+    const int count = __popcll(takers);
+    if (count <= 16) moe_tiles<WF, DOWN, RT, NW, UK, POOL, 1, NT>(p, sh, e, count, g0, g1, smem, lane, wave);
+    else if (count <= 32) moe_tiles<WF, DOWN, RT, NW, UK, POOL, 2, NT>(p, sh, e, count, g0, g1, smem, lane, wave);
+    else if (count <= 48) moe_tiles<WF, DOWN, RT, NW, UK, POOL, 3, NT>(p, sh, e, count, g0, g1, smem, lane, wave);
+    else moe_tiles<WF, DOWN, RT, NW, UK, POOL, 4, NT>(p, sh, e, count, g0, g1, smem, lane, wave);
+  }
+}
+
+// out[t] = the sum of its experts' parts in the order of the slots, rounded once.
+__global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs p) {
+  const int t = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= p.k / 4) return;
+  const int32_t* const ids = p.ids + t * p.top;
+  uint32_t firsts = 0;  // slots that name an expert first
+  for (int i = 0; i < p.top; ++i) {
+    const int e = ids[i];
+    bool first = e >= 0 && e < p.experts;
+    for (int j = 0; j < i; ++j) first = first && ids[j] != e;
+    firsts |= (uint32_t)first << i;
+  }
+  const v4f* const y = reinterpret_cast<const v4f*>(p.y + (int64_t)t * p.top * p.k) + c;
+  v4f s = v4f{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < p.top; i += 4) {  // four loads in flight
+    v4f v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] = firsts >> (i + j) & 1 ? y[(int64_t)(i + j) * (p.k / 4)] : v4f{-0.f, -0.f, -0.f, -0.f};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s += v[j];
+  }
+  reinterpret_cast<uint2*>(p.out + (int64_t)t * p.k)[c] = make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
+}
+
 template <class K>
 hipError_t allow_lds(K* kernel, int bytes) {
   return bytes > 49152 ? hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
@@ -571,13 +926,17 @@ hipError_t allow_lds(K* kernel, int bytes) {
                        : hipSuccess;
 }
 
-constexpr int kLdsLeft = 160 * 1024 - (int)sizeof(Choices) - 2 * kMoeTokens * 4;
+int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
 
-template <int WF, int RT, int R, int NW, int D, bool NT>
-hipError_t run_up(const MoeArgs& p, hipStream_t stream) {
-  constexpr int bytes = Unit<WF, RT, R, NW, D>::LDS, cover = RT / 2 * 16;
+constexpr int kLdsLeft = 160 * 1024 - (int)sizeof(ManyChoices::Shared) - (int)sizeof(TileShared);
+// Whether the layer is two launches of the streaming kernels, or three of the tiled ones.
+bool streamed(int64_t m, int top) { return m <= 2 || (m <= 8 && top <= 4); }
+
+template <class C, int WF, int RT, int R, int NW, int D, bool NT>
+hipError_t run_up_with(const MoeArgs& p, hipStream_t stream) {
+  constexpr int bytes = Streamed<WF, RT, R, NW, D>::LDS, cover = RT / 2 * 16;
   static_assert(bytes <= kLdsLeft, "LDS of a CU");
-  auto* kernel = moe_up_kernel<WF, RT, R, NW, D, NT>;
+  auto* kernel = moe_up_kernel<C, WF, RT, R, NW, D, NT>;
   const hipError_t e = allow_lds(kernel, bytes);
   if (e != hipSuccess) return e;
   const dim3 grid((unsigned)((p.f + cover - 1) / cover), (unsigned)min(p.experts, p.m * p.top));
@@ -585,57 +944,109 @@ hipError_t run_up(const MoeArgs& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int WF, int RT, int R, int NW, int D, bool NT>
-hipError_t run_down(const MoeArgs& p, hipStream_t stream) {
-  constexpr int bytes = Unit<WF, RT, R, NW, D>::LDS, cover = RT * 16;
+template <class C, int WF, int RT, int R, int NW, int D, bool NT>
+hipError_t run_down_with(const MoeArgs& p, hipStream_t stream) {
+  constexpr int bytes = Streamed<WF, RT, R, NW, D>::LDS, cover = RT * 16;
   static_assert(bytes <= kLdsLeft, "LDS of a CU");
-  auto* kernel = moe_down_kernel<WF, RT, R, NW, D, NT>;
+  auto* kernel = moe_down_kernel<C, WF, RT, R, NW, D, NT>;
   const hipError_t e = allow_lds(kernel, bytes);
   if (e != hipSuccess) return e;
   kernel<<<dim3((unsigned)((p.k + cover - 1) / cover)), dim3(64 * NW), bytes, stream>>>(p);
   return hipGetLastError();
 }
 
+template <int WF, int RT, int R, int NW, int D, bool NT>
+hipError_t run_up(const MoeArgs& p, hipStream_t stream) {
+  return p.m * p.top <= 64 ? run_up_with<FewChoices, WF, RT, R, NW, D, NT>(p, stream)
+                           : run_up_with<ManyChoices, WF, RT, R, NW, D, NT>(p, stream);
+}
+template <int WF, int RT, int R, int NW, int D, bool NT>
+hipError_t run_down(const MoeArgs& p, hipStream_t stream) {
+  return p.m * p.top <= 64 ? run_down_with<FewChoices, WF, RT, R, NW, D, NT>(p, stream)
+                           : run_down_with<ManyChoices, WF, RT, R, NW, D, NT>(p, stream);
+}
+
+template <int WF, bool DOWN, int RT, int NW, int UK, int POOL, bool NT>
+hipError_t run_tile(const MoeArgs& p, hipStream_t stream) {
+  constexpr int cover = NW * (DOWN ? RT : RT / 2) * 16;
+  static_assert(POOL <= kLdsLeft, "LDS of a CU");
+  auto* kernel = moe_tile_kernel<WF, DOWN, RT, NW, UK, POOL, NT>;
+  const hipError_t e = allow_lds(kernel, POOL);
+  if (e != hipSuccess) return e;
+  // as many workgroups as the CUs hold, fewer where there are not so many groups of tiles
+  const int n = DOWN ? p.k : p.f, most = min(p.experts, p.m * p.top) * ((n + cover - 1) / cover);
+  constexpr int fit = 256 * (160 * 1024 / (POOL + (int)sizeof(ManyChoices::Shared) + (int)sizeof(TileShared)));
+  kernel<<<dim3((unsigned)min(most, fit)), dim3(64 * NW), POOL, stream>>>(p);
+  return hipGetLastError();
+}
+
 template <int WF>
 hipError_t run_layer(const MoeArgs& p, hipStream_t stream) {
-  hipError_t e = p.m <= 2    ? run_up<WF, 2, 2, 3, 2, true>(p, stream)
-                 : p.m <= 8  ? run_up<WF, 2, 8, 3, 2, true>(p, stream)
-                 : p.m <= 16 ? run_up<WF, 2, 16, 3, 2, true>(p, stream)
-                             : run_up<WF, 2, 32, 2, 2, false>(p, stream);
+  if (!streamed(p.m, p.top)) {
+    constexpr int pool = 148 * 1024;
+    hipError_t e;
+    if constexpr (WF == EXPERT_BF16) {
+      e = run_tile<WF, false, 2, 4, 128, pool, false>(p, stream);
+      if (e == hipSuccess) e = run_tile<WF, true, 2, 4, 128, pool, false>(p, stream);
+    } else if constexpr (WF == EXPERT_INT8) {
+      e = run_tile<WF, false, 4, 4, 128, pool, false>(p, stream);
+      if (e == hipSuccess) e = run_tile<WF, true, 1, 8, 128, pool, false>(p, stream);
+    } else {
+      e = run_tile<WF, false, 2, 8, 256, pool, false>(p, stream);
+      if (e == hipSuccess) e = run_tile<WF, true, 1, 8, 256, pool, false>(p, stream);
+    }
+    if (e != hipSuccess) return e;
+    moe_combine_kernel<<<dim3((unsigned)((p.k / 4 + 255) / 256), (unsigned)p.m), dim3(256), 0, stream>>>(p);
+    return hipGetLastError();
+  }
+  const hipError_t e = p.m > 2 ? run_up<WF, 2, 8, WF == EXPERT_FP4 ? 2 : 3, 2, true>(p, stream)
+                       : p.k >= 16 * stream_k(WF) ? run_up<WF, 2, 2, 4, 2, true>(p, stream)
+                                                  : run_up<WF, 2, 2, 2, 2, true>(p, stream);
   if (e != hipSuccess) return e;
-  return p.m <= 2    ? run_down<WF, 1, 2, 8, 2, true>(p, stream)
-         : p.m <= 8  ? run_down<WF, 1, 8, 6, 2, true>(p, stream)
-         : p.m <= 16 ? run_down<WF, 1, 16, 4, 2, true>(p, stream)
-         : p.m <= 32 ? run_down<WF, 1, 32, 2, 2, true>(p, stream)
-                     : run_down<WF, 1, 64, 2, 2, true>(p, stream);
+  return p.m <= 2 ? run_down<WF, 1, 2, 12, 2, true>(p, stream) : run_down<WF, 1, 8, 8, 2, true>(p, stream);
+}
+
+template <int TB, int EB>
+void run_many(const RouteArgs& a, hipStream_t stream) {
+  for (int64_t t = 0; t < a.m; t += 65535 * 16 * TB) {  // grid y
+    RouteArgs p = a;
+    p.x = a.x + t * a.k;
+    p.logits = a.logits + t * a.experts;
+    p.m = a.m - t;
+    const int64_t groups = (p.m + 16 * TB - 1) / (16 * TB);
+    const dim3 grid((unsigned)((a.experts + 16 * EB - 1) / (16 * EB)), (unsigned)(groups < 65535 ? groups : 65535));
+    route_many_kernel<TB, EB, 8><<<grid, dim3(512), 0, stream>>>(p);
+  }
 }
 
 }  // namespace
 
 hipError_t launch_moe_route(const RouteArgs& a, hipStream_t stream) {
-  const int64_t groups = (a.m + kTokens - 1) / kTokens;
-  for (int64_t g = 0; g < groups; g += 65535) {  // grid y
-    const int64_t t = g * kTokens, n = groups - g < 65535 ? groups - g : 65535;
-    route_logits_kernel<<<dim3(a.experts, (unsigned)n), dim3(256), 0, stream>>>(
-        a.x + t * a.k, a.m - t, a.k, a.w, a.experts, a.bias, a.logits + t * a.experts);
-  }
+  const int64_t blocks = ((a.m + 15) / 16) * ((a.experts + 15) / 16);
+  if (a.m * a.experts <= kFewLogits)
+    route_few_kernel<<<dim3(a.experts, (unsigned)((a.m + kFewTokens - 1) / kFewTokens)), dim3(256), 0, stream>>>(a);
+  else if (blocks < 1024) run_many<1, 1>(a, stream);
+  else run_many<2, 2>(a, stream);
   const dim3 grid((unsigned)((a.m + 3) / 4)), block(256);
   auto* select = a.experts <= 64    ? route_select_kernel<1>
                  : a.experts <= 128 ? route_select_kernel<2>
                  : a.experts <= 256 ? route_select_kernel<4>
                                     : route_select_kernel<kMoeExperts / 64>;
-  select<<<grid, block, 0, stream>>>(a.logits, a.m, a.experts, a.top, a.score, a.renormalize, a.ids, a.weights);
+  select<<<grid, block, 0, stream>>>(a);
   return hipGetLastError();
 }
 
-// h of the tokens of one pass
-int64_t moe_workspace_bytes(int64_t m, int64_t f, int top) {
-  return (m < kMoeTokens ? m : kMoeTokens) * top * f * 2;
+// Workspace: h of the tokens of one pass, bf16; the experts' parts of their results, binary32.
+int64_t moe_workspace_bytes(int64_t m, int64_t k, int64_t f, int top) {
+  const int64_t pairs = (m < kMoeTokens ? m : kMoeTokens) * top;
+  return align256(pairs * f * 2) + (streamed(m, top) ? 0 : pairs * k * 4);
 }
 
 // kMoeTokens tokens at a time (a lane of a wavefront each).
 hipError_t launch_moe_layer(const MoeArgs& args, int64_t m, hipStream_t stream) {
   MoeArgs p = args;
+  p.y = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.h) +
+                                 align256((m < kMoeTokens ? m : kMoeTokens) * p.top * p.f * 2));
   for (int64_t t = 0; t < m; t += kMoeTokens) {
     p.m = (int)(m - t < kMoeTokens ? m - t : kMoeTokens);
     p.x = args.x + t * p.k;

@@ -209,9 +209,10 @@ struct MoeArgs {
   const void *w_down, *s_down;  // [experts, k, f]
   int act;
   uint16_t* h;  // workspace [m, top, f]
+  float* y;     // workspace [m, top, k]
   uint16_t* out;
 };
-int64_t moe_workspace_bytes(int64_t m, int64_t f, int top);
+int64_t moe_workspace_bytes(int64_t m, int64_t k, int64_t f, int top);
 hipError_t launch_moe_layer(const MoeArgs& a, int64_t m, hipStream_t stream);
 
 }  // namespace sfr
