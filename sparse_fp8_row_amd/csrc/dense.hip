@@ -42,9 +42,16 @@ __device__ __forceinline__ PlainOut plain_of(const DenseParams& p, uint32_t slic
   }
   return o;
 }
-__device__ __forceinline__ Int8Scales scales_of(const DenseParams& p) {
-  return p.partial ? Int8Scales{nullptr, nullptr} : p.scales;
-}
+
+// A workgroup's scales in LDS (EPI_INT8), nothing otherwise.
+template <int EPI, int BM, int BN>
+struct TileScales {
+  Int8Tile<BM, BN> t;
+};
+template <int BM, int BN>
+struct TileScales<EPI_PLAIN, BM, BN> {};
+template <int BM, int BN>
+struct TileScales<EPI_GATED, BM, BN> {};
 
 // The W operand's loader in the three forms.
 template <int LW, int BR, int NW, bool PAIR, int DEPTH = 1>
@@ -118,10 +125,16 @@ __global__ __launch_bounds__(64 * WN * WM * KS) void dense_tile_kernel(DensePara
 #pragma unroll
     for (int j = 0; j < FM; ++j) acc[i][j] = Sum<EPI>{};
 
+  __shared__ TileScales<EPI, BM, BN> scales;
+  Int8Fetched fetched{};
+  if constexpr (EPI == EPI_INT8)
+    if (!p.partial) fetched = fetch_scales<BM, BN>(p.scales, p.plain, m0, n0, threadIdx.x, 64 * NW * KS);
   if constexpr (FP4) lw.codes.template fetch<0>(kdim);
 #pragma unroll
   for (int s = 0; s < S - 1; ++s)
     if (s < KT) load(s);
+  if constexpr (EPI == EPI_INT8)
+    if (!p.partial) put_scales<BM, BN>(scales.t, fetched, p.plain.bias, threadIdx.x, 64 * NW * KS);
   for (int kt = 0; kt < KT; ++kt) {
     // stage kt has landed once only the later stages' loads (and the codes
     // fetched with and after it) are pending
@@ -176,7 +189,9 @@ __global__ __launch_bounds__(64 * WN * WM * KS) void dense_tile_kernel(DensePara
     }
     gated_epilogue<FM>(g, u, p.gated, mb, n0 + wn * 32, lane, region);
   } else if constexpr (EPI == EPI_INT8) {
-    int8_epilogue<FM>(acc, scales_of(p), plain_of(p, slice), mb, n0 + wn * 64, lane, region);
+    const Int8Tile<BM, BN>& t = scales.t;
+    int8_epilogue<FM>(acc, p.partial ? nullptr : t.x + wm * (FM * 16), t.w + wn * 64, t.bias + wn * 64,
+                      plain_of(p, slice), mb, n0 + wn * 64, lane, region);
   } else {
     plain_epilogue<FM>(acc, plain_of(p, slice), mb, n0 + wn * 64, lane, region);
   }
@@ -289,6 +304,10 @@ __global__ __launch_bounds__(512, 2) void dense_wide_kernel(DenseParams p) {
     ahead(lw1);
     if constexpr (WH == 3) ahead(lw2);
   }
+  __shared__ TileScales<EPI, 64 * XF, 128 * WH> scales;
+  Int8Fetched fetched{};
+  if constexpr (EPI == EPI_INT8)
+    if (!p.partial) fetched = fetch_scales<64 * XF, 128 * WH>(p.scales, p.plain, m0, n0, threadIdx.x, 512);
   load_w(Even{}, lw0, 0, 0);
   load_x(0);
   load_w(Even{}, lw1, 1, 0);
@@ -296,6 +315,8 @@ __global__ __launch_bounds__(512, 2) void dense_wide_kernel(DenseParams p) {
   load_w(Odd{}, lw0, 0, 1);
   load_x(1);
   if constexpr (WH == 3) load_w(Odd{}, lw1, 1, 1);
+  if constexpr (EPI == EPI_INT8)
+    if (!p.partial) put_scales<64 * XF, 128 * WH>(scales.t, fetched, p.plain.bias, threadIdx.x, 512);
   // W0 and X of step 0 have landed
   wait_vm<(WH == 3 ? 4 : 2) * LOADS_W + LOADS_X>();
   wait_lds();
@@ -375,7 +396,10 @@ __global__ __launch_bounds__(512, 2) void dense_wide_kernel(DenseParams p) {
         }
         gated_epilogue<XFT>(g, u, p.gated, mb, n0 + h * 64 + wn * 32, lane, region);
       } else if constexpr (EPI == EPI_INT8) {
-        int8_epilogue<XFT>(a, scales_of(p), plain_of(p, slice), mb, n0 + h * 128 + wn * 64, lane, region);
+        const Int8Tile<64 * XF, 128 * WH>& t = scales.t;
+        const int c = h * 128 + wn * 64;
+        int8_epilogue<XFT>(a, p.partial ? nullptr : t.x + q * XR + wm * (XFT * 16), t.w + c, t.bias + c,
+                           plain_of(p, slice), mb, n0 + c, lane, region);
       } else {
         plain_epilogue<XFT>(a, plain_of(p, slice), mb, n0 + h * 128 + wn * 64, lane, region);
       }
@@ -515,6 +539,19 @@ constexpr Config kConfigs[CFG_COUNT] = {
     {"tile_128x128_k2", 128, 128, 1, true, 0.45, 0.58, 0.58, 0.58, 4.0, 1.0},
     {"tile_128x64_k2", 128, 64, 1, true, 0.30, 0.34, 0.34, 0.34, 4.0, 1.0},
     {"tile_64x64_k2", 64, 64, 2, true, 0.23, 0.32, 0.42, 0.42, 3.0, 1.0}};
+// The same kernels on 8-bit integers (stages of 128 k), measured with 64, 256 and full
+// rounds of tiles at k = 4096 and 12288; the epilogue's share of `fixed` is larger, as
+// the tiles of a given k take half as many stages.
+constexpr Config kInt8Configs[CFG_COUNT] = {
+    {"wide_256x256", 256, 256, 1, false, 0.98, 1.50, 1.50, 1.50, 9.5, 1.0},
+    {"wide_256x192", 256, 192, 1, true, 0.82, 1.20, 1.20, 1.25, 8.5, 1.0},
+    {"wide_384x192", 384, 192, 1, true, 1.32, 1.90, 1.90, 1.90, 8.5, 1.0},
+    {"tile_128x128", 128, 128, 2, false, 0.68, 0.70, 1.30, 1.45, 6.0, 1.0},
+    {"tile_128x64", 128, 64, 2, false, 0.41, 0.43, 0.62, 0.70, 5.5, 1.0},
+    {"tile_64x64", 64, 64, 3, false, 0.31, 0.32, 0.62, 0.70, 4.5, 1.0},
+    {"tile_128x128_k2", 128, 128, 1, true, 0.52, 0.54, 0.54, 0.60, 7.0, 1.0},
+    {"tile_128x64_k2", 128, 64, 1, true, 0.33, 0.35, 0.35, 0.40, 5.5, 1.0},
+    {"tile_64x64_k2", 64, 64, 2, true, 0.35, 0.35, 0.40, 0.45, 3.5, 1.0}};
 struct Choice {
   int config, slices;
   int64_t k_per_split;
@@ -535,11 +572,11 @@ double model_us(const Config& g, uint32_t tiles, uint32_t stages, bool cols_w) {
 // n: columns of the output's tiles (2 f when gated).  lx, lw: the operands'
 // layouts.  can_slice: a plain output.  (On the way of every call: 32-bit
 // divisions, and no slices where the tiles alone make four rounds.)
-Choice choose(int64_t m, int64_t n, int64_t k, int lx, int lw, bool can_slice) {
+Choice choose(int64_t m, int64_t n, int64_t k, int lx, int lw, bool can_slice, const Config* configs = kConfigs) {
   const uint32_t stages = (uint32_t)((k + BK - 1) / BK);
   uint32_t tiles[CFG_COUNT];
   for (int c = 0; c < CFG_COUNT; ++c) {
-    const uint32_t bm = kConfigs[c].bm, bn = kConfigs[c].bn;
+    const uint32_t bm = configs[c].bm, bn = configs[c].bn;
     tiles[c] = (((uint32_t)m + bm - 1) / bm) * (((uint32_t)n + bn - 1) / bn);
   }
   Choice best{CFG_64, 1, k, 1e300};
@@ -551,7 +588,7 @@ Choice choose(int64_t m, int64_t n, int64_t k, int lx, int lw, bool can_slice) {
     const double join = s > 1 ? 3.0 + 8.0 * s * m * n / 6e6 : 0.0;
     if (join >= best.us) break;
     for (int c = 0; c < CFG_COUNT; ++c) {
-      const Config& g = kConfigs[c];
+      const Config& g = configs[c];
       if ((g.rows_x && lx != ROWS) || (s > 1 && tiles[c] * s > 1024)) continue;
       if (c >= CFG_128_K2 && per < 2) continue;  // nothing for the second group
       // with few stages the stores are most of the time, and only where a CU
@@ -602,7 +639,7 @@ hipError_t run_dense(DenseParams p, const Choice& c, void* workspace, hipStream_
 // The choice of each product, for its launch, its workspace and its name.
 Choice choose_gated(int64_t m, int64_t k, int64_t f) { return choose(m, 2 * f, k, ROWS, ROWS, false); }
 Choice choose_mxfp4(int64_t m, int64_t n, int64_t k) { return choose(m, n, k, ROWS, CODES, true); }
-Choice choose_int8(int64_t m, int64_t n, int64_t k) { return choose(m, n, k / 2, ROWS, ROWS, true); }
+Choice choose_int8(int64_t m, int64_t n, int64_t k) { return choose(m, n, k / 2, ROWS, ROWS, true, kInt8Configs); }
 Choice choose_dx(int64_t m, int64_t k, int64_t f2) { return choose(m, k, f2, ROWS, COLS, true); }
 Choice choose_dw(int64_t m, int64_t k, int64_t f2) { return choose(f2, k, m, COLS, COLS, false); }
 

@@ -543,34 +543,70 @@ __device__ __forceinline__ v4f bias4(const uint16_t* bias, int64_t n) {
   return v4f{bf16_to_f32(b.x & 0xFFFFu), bf16_to_f32(b.x >> 16), bf16_to_f32(b.y & 0xFFFFu), bf16_to_f32(b.y >> 16)};
 }
 
-// Columns col .. col + 63 of rows m0 .. from their exact sums.  Rows and columns
-// past the ends take the last one's scales and are not stored.
+// The scales and biases of a workgroup's BM rows and BN columns, in LDS.  They are
+// read at the start of its work (BM + BN is at most twice the threads, BN at most as many):
+// read in the epilogue they held every tile up by 5 us.
+template <int BM, int BN>
+struct Int8Tile {
+  float x[BM], w[BN], bias[BN];
+};
+struct Int8Fetched {
+  float v[2];
+  uint32_t bias;
+};
+// Rows m0 .. and columns n0 .. ; past the ends the last one's (not stored).
+template <int BM, int BN>
+__device__ __forceinline__ Int8Fetched fetch_scales(const Int8Scales& sc, const PlainOut& o, int64_t m0, int64_t n0,
+                                                    int tid, int threads) {
+  Int8Fetched f{};
+  if (o.bias && tid < BN) f.bias = o.bias[min(n0 + tid, o.n - 1)];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int at = tid + i * threads;
+    if (at < BM) f.v[i] = sc.x[min(m0 + at, o.m - 1)];
+    else if (at < BM + BN) f.v[i] = sc.w[min(n0 + at - BM, o.n - 1)];
+  }
+  return f;
+}
+template <int BM, int BN>
+__device__ __forceinline__ void put_scales(Int8Tile<BM, BN>& t, const Int8Fetched& f, bool biased, int tid,
+                                           int threads) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int at = tid + i * threads;
+    if (at < BM) t.x[at] = f.v[i];
+    else if (at < BM + BN) t.w[at - BM] = f.v[i];
+  }
+  if (tid < BN) t.bias[tid] = biased ? bf16_to_f32(f.bias) : -0.f;
+}
+
+// Columns col .. col + 63 of rows m0 .. from their exact sums; xs, ws, bias: in LDS,
+// of the first of these rows and columns (null for a slice's partial sums, which
+// are kept as integers).
 template <int FM>
-__device__ __forceinline__ void int8_epilogue(const v4i (&acc)[4][FM], const Int8Scales& sc, PlainOut o, int64_t m0,
-                                              int64_t col, int lane, uint8_t* region) {
+__device__ __forceinline__ void int8_epilogue(const v4i (&acc)[4][FM], const float* xs, const float* ws,
+                                              const float* bias, PlainOut o, int64_t m0, int64_t col, int lane,
+                                              uint8_t* region) {
   const int r16 = lane & 15, lg = lane >> 4;
   if (col >= o.n) return;
   v4f y[4][FM];
-  if (!sc.x) {  // a slice's partial sums, kept as integers
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+  for (int j = 0; j < 4; ++j) {
+    if (!xs) {
 #pragma unroll
       for (int fm = 0; fm < FM; ++fm) y[j][fm] = __builtin_bit_cast(v4f, acc[j][fm]);
-  } else {
-    float xs[FM];
-#pragma unroll
-    for (int fm = 0; fm < FM; ++fm) xs[fm] = sc.x[min(m0 + fm * 16 + r16, o.m - 1)];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t n = min(col + 16 * j + 4 * lg, o.n - 4);
-      const v4f ws = *reinterpret_cast<const v4f*>(sc.w + n), b = bias4(o.bias, n);
-#pragma unroll
-      for (int fm = 0; fm < FM; ++fm)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[j][fm][i] = int8_value(acc[j][fm][i], xs[fm], ws[i], b[i]);
+      continue;
     }
-    o.bias = nullptr;
+    const v4f w = *reinterpret_cast<const v4f*>(ws + 16 * j + 4 * lg);
+    const v4f b = *reinterpret_cast<const v4f*>(bias + 16 * j + 4 * lg);
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm) {
+      const float x = xs[fm * 16 + r16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[j][fm][i] = int8_value(acc[j][fm][i], x, w[i], b[i]);
+    }
   }
+  if (xs) o.bias = nullptr;
   plain_epilogue<FM>(y, o, m0, col, lane, region);
 }
 

@@ -255,12 +255,11 @@ constexpr Form kT1W4{"stream_4bit_t1w4", run_stream<true, false, 1, 16, 4, 2>};
 constexpr Form kT2W4{"stream_4bit_t2w4", run_stream<true, false, 2, 16, 4, 2>};
 constexpr Form kT2W3{"stream_4bit_t2w3", run_stream<true, false, 2, 16, 3, 2>};
 constexpr Form kT2W2{"stream_4bit_t2w2", run_stream<true, false, 2, 16, 2, 2>};
-constexpr Form kI8R2T1W8{"stream_int8_r2_t1w8", run_stream<false, false, 1, 2, 8, 2, false, true>};
-constexpr Form kI8R2T2W4{"stream_int8_r2_t2w4", run_stream<false, false, 2, 2, 4, 2, false, true>};
+constexpr Form kI8R2{"stream_int8_r2", run_stream<false, false, 1, 2, 8, 3, false, true>};
 constexpr Form kI8R8T1W8{"stream_int8_r8_t1w8", run_stream<false, false, 1, 8, 8, 2, false, true>};
-constexpr Form kI8R8T2W4{"stream_int8_r8_t2w4", run_stream<false, false, 2, 8, 4, 2, false, true>};
-constexpr Form kI8T1W8{"stream_int8_t1w8", run_stream<false, false, 1, 16, 8, 2, false, true>};
-constexpr Form kI8T2W4{"stream_int8_t2w4", run_stream<false, false, 2, 16, 4, 2, false, true>};
+constexpr Form kI8R8T2W3{"stream_int8_r8_t2w3", run_stream<false, false, 2, 8, 3, 2, false, true>};
+constexpr Form kI8T1W4{"stream_int8_t1w4", run_stream<false, false, 1, 16, 4, 2, false, true>};
+constexpr Form kI8T2W3{"stream_int8_t2w3", run_stream<false, false, 2, 16, 3, 2, false, true>};
 
 // The form of a call.
 //
@@ -284,10 +283,16 @@ constexpr Form kI8T2W4{"stream_int8_t2w4", run_stream<false, false, 2, 16, 4, 2,
 // 8.3, 6.3, 32 rows 15.0, 9.7;  n = 4096: 8 rows 4.0 against 4.9, 16 rows 4.7
 // against 5.7;  gated k = 4096, 16 rows: f = 4096 6.4 against 9.2, f = 8192 10.4, 10.0;
 // k = 704, f = 9248: 8.5, 5.4;  k = 4096, f = 4096, 64 rows: 19.4, 15.5.
+//
+// 8-bit integers, by the same rule, us: 16 rows, n = 4096, k = 14336: one tile and four
+// wavefronts 12.0, two tiles and three 12.8; n = 14336, k = 4096: 15.2, 13.0 (two and four
+// 16.7); 8 rows: one and eight 11.7, two and three 12.0; 15.6, 12.3.  Up to two rows one
+// tile and eight, three buffers: n = 4096, k = 28672 22.8 (two buffers 24.2), n = 14336
+// 72.7 (76.0).
 const Form& stream_form(const StreamArgs& a) {
   if (a.ws) {
     const bool few = a.rows / 16 * ((a.m + 15) / 16) <= 256;
-    return a.m <= 2 ? (few ? kI8R2T1W8 : kI8R2T2W4) : a.m <= 8 ? (few ? kI8R8T1W8 : kI8R8T2W4) : few ? kI8T1W8 : kI8T2W4;
+    return a.m <= 2 ? kI8R2 : a.m <= 8 ? (few ? kI8R8T1W8 : kI8R8T2W3) : few ? kI8T1W4 : kI8T2W3;
   }
   if (!a.w_scale) return a.m <= 2 ? kBf16R2 : a.m <= 8 ? kBf16R8 : a.m <= 16 ? kBf16R16 : kBf16Passes;
   const int64_t tiles = a.rows / 16 * ((a.m + 15) / 16);

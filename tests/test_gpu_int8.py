@@ -16,9 +16,10 @@ SHAPES = [(1, 16, 16), (1, 4096, 4096), (2, 48, 144), (3, 272, 400), (5, 16, 819
           (100, 5648, 2080), (128, 128, 128), (129, 272, 16), (200, 64, 32768), (257, 1552, 784), (300, 4096, 1024),
           (517, 784, 4112), (700, 3600, 272), (1025, 528, 3088), (2100, 4368, 528),
           # one for every other kernel, with and without slices of the sum
-          (1, 5648, 16), (3, 5648, 16), (17, 3600, 28672), (17, 4096, 14336), (17, 5648, 8192), (17, 28672, 2080),
+          (1, 16, 28672), (1, 5648, 28672), (1, 5648, 16), (3, 5648, 16), (5, 5648, 16), (17, 3600, 28672), (17, 4096, 14336), (17, 5648, 8192), (17, 28672, 2080),
           (65, 5648, 5648), (65, 5648, 28672), (129, 5648, 14336), (200, 14336, 16), (257, 14336, 16),
-          (769, 14336, 528), (1025, 14336, 528), (4097, 272, 28672), (4097, 528, 14336), (4097, 784, 272)]
+          (769, 14336, 528), (1025, 14336, 528), (4097, 272, 28672), (4097, 528, 14336), (4097, 784, 272),
+          (17, 28672, 8192), (65, 28672, 5648), (129, 2080, 28672), (129, 8192, 14336), (200, 5648, 28672)]
 
 
 @pytest.fixture(scope="module")
