@@ -623,7 +623,7 @@ const char* sfr_int8_kernel(int64_t m, int64_t n, int64_t k, int dynamic, int32_
 /*
  * ---------------------------------------------------------------------------
  * A mixture of gated feed-forward blocks ("experts") for a few tokens: the router,
- * and the whole layer in two launches.
+ * and the whole layer.
  * ---------------------------------------------------------------------------
  */
 #define SFR_MAX_EXPERTS 1024
@@ -661,7 +661,8 @@ sfr_status moe_route(const uint16_t* x, int64_t m, int64_t k, const uint16_t* w,
 typedef enum { SFR_EXPERT_BF16 = 0, SFR_EXPERT_INT8 = 1, SFR_EXPERT_MXFP4 = 2 } sfr_expert_t;
 
 /*
- * moe_layer -- the layer on the router's choice:
+ * moe_layer -- the layer on the router's choice, in two launches up to two tokens (up
+ * to eight with top <= 4), three for each further 64:
  *     h[t, s]  = act(x[t] Wg[e]^T) * (x[t] Wu[e]^T),  e = ids[t, s]
  *     out[t]   = sum_s weights[t, s] h[t, s] Wd[e]^T
  * Sums are binary32; h is rounded once to bf16, the type in which the second
@@ -669,8 +670,9 @@ typedef enum { SFR_EXPERT_BF16 = 0, SFR_EXPERT_INT8 = 1, SFR_EXPERT_MXFP4 = 2 } 
  * (padding, or experts held elsewhere: out is then this device's share); a token
  * without a choice gets zeros.  An expert named twice counts with the sum of its
  * weights.  A token's result depends on no other token's values, and infinities and
- * NaN in an expert reach only the tokens that chose it; the order of a token's
- * sums depends on which experts the call's tokens chose.  No atomics on results.
+ * NaN in an expert reach only the tokens that chose it.  The sums' order is fixed,
+ * no atomics: in the calls of three launches for a token by itself, in those of two by
+ * the experts that the call's tokens chose.
  *
  *   x [m, k], out [m, k]: bf16 bits.  ids [m, top] int32, weights [m, top] binary32.
  *   w_gate_up  [experts, 2 f, k]: every expert's gate rows, then its up rows.

@@ -1032,10 +1032,15 @@ def _expert_parts(t, name: str, device: int):
     return 0, a * b, c, t.data_ptr(), None
 
 
+@functools.lru_cache(maxsize=4096)
+def _moe_workspace_bytes(m: int, k: int, f: int, top: int) -> int:
+    return load().sfr_moe_workspace_bytes(m, k, f, top)
+
+
 def moe_layer(x: torch.Tensor, route: MoeRoute, w_gate_up, w_down, activation: str = "silu",
               out: Optional[torch.Tensor] = None, *, stream=None) -> torch.Tensor:
-    """The whole mixture of gated feed-forward blocks for a few tokens, in two
-    launches: out[t] = sum_s weights[t, s] * (act(x[t] @ Wg[e].T) * (x[t] @ Wu[e].T)) @ Wd[e].T,
+    """The whole mixture of gated feed-forward blocks for a few tokens:
+    out[t] = sum_s weights[t, s] * (act(x[t] @ Wg[e].T) * (x[t] @ Wu[e].T)) @ Wd[e].T,
     e = ids[t, s], for bf16 x [m, k].
 
     w_gate_up: bf16 [experts, 2 f, k], every expert's gate rows and then its up
@@ -1073,9 +1078,8 @@ def moe_layer(x: torch.Tensor, route: MoeRoute, w_gate_up, w_down, activation: s
     else:
         out = torch.empty_like(x)
     top = ids.shape[1]
-    lib = load()
-    nbytes = lib.sfr_moe_workspace_bytes(m, k, f, top)
-    work = x.new_empty((max(nbytes, 16),), dtype=torch.uint8)
-    _check(lib.moe_layer(px, m, k, ids.data_ptr(), weights.data_ptr(), top, experts, f, form, pg, pgs, pd, pds, act,
+    nbytes = _moe_workspace_bytes(m, k, f, top)
+    work = x.new_empty((nbytes // 2 + 8,))  # bf16
+    _check(load().moe_layer(px, m, k, ids.data_ptr(), weights.data_ptr(), top, experts, f, form, pg, pgs, pd, pds, act,
                          out.data_ptr(), work.data_ptr(), nbytes, _raw_stream(device)), "moe_layer")
     return out

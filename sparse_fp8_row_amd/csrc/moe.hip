@@ -1,7 +1,8 @@
 // A mixture of gated feed-forward blocks for a few tokens: the router, and the
 // layer
 //     out[t] = sum_s weights[t, s] (act(x[t] Wg[e]^T) * (x[t] Wu[e]^T)) Wd[e]^T,  e = ids[t, s]
-// in two launches.  Bound by reading the chosen experts' weights once.
+// in two launches for a few tokens and three for up to 64, the tokens of one pass.
+// Bound by reading the chosen experts' weights once.
 #include <type_traits>
 
 #include "sfr_dense.hpp"
@@ -236,21 +237,12 @@ __global__ __launch_bounds__(256) void route_select_kernel(RouteArgs a) {
 // ---------------------------------------------------------------------------
 // The layer
 //
-// Both kernels stream weight rows the way the few-row products do (stream.hip):
-// wavefronts take units of UK k in LDS buffers of their own, D - 1 units ahead,
-// 16 RT weight rows a workgroup, and add their sums in a fixed order at the end.
-//
-// Up: a workgroup owns RT / 2 pairs of gate and up row tiles of one expert, and
-//   runs them on that expert's tokens, R at a time, gathered by their rows of x.
-//   h = act(g) u goes to the workspace, rounded to bf16, at row (token, first
-//   slot of the expert).  A workgroup reads ids by itself: a bit per chosen
-//   expert in LDS, the blockIdx.y-th of which is its own.
-// Down: a workgroup owns 16 RT columns of out for all tokens and walks all chosen
-//   experts in ascending order; its wavefronts take even shares of their units.
-//   Tokens are the columns of the product, zeros where a token did not choose the
-//   expert; at the end of an expert a token's sums are added to its total with
-//   its weight, and only where it did choose it, so that an infinity in a weight
-//   stays with the tokens that met it.
+// Every workgroup reads ids by itself and finds its expert's tokens; a weight in
+// any of its forms is staged in LDS as it is stored and becomes bf16 operands there
+// (exactly: 8-bit integers and 4-bit floats with their scale are bf16 numbers;
+// the 8-bit form's row scales multiply the sums).  h = act(g) u is formed from
+// binary32 sums and rounded to bf16 in the workspace, at row (token, first slot of
+// the expert).
 // ---------------------------------------------------------------------------
 
 // What a workgroup knows of the tokens' choices, in two forms with the same calls.
@@ -259,19 +251,18 @@ __global__ __launch_bounds__(256) void route_select_kernel(RouteArgs a) {
 //   expert(i)      the i-th of them (uniform)
 //   slot(e)        in lane t: token t's first slot with expert e, or -1
 //   weight(e)      in lane t: the sum of its weights over its slots with e
-// Shared is the LDS that a form takes.
 
 // Up to 64 slots in all: a lane holds one (lane = t * top + s), and ballots do the
-// rest, without LDS or a barrier.  Experts in the order of their first slots.
+// rest, without LDS or a barrier (one token, 6 of 64 experts: 21.5 us a layer with the
+// form below, 19.9).  Experts in the order of their first slots.
 struct FewChoices {
-  struct Shared {};
   const MoeArgs& p;
   int id;
   float w;
   uint64_t firsts;  // slots that name an expert first
   int count;
   template <bool WEIGHTS>
-  __device__ __forceinline__ FewChoices(const MoeArgs& p_, Shared&, int lane, std::bool_constant<WEIGHTS>)
+  __device__ __forceinline__ FewChoices(const MoeArgs& p_, int lane, std::bool_constant<WEIGHTS>)
       : p(p_), id(-1), w(0.f), firsts(0) {
     if (lane < p.m * p.top) {
       const int v = p.ids[lane];
@@ -321,9 +312,7 @@ struct ManyChoices {
   uint32_t word;  // lane l < 32: bits of experts 32 l ..
   int upto;       // chosen experts up to this word's end
   int count;
-  template <bool WEIGHTS>
-  __device__ __forceinline__ ManyChoices(const MoeArgs& p_, Shared& c, int lane, std::bool_constant<WEIGHTS>)
-      : p(p_), ids(c.ids) {
+  __device__ __forceinline__ ManyChoices(const MoeArgs& p_, Shared& c, int lane) : p(p_), ids(c.ids) {
     static_assert(kMoeExperts <= 64 * 32, "a word per lane");
     for (int i = threadIdx.x; i < kMoeExperts / 32; i += blockDim.x) c.bits[i] = 0;
     __syncthreads();
@@ -478,7 +467,27 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t scale_rows(const void* s, int6
   return buf_rsrc(static_cast<const uint8_t*>(s) + (WF == EXPERT_FP4 ? row * (k / 32) : 0), kPastRange);
 }
 
-// LDS of the kernels whose wavefronts stream units by themselves.
+// ---------------------------------------------------------------------------
+// Few tokens: the weight rows are streamed the way the few-row products do
+// (stream.hip): wavefronts take units of UK k in LDS buffers of their own, D - 1
+// units ahead, 16 RT weight rows a workgroup, and add their sums in a fixed order
+// at the end.  The weight is loaded non-temporally, being read once.
+//
+// Up: a workgroup owns RT / 2 pairs of gate and up row tiles of one expert, and
+//   runs them on that expert's tokens (at most R), gathered by their rows of x.
+// Down: a workgroup owns 16 RT columns of out for all tokens and walks all chosen
+//   experts; its wavefronts take even shares of their units.  Tokens are the
+//   columns of the product, zeros where a token did not choose the expert; at the
+//   end of an expert a token's sums are added to its total with its weight, and
+//   only where it did choose it, so that an infinity in a weight stays with the
+//   tokens that met it.
+//
+// One token, 2 of 8 experts, k = 4096, f = 14336, bf16: up 72 us, down 37, 6.4 TB/s; 8-bit
+// 70 us together, 4-bit 43.  With little to read the two launches' latencies are
+// most of the time: 6 of 64, k = 2048, f = 1408, 8-bit 10.1 + 7.6 us for 52 MB.
+// ---------------------------------------------------------------------------
+
+// LDS of these kernels.
 template <int WF, int RT, int R, int NW, int D>
 struct Streamed : Unit<WF, RT, R, stream_k(WF)> {
   using U = Unit<WF, RT, R, stream_k(WF)>;
@@ -488,19 +497,18 @@ struct Streamed : Unit<WF, RT, R, stream_k(WF)> {
   static_assert((D - 1) * LOADS < 64, "wait counts");
 };
 
-template <class C, int WF, int RT, int R, int NW, int D, bool NT>
+template <int WF, int RT, int R, int NW, int D>
 __global__ __launch_bounds__(64 * NW) void moe_up_kernel(MoeArgs p) {
   using U = Unit<WF, RT, R, stream_k(WF)>;
   using L = Streamed<WF, RT, R, NW, D>;
   static_assert(RT % 2 == 0, "row tiles come in pairs");
   constexpr int RB = (R + 15) / 16;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-  __shared__ typename C::Shared shared;
   __shared__ int rows[kMoeTokens], pairs[kMoeTokens];  // the expert's tokens, and their rows of h
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, lg = lane >> 4;
 
-  const C chosen(p, shared, lane, std::false_type{});
+  const FewChoices chosen(p, lane, std::false_type{});
   if ((int)blockIdx.y >= chosen.count) return;
   const int e = chosen.expert(blockIdx.y), slot = chosen.slot(e, lane);
   const uint64_t takers = __ballot(slot >= 0);
@@ -526,93 +534,85 @@ __global__ __launch_bounds__(64 * NW) void moe_up_kernel(MoeArgs p) {
   const int units = (K + U::UK - 1) / U::UK;
   constexpr int XC = U::XROW / 16, XPL = 64 / XC;
 
-  for (int r0 = 0; r0 < count; r0 += R) {
-    const int mr = min(count - r0, R);
-    int xoff[U::XL];
+  int xoff[U::XL];
+#pragma unroll
+  for (int j = 0; j < U::XL; ++j) {
+    const int row = j * XPL + lane / XC;
+    xoff[j] = row < count ? rows[row] * (K * 2) + 16 * ((lane % XC) ^ (row & 7)) : kPastRange;
+  }
+  auto issue = [&](int at, int u) __attribute__((always_inline)) {
+    uint8_t* b = mine + at * L::BYTES;
+    const int left = K - u * U::UK;  // may be negative: every lane masked
+#pragma unroll
+    for (int t = 0; t < RT; ++t) issue_weight<WF, true, U>(rw[t], rs[t], b + t * U::TILE, u, left, K, lane);
 #pragma unroll
     for (int j = 0; j < U::XL; ++j) {
-      const int row = j * XPL + lane / XC;
-      xoff[j] = row < mr ? rows[r0 + row] * (K * 2) + 16 * ((lane % XC) ^ (row & 7)) : kPastRange;
+      const int c = (lane % XC) ^ ((j * XPL + lane / XC) & 7);
+      const bool in = c * 8 < left && xoff[j] != kPastRange;
+      buf_to_lds(rx, b + U::WBYTES + j * 1024, in ? xoff[j] + u * U::XROW : kPastRange);
     }
-    auto issue = [&](int at, int u) __attribute__((always_inline)) {
-      uint8_t* b = mine + at * L::BYTES;
-      const int left = K - u * U::UK;  // may be negative: every lane masked
+  };
+  v4f acc[RT][RB];
 #pragma unroll
-      for (int t = 0; t < RT; ++t) issue_weight<WF, NT, U>(rw[t], rs[t], b + t * U::TILE, u, left, K, lane);
+  for (int t = 0; t < RT; ++t)
 #pragma unroll
-      for (int j = 0; j < U::XL; ++j) {
-        const int c = (lane % XC) ^ ((j * XPL + lane / XC) & 7);
-        const bool in = c * 8 < left && xoff[j] != kPastRange;
-        buf_to_lds(rx, b + U::WBYTES + j * 1024, in ? xoff[j] + u * U::XROW : kPastRange);
-      }
-    };
-    v4f acc[RT][RB];
+    for (int b = 0; b < RB; ++b) acc[t][b] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
-#pragma unroll
-      for (int b = 0; b < RB; ++b) acc[t][b] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < D - 1; ++i) issue(i, wave + i * NW);
-    int at = 0;
-    for (int u = wave; u < units; u += NW) {
-      wait_lds();  // the buffer to be refilled has been read
-      issue(at == 0 ? D - 1 : at - 1, u + (D - 1) * NW);
-      wait_vm<(D - 1) * L::LOADS>();
-      asm volatile("" ::: "memory");
-      multiply_unit<WF, RT, RB, R, U>(acc, mine + at * L::BYTES, mine + at * L::BYTES + U::WBYTES, lane);
-      at = at == D - 1 ? 0 : at + 1;
-    }
-    wait_vm<0>();
-    wait_lds();
-    wg_barrier();  // no load in flight, no read pending: the buffers become the sums'
+  for (int i = 0; i < D - 1; ++i) issue(i, wave + i * NW);
+  int at = 0;
+  for (int u = wave; u < units; u += NW) {
+    wait_lds();  // the buffer to be refilled has been read
+    issue(at == 0 ? D - 1 : at - 1, u + (D - 1) * NW);
+    wait_vm<(D - 1) * L::LOADS>();
+    asm volatile("" ::: "memory");
+    multiply_unit<WF, RT, RB, R, U>(acc, mine + at * L::BYTES, mine + at * L::BYTES + U::WBYTES, lane);
+    at = at == D - 1 ? 0 : at + 1;
+  }
+  wait_vm<0>();
+  wait_lds();
+  wg_barrier();  // no load in flight, no read pending: the buffers become the sums'
 
-    float* const red = reinterpret_cast<float*>(smem);  // [NW][RT][R][16]
+  float* const red = reinterpret_cast<float*>(smem);  // [NW][RT][R][16]
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
+  for (int t = 0; t < RT; ++t)
 #pragma unroll
-      for (int b = 0; b < RB; ++b)
-        if (16 * b + r16 < mr)
-          *reinterpret_cast<v4f*>(red + ((wave * RT + t) * R + 16 * b + r16) * 16 + 4 * lg) = acc[t][b];
-    wait_lds();
-    wg_barrier();
-    constexpr int OT = RT / 2;
-    for (int i = threadIdx.x; i < OT * 16 * mr; i += 64 * NW) {
-      const int n = i % 16, t = i / 16 % OT, r = i / (16 * OT);
-      const int col = (tile0 + t) * 16 + n;
-      if (col >= p.f) continue;
-      float g = 0.f, u = 0.f;
+    for (int b = 0; b < RB; ++b)
+      if (16 * b + r16 < count)
+        *reinterpret_cast<v4f*>(red + ((wave * RT + t) * R + 16 * b + r16) * 16 + 4 * lg) = acc[t][b];
+  wait_lds();
+  wg_barrier();
+  constexpr int OT = RT / 2;
+  for (int i = threadIdx.x; i < OT * 16 * count; i += 64 * NW) {
+    const int n = i % 16, t = i / 16 % OT, r = i / (16 * OT);
+    const int col = (tile0 + t) * 16 + n;
+    if (col >= p.f) continue;
+    float g = 0.f, u = 0.f;
 #pragma unroll
-      for (int v = 0; v < NW; ++v) {
-        g += red[((v * RT + 2 * t) * R + r) * 16 + n];
-        u += red[((v * RT + 2 * t + 1) * R + r) * 16 + n];
-      }
-      if constexpr (WF == EXPERT_INT8) {
-        const float* s = static_cast<const float*>(p.s_gu) + (int64_t)e * 2 * p.f + col;
-        g *= s[0];
-        u *= s[p.f];
-      }
-      const float h = u * gate_value(p.act, g);
-      p.h[(int64_t)pairs[r0 + r] * p.f + col] = (uint16_t)pack_bf16x2(h, 0.f);
+    for (int v = 0; v < NW; ++v) {
+      g += red[((v * RT + 2 * t) * R + r) * 16 + n];
+      u += red[((v * RT + 2 * t + 1) * R + r) * 16 + n];
     }
-    if (r0 + R < count) {
-      wait_lds();
-      wg_barrier();  // the sums are read: the buffers are free again
+    if constexpr (WF == EXPERT_INT8) {
+      const float* s = static_cast<const float*>(p.s_gu) + (int64_t)e * 2 * p.f + col;
+      g *= s[0];
+      u *= s[p.f];
     }
+    const float h = u * gate_value(p.act, g);
+    p.h[(int64_t)pairs[r] * p.f + col] = (uint16_t)pack_bf16x2(h, 0.f);
   }
 }
 
-template <class C, int WF, int RT, int R, int NW, int D, bool NT>
+template <int WF, int RT, int R, int NW, int D>
 __global__ __launch_bounds__(64 * NW) void moe_down_kernel(MoeArgs p) {
   using U = Unit<WF, RT, R, stream_k(WF)>;
   using L = Streamed<WF, RT, R, NW, D>;
   constexpr int RB = (R + 15) / 16;
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
-  __shared__ typename C::Shared shared;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, lg = lane >> 4;
   const int F = p.f, tile0 = blockIdx.x * RT, tiles = p.k / 16;
 
-  const C chosen(p, shared, lane, std::true_type{});
+  const FewChoices chosen(p, lane, std::true_type{});
   const int each = (F + U::UK - 1) / U::UK, units = chosen.count * each;
   const int share = (units + NW - 1) / NW, first = min(wave * share, units), last = min(first + share, units);
 
@@ -654,7 +654,7 @@ __global__ __launch_bounds__(64 * NW) void moe_down_kernel(MoeArgs p) {
     }
     const int left = next < last ? F - unit_in * U::UK : 0;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) issue_weight<WF, NT, U>(rw[t], rs[t], b + t * U::TILE, unit_in, left, F, lane);
+    for (int t = 0; t < RT; ++t) issue_weight<WF, true, U>(rw[t], rs[t], b + t * U::TILE, unit_in, left, F, lane);
 #pragma unroll
     for (int j = 0; j < U::XL; ++j) {
       const int c = (lane % XC) ^ ((j * XPL + lane / XC) & 7);
@@ -753,7 +753,7 @@ struct TileShared {
   float weights[kMoeTokens];                // DOWN: over all the token's slots with the expert
 };
 
-template <int WF, bool DOWN, int RT, int NW, int UK, int POOL, int NB, bool NT>
+template <int WF, bool DOWN, int RT, int NW, int UK, int POOL, int NB>
 __device__ __forceinline__ void moe_tiles(const MoeArgs& p, const TileShared& sh, int e, int count, int g0, int g1,
                                           uint8_t* smem, int lane, int wave) {
   using U = Unit<WF, RT, 16 * NB, UK>;
@@ -798,7 +798,7 @@ __device__ __forceinline__ void moe_tiles(const MoeArgs& p, const TileShared& sh
     const int left = K - unit_in * U::UK;  // not positive past the last unit: every lane masked
 #pragma unroll
     for (int t = 0; t < RT; ++t)
-      issue_weight<WF, NT, U>(rw[t], rs[t], b + wave * U::WBYTES + t * U::TILE, unit_in, left, K, lane);
+      issue_weight<WF, false, U>(rw[t], rs[t], b + wave * U::WBYTES + t * U::TILE, unit_in, left, K, lane);
 #pragma unroll
     for (int j = 0; j < XL; ++j) {
       const int row = (wave * XL + j) * XPL + lane / XC, c = (lane % XC) ^ (row & 7);
@@ -860,13 +860,13 @@ __device__ __forceinline__ void moe_tiles(const MoeArgs& p, const TileShared& sh
   wait_vm<0>();  // the loads past the last unit (zeros) end before the LDS is used for anything else
 }
 
-template <int WF, bool DOWN, int RT, int NW, int UK, int POOL, bool NT>
+template <int WF, bool DOWN, int RT, int NW, int UK, int POOL>
 __global__ __launch_bounds__(64 * NW) void moe_tile_kernel(MoeArgs p) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
   __shared__ ManyChoices::Shared shared;
   __shared__ TileShared sh;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const ManyChoices chosen(p, shared, lane, std::bool_constant<DOWN>{});
+  const ManyChoices chosen(p, shared, lane);
   constexpr int cover = NW * (DOWN ? RT : RT / 2) * 16;
   const int groups = ((DOWN ? p.k : p.f) + cover - 1) / cover, tasks = chosen.count * groups;
   const int share = (tasks + gridDim.x - 1) / gridDim.x, last = min((int)(blockIdx.x + 1) * share, tasks);
@@ -887,25 +887,25 @@ __global__ __launch_bounds__(64 * NW) void moe_tile_kernel(MoeArgs p) {
     }
     __syncthreads();
     const int count = __popcll(takers);
-    if (count <= 16) moe_tiles<WF, DOWN, RT, NW, UK, POOL, 1, NT>(p, sh, e, count, g0, g1, smem, lane, wave);
-    else if (count <= 32) moe_tiles<WF, DOWN, RT, NW, UK, POOL, 2, NT>(p, sh, e, count, g0, g1, smem, lane, wave);
-    else if (count <= 48) moe_tiles<WF, DOWN, RT, NW, UK, POOL, 3, NT>(p, sh, e, count, g0, g1, smem, lane, wave);
-    else moe_tiles<WF, DOWN, RT, NW, UK, POOL, 4, NT>(p, sh, e, count, g0, g1, smem, lane, wave);
+    if (count <= 16) moe_tiles<WF, DOWN, RT, NW, UK, POOL, 1>(p, sh, e, count, g0, g1, smem, lane, wave);
+    else if (count <= 32) moe_tiles<WF, DOWN, RT, NW, UK, POOL, 2>(p, sh, e, count, g0, g1, smem, lane, wave);
+    else if (count <= 48) moe_tiles<WF, DOWN, RT, NW, UK, POOL, 3>(p, sh, e, count, g0, g1, smem, lane, wave);
+    else moe_tiles<WF, DOWN, RT, NW, UK, POOL, 4>(p, sh, e, count, g0, g1, smem, lane, wave);
   }
 }
 
 // out[t] = the sum of its experts' parts in the order of the slots, rounded once.
 __global__ __launch_bounds__(256) void moe_combine_kernel(MoeArgs p) {
-  const int t = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x;
-  if (c >= p.k / 4) return;
-  const int32_t* const ids = p.ids + t * p.top;
+  const int t = blockIdx.y, c = blockIdx.x * 256 + threadIdx.x, lane = threadIdx.x & 63;
+  int id = lane < p.top ? p.ids[t * p.top + lane] : -1;
+  if (id >= p.experts) id = -1;
   uint32_t firsts = 0;  // slots that name an expert first
-  for (int i = 0; i < p.top; ++i) {
-    const int e = ids[i];
-    bool first = e >= 0 && e < p.experts;
-    for (int j = 0; j < i; ++j) first = first && ids[j] != e;
-    firsts |= (uint32_t)first << i;
+  for (uint64_t rest = __ballot(id >= 0); rest != 0;) {
+    const int first = __builtin_ctzll(rest);
+    firsts |= 1u << first;
+    rest &= ~__ballot(id == __builtin_amdgcn_readlane(id, first));
   }
+  if (c >= p.k / 4) return;
   const v4f* const y = reinterpret_cast<const v4f*>(p.y + (int64_t)t * p.top * p.k) + c;
   v4f s = v4f{0.f, 0.f, 0.f, 0.f};
   for (int i = 0; i < p.top; i += 4) {  // four loads in flight
@@ -929,14 +929,19 @@ hipError_t allow_lds(K* kernel, int bytes) {
 int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
 
 constexpr int kLdsLeft = 160 * 1024 - (int)sizeof(ManyChoices::Shared) - (int)sizeof(TileShared);
-// Whether the layer is two launches of the streaming kernels, or three of the tiled ones.
+// Whether the layer is two launches of the streaming kernels, or three of the tiled
+// ones.  Every workgroup that streams loads all tokens' activation for 16 or 32
+// weight rows, where the tiled ones share it, so it is for few tokens on few
+// experts (us, streamed against tiled: 8 tokens E8 8-bit 181, 191, bf16 308, 357; 4 tokens
+// E64 8-bit 57.4, 48.5, 4-bit 41.1, 37.6; 6 tokens E64 bf16 97.2, 99.6; 2 tokens on 2 of 16
+// experts of 1024 x 512 15.4, 19.3).
 bool streamed(int64_t m, int top) { return m <= 2 || (m <= 8 && top <= 4); }
 
-template <class C, int WF, int RT, int R, int NW, int D, bool NT>
-hipError_t run_up_with(const MoeArgs& p, hipStream_t stream) {
+template <int WF, int RT, int R, int NW, int D>
+hipError_t run_up(const MoeArgs& p, hipStream_t stream) {
   constexpr int bytes = Streamed<WF, RT, R, NW, D>::LDS, cover = RT / 2 * 16;
   static_assert(bytes <= kLdsLeft, "LDS of a CU");
-  auto* kernel = moe_up_kernel<C, WF, RT, R, NW, D, NT>;
+  auto* kernel = moe_up_kernel<WF, RT, R, NW, D>;
   const hipError_t e = allow_lds(kernel, bytes);
   if (e != hipSuccess) return e;
   const dim3 grid((unsigned)((p.f + cover - 1) / cover), (unsigned)min(p.experts, p.m * p.top));
@@ -944,33 +949,22 @@ hipError_t run_up_with(const MoeArgs& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <class C, int WF, int RT, int R, int NW, int D, bool NT>
-hipError_t run_down_with(const MoeArgs& p, hipStream_t stream) {
+template <int WF, int RT, int R, int NW, int D>
+hipError_t run_down(const MoeArgs& p, hipStream_t stream) {
   constexpr int bytes = Streamed<WF, RT, R, NW, D>::LDS, cover = RT * 16;
   static_assert(bytes <= kLdsLeft, "LDS of a CU");
-  auto* kernel = moe_down_kernel<C, WF, RT, R, NW, D, NT>;
+  auto* kernel = moe_down_kernel<WF, RT, R, NW, D>;
   const hipError_t e = allow_lds(kernel, bytes);
   if (e != hipSuccess) return e;
   kernel<<<dim3((unsigned)((p.k + cover - 1) / cover)), dim3(64 * NW), bytes, stream>>>(p);
   return hipGetLastError();
 }
 
-template <int WF, int RT, int R, int NW, int D, bool NT>
-hipError_t run_up(const MoeArgs& p, hipStream_t stream) {
-  return p.m * p.top <= 64 ? run_up_with<FewChoices, WF, RT, R, NW, D, NT>(p, stream)
-                           : run_up_with<ManyChoices, WF, RT, R, NW, D, NT>(p, stream);
-}
-template <int WF, int RT, int R, int NW, int D, bool NT>
-hipError_t run_down(const MoeArgs& p, hipStream_t stream) {
-  return p.m * p.top <= 64 ? run_down_with<FewChoices, WF, RT, R, NW, D, NT>(p, stream)
-                           : run_down_with<ManyChoices, WF, RT, R, NW, D, NT>(p, stream);
-}
-
-template <int WF, bool DOWN, int RT, int NW, int UK, int POOL, bool NT>
+template <int WF, bool DOWN, int RT, int NW, int UK, int POOL>
 hipError_t run_tile(const MoeArgs& p, hipStream_t stream) {
   constexpr int cover = NW * (DOWN ? RT : RT / 2) * 16;
   static_assert(POOL <= kLdsLeft, "LDS of a CU");
-  auto* kernel = moe_tile_kernel<WF, DOWN, RT, NW, UK, POOL, NT>;
+  auto* kernel = moe_tile_kernel<WF, DOWN, RT, NW, UK, POOL>;
   const hipError_t e = allow_lds(kernel, POOL);
   if (e != hipSuccess) return e;
   // as many workgroups as the CUs hold, fewer where there are not so many groups of tiles
@@ -980,30 +974,43 @@ hipError_t run_tile(const MoeArgs& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// The forms, each by what it measured of those that fit LDS (us a layer in a graph;
+// E8: 2 of 8 experts, k = 4096, f = 14336, E64: 8 of 64, k = 2048, f = 1408):
+//   tiled, by tiles, wavefronts and k of a unit (one workgroup a CU; two with half the
+//     LDS are within 5%, as is a group of tiles a workgroup instead of even shares):
+//     up   bf16 2, 4, 128;  8-bit 4, 4, 128 (64 tokens E8 290, with 2, 8, 128 301, 2, 4, 256
+//          308);  4-bit 2, 8, 256 (225, with 2, 4, 128 238)
+//     down bf16 2, 4, 128;  8-bit 1, 8, 128 (285, with 2, 4, 128 287);  4-bit 1, 8, 256 (216,
+//          2, 4, 128 222)
+//   streamed up, by wavefronts: up to two tokens four, where each has four units of k or
+//     more, else two (E8 4-bit 42.4, two 46.7; E64 8-bit, 6 of 64, 20.9, two 20.1); up to eight
+//     three, and two for 4-bit (8 tokens E8 bf16 314, two 320; 4-bit 133, two 126)
+//   streamed down: twelve wavefronts up to two tokens (E64 19.9, four 20.5), eight up to
+//     eight (8 tokens E8 4-bit 124.7, four 130.6).
 template <int WF>
 hipError_t run_layer(const MoeArgs& p, hipStream_t stream) {
   if (!streamed(p.m, p.top)) {
     constexpr int pool = 148 * 1024;
     hipError_t e;
     if constexpr (WF == EXPERT_BF16) {
-      e = run_tile<WF, false, 2, 4, 128, pool, false>(p, stream);
-      if (e == hipSuccess) e = run_tile<WF, true, 2, 4, 128, pool, false>(p, stream);
+      e = run_tile<WF, false, 2, 4, 128, pool>(p, stream);
+      if (e == hipSuccess) e = run_tile<WF, true, 2, 4, 128, pool>(p, stream);
     } else if constexpr (WF == EXPERT_INT8) {
-      e = run_tile<WF, false, 4, 4, 128, pool, false>(p, stream);
-      if (e == hipSuccess) e = run_tile<WF, true, 1, 8, 128, pool, false>(p, stream);
+      e = run_tile<WF, false, 4, 4, 128, pool>(p, stream);
+      if (e == hipSuccess) e = run_tile<WF, true, 1, 8, 128, pool>(p, stream);
     } else {
-      e = run_tile<WF, false, 2, 8, 256, pool, false>(p, stream);
-      if (e == hipSuccess) e = run_tile<WF, true, 1, 8, 256, pool, false>(p, stream);
+      e = run_tile<WF, false, 2, 8, 256, pool>(p, stream);
+      if (e == hipSuccess) e = run_tile<WF, true, 1, 8, 256, pool>(p, stream);
     }
     if (e != hipSuccess) return e;
     moe_combine_kernel<<<dim3((unsigned)((p.k / 4 + 255) / 256), (unsigned)p.m), dim3(256), 0, stream>>>(p);
     return hipGetLastError();
   }
-  const hipError_t e = p.m > 2 ? run_up<WF, 2, 8, WF == EXPERT_FP4 ? 2 : 3, 2, true>(p, stream)
-                       : p.k >= 16 * stream_k(WF) ? run_up<WF, 2, 2, 4, 2, true>(p, stream)
-                                                  : run_up<WF, 2, 2, 2, 2, true>(p, stream);
+  const hipError_t e = p.m > 2 ? run_up<WF, 2, 8, WF == EXPERT_FP4 ? 2 : 3, 2>(p, stream)
+                       : p.k >= 16 * stream_k(WF) ? run_up<WF, 2, 2, 4, 2>(p, stream)
+                                                  : run_up<WF, 2, 2, 2, 2>(p, stream);
   if (e != hipSuccess) return e;
-  return p.m <= 2 ? run_down<WF, 1, 2, 12, 2, true>(p, stream) : run_down<WF, 1, 8, 8, 2, true>(p, stream);
+  return p.m <= 2 ? run_down<WF, 1, 2, 12, 2>(p, stream) : run_down<WF, 1, 8, 8, 2>(p, stream);
 }
 
 template <int TB, int EB>

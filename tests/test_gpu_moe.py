@@ -16,7 +16,9 @@ FORMS = ["bf16", "int8", "fp4"]
 LAYERS = [(1, 32, 32, 1, 1), (1, 4096, 64, 4, 2), (1, 96, 1408, 8, 8), (2, 288, 160, 5, 3), (3, 64, 4128, 3, 2),
           (5, 544, 96, 33, 6), (8, 160, 288, 64, 8), (9, 256, 416, 4, 2), (15, 32, 96, 130, 16), (16, 320, 224, 16, 4),
           (17, 96, 352, 8, 2), (31, 416, 160, 3, 1), (32, 128, 128, 12, 4), (33, 224, 64, 6, 3), (47, 64, 544, 64, 8),
-          (64, 352, 288, 8, 2), (65, 128, 96, 9, 2), (130, 96, 160, 1000, 5), (200, 64, 32, 2, 2)]
+          (64, 352, 288, 8, 2), (65, 128, 96, 9, 2), (130, 96, 160, 1000, 5), (200, 64, 32, 2, 2),
+          # more groups of tiles than workgroups, of one expert and of several
+          (20, 64, 16416, 5, 2), (20, 8224, 64, 5, 2), (12, 2080, 1056, 40, 3), (2, 64, 8224, 16, 16), (8, 8224, 96, 6, 4)]
 
 
 @pytest.fixture(scope="module")
@@ -67,7 +69,7 @@ def test_root_mean_square(sfr, m, k, f, experts, top, form):
 
 
 @pytest.mark.parametrize("form", FORMS)
-@pytest.mark.parametrize("m", [1, 2, 7, 16, 20, 32, 64, 70])
+@pytest.mark.parametrize("m", [1, 2, 7, 16, 20, 32, 33, 48, 49, 64, 70])
 def test_every_token_to_one_expert(sfr, m, form):
     """The longest list an expert can have, in the last place."""
     x, ids, weights, gu, down = stacked(m, m, 160, 96, 6, 2, form, sfr)
@@ -260,6 +262,21 @@ def test_streams_graphs_and_threads(sfr):
     assert not bad
 
 
+@pytest.mark.parametrize("form", FORMS)
+def test_tokens_do_not_depend_on_the_batch(sfr, form):
+    """From nine tokens on a token's bits are its own, whoever else is in the pass."""
+    x, ids, weights, gu, down = stacked(9, 64, 288, 416, 6, 2, form, sfr)
+    ids[::2, 0] = 5  # 32 tokens and more to one expert
+    whole = sfr.moe_layer(x, sfr.MoeRoute(ids, weights), gu, down)
+    for rows in (slice(0, 9), slice(3, 20), slice(20, 57), slice(0, 64, 2), slice(0, 64, 5)):
+        part = [t[rows].contiguous() for t in (x, ids, weights)]
+        assert torch.equal(sfr.moe_layer(part[0], sfr.MoeRoute(*part[1:]), gu, down), whole[rows]), rows
+    # one more than a pass: the last token in a pass of its own
+    twice = [torch.cat((t, t[:1])) for t in (x, ids, weights)]
+    again = sfr.moe_layer(twice[0], sfr.MoeRoute(*twice[1:]), gu, down)
+    assert torch.equal(again[:64], whole)
+
+
 def test_layer_refusals(sfr):
     x, ids, weights, gu, down = stacked(1, 4, 64, 96, 5, 2, "bf16", sfr)
     r = sfr.MoeRoute(ids, weights)
@@ -322,7 +339,8 @@ def check_route(r, logits64, top, score, renormalize):
 @pytest.mark.parametrize("score,renormalize", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
 @pytest.mark.parametrize("m,k,experts,top", [(1, 32, 1, 1), (1, 2048, 64, 8), (2, 96, 5, 5), (3, 4096, 130, 6),
                                              (5, 7200, 256, 16), (16, 160, 63, 4), (17, 544, 65, 2), (33, 1056, 129, 8),
-                                             (64, 256, 1024, 16), (300, 416, 257, 7), (1000, 4096, 161, 6)])
+                                             (64, 256, 1024, 16), (300, 416, 257, 7), (1000, 4096, 161, 6), (1100, 96, 250, 3), (70000, 32, 3, 2),
+                                             (6000, 32, 2, 1)])
 def test_route(sfr, m, k, experts, top, score, renormalize):
     g = torch.Generator("cuda").manual_seed(m + k)
     x = torch.randn(m, k, generator=g, device="cuda").bfloat16()
@@ -379,16 +397,17 @@ def test_route_masked_and_far(sfr, score, renormalize):
         check_route(sfr.moe_route(x, w, 5, bias, score, renormalize), ref + shift, 5, score, renormalize)
 
 
+@pytest.mark.parametrize("m,experts", [(4, 20), (200, 100), (1100, 300)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
-def test_route_not_finite(sfr, score):
-    x = torch.randn(4, 64, device="cuda").bfloat16()
+def test_route_not_finite(sfr, score, m, experts):
+    x = torch.randn(m, 64, device="cuda").bfloat16()
     x[1, 5] = math.nan
-    w = torch.randn(20, 64, device="cuda").bfloat16()
-    bias = torch.zeros(20, device="cuda")
+    w = torch.randn(experts, 64, device="cuda").bfloat16()
+    bias = torch.zeros(experts, device="cuda")
     bias[7] = math.nan
     r = sfr.moe_route(x, w, 3, None, score)
     assert torch.equal(r.ids[1].cpu(), torch.arange(3, dtype=torch.int32)) and bool(torch.isnan(r.weights[1]).all())
-    keep = torch.tensor([0, 2, 3], device="cuda")
+    keep = torch.arange(m, device="cuda") != 1
     assert bool(torch.isfinite(r.weights[keep]).all())
     r = sfr.moe_route(x[keep], w, 3, bias, score)
     assert bool((r.ids[:, 0] == 7).all()) and bool(torch.isnan(r.weights[:, 0]).all())
