@@ -521,6 +521,7 @@ enum {
   CFG_128_K2,
   CFG_128x64_K2,
   CFG_64_K2,
+  CFG_64_K2_DEEP,  // four stages instead of two; 8-bit integers only
   CFG_COUNT
 };
 struct Config {
@@ -538,10 +539,14 @@ constexpr Config kConfigs[CFG_COUNT] = {
     {"tile_64x64", 64, 64, 3, false, 0.36, 0.40, 0.59, 0.59, 3.0, 1.0},
     {"tile_128x128_k2", 128, 128, 1, true, 0.45, 0.58, 0.58, 0.58, 4.0, 1.0},
     {"tile_128x64_k2", 128, 64, 1, true, 0.30, 0.34, 0.34, 0.34, 4.0, 1.0},
-    {"tile_64x64_k2", 64, 64, 2, true, 0.23, 0.32, 0.42, 0.42, 3.0, 1.0}};
+    {"tile_64x64_k2", 64, 64, 2, true, 0.23, 0.32, 0.42, 0.42, 3.0, 1.0},
+    {}};
 // The same kernels on 8-bit integers (stages of 128 k), measured with 64, 256 and full
 // rounds of tiles at k = 4096 and 12288; the epilogue's share of `fixed` is larger, as
-// the tiles of a given k take half as many stages.
+// the tiles of a given k take half as many stages.  With half the stages a tile waits
+// out more of its latencies, so the 64 x 64 tiles with two groups of wavefronts have a
+// form of four stages (m = 128, n = k = 4096 15.2 -> 11.6 us in a graph, 100 x 5648 x 2080 10.9
+// -> 10.0, 60 x 14336 x 4096 14.9 -> 13.4).
 constexpr Config kInt8Configs[CFG_COUNT] = {
     {"wide_256x256", 256, 256, 1, false, 0.98, 1.50, 1.50, 1.50, 9.5, 1.0},
     {"wide_256x192", 256, 192, 1, true, 0.82, 1.20, 1.20, 1.25, 8.5, 1.0},
@@ -551,7 +556,8 @@ constexpr Config kInt8Configs[CFG_COUNT] = {
     {"tile_64x64", 64, 64, 3, false, 0.31, 0.32, 0.62, 0.70, 4.5, 1.0},
     {"tile_128x128_k2", 128, 128, 1, true, 0.52, 0.54, 0.54, 0.60, 7.0, 1.0},
     {"tile_128x64_k2", 128, 64, 1, true, 0.33, 0.35, 0.35, 0.40, 5.5, 1.0},
-    {"tile_64x64_k2", 64, 64, 2, true, 0.35, 0.35, 0.40, 0.45, 3.5, 1.0}};
+    {"tile_64x64_k2", 64, 64, 2, true, 0.35, 0.35, 0.40, 0.45, 3.5, 1.0},
+    {"tile_64x64_k2_deep", 64, 64, 1, true, 0.17, 0.23, 0.23, 0.26, 3.6, 1.0}};
 struct Choice {
   int config, slices;
   int64_t k_per_split;
@@ -575,7 +581,8 @@ double model_us(const Config& g, uint32_t tiles, uint32_t stages, bool cols_w) {
 Choice choose(int64_t m, int64_t n, int64_t k, int lx, int lw, bool can_slice, const Config* configs = kConfigs) {
   const uint32_t stages = (uint32_t)((k + BK - 1) / BK);
   uint32_t tiles[CFG_COUNT];
-  for (int c = 0; c < CFG_COUNT; ++c) {
+  const int count = configs == kInt8Configs ? CFG_COUNT : CFG_64_K2_DEEP;
+  for (int c = 0; c < count; ++c) {
     const uint32_t bm = configs[c].bm, bn = configs[c].bn;
     tiles[c] = (((uint32_t)m + bm - 1) / bm) * (((uint32_t)n + bn - 1) / bn);
   }
@@ -587,7 +594,7 @@ Choice choose(int64_t m, int64_t n, int64_t k, int lx, int lw, bool can_slice, c
     if (s > 1 && (stages + per - 1) / per != s) continue;
     const double join = s > 1 ? 3.0 + 8.0 * s * m * n / 6e6 : 0.0;
     if (join >= best.us) break;
-    for (int c = 0; c < CFG_COUNT; ++c) {
+    for (int c = 0; c < count; ++c) {
       const Config& g = configs[c];
       if ((g.rows_x && lx != ROWS) || (s > 1 && tiles[c] * s > 1024)) continue;
       if (c >= CFG_128_K2 && per < 2) continue;  // nothing for the second group
@@ -625,6 +632,9 @@ hipError_t run_dense(DenseParams p, const Choice& c, void* workspace, hipStream_
     case CFG_64_K2:
       if constexpr (LX == ROWS) e = run_tile<LX, LW, EPI, 64, 64, 1, 4, 2, 2>(p, c.slices, stream);
       break;
+    case CFG_64_K2_DEEP:
+      if constexpr (EPI == EPI_INT8) e = run_tile<LX, LW, EPI, 64, 64, 1, 4, 4, 2>(p, c.slices, stream);
+      break;
     case CFG_128: e = run_tile<LX, LW, EPI, 128, 128, 2, 2, 2>(p, c.slices, stream); break;
     case CFG_128x64: e = run_tile<LX, LW, EPI, 128, 64, 2, 2, 3>(p, c.slices, stream); break;
     default: e = run_tile<LX, LW, EPI, 64, 64, 1, 4, 3>(p, c.slices, stream);
@@ -645,7 +655,7 @@ Choice choose_dw(int64_t m, int64_t k, int64_t f2) { return choose(f2, k, m, COL
 
 int64_t slice_bytes(const Choice& c, int64_t m, int64_t n) { return c.slices > 1 ? c.slices * m * n * 4 : 0; }
 
-DenseKernel named(const Choice& c) { return {kConfigs[c.config].name, c.slices}; }
+DenseKernel named(const Choice& c, const Config* configs = kConfigs) { return {configs[c.config].name, c.slices}; }
 
 }  // namespace
 
@@ -654,7 +664,7 @@ DenseKernel dense_mxfp4_kernel(int64_t m, int64_t n, int64_t k) { return named(c
 DenseKernel dense_dx_kernel(int64_t m, int64_t k, int64_t f2) { return named(choose_dx(m, k, f2)); }
 DenseKernel dense_dw_kernel(int64_t m, int64_t k, int64_t f2) { return named(choose_dw(m, k, f2)); }
 
-DenseKernel dense_int8_kernel(int64_t m, int64_t n, int64_t k) { return named(choose_int8(m, n, k)); }
+DenseKernel dense_int8_kernel(int64_t m, int64_t n, int64_t k) { return named(choose_int8(m, n, k), kInt8Configs); }
 
 double dense_us(int64_t m, int64_t n, int64_t k, bool fp4, bool gated) {
   return choose(m, n, k, ROWS, fp4 ? CODES : ROWS, !gated).us;

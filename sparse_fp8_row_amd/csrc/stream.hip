@@ -219,13 +219,15 @@ bool stream_rows(int64_t m, int64_t n, int64_t k, bool fp4, bool gated) {
   return 3 + passes * pass <= (tiles > read ? tiles : read);
 }
 
-// The same for 8-bit integers, first taken as the bf16 product of half the k.
+// The same for 8-bit integers (streamed, less 2.5 us of a graph's launch: 12 rows, n = k
+// = 4096 3.9 us; 24, 8192 x 4096 11.5; 40, 14336 x 2080 19.4; 100, 1040 x 8192 11.5; 128, 4096 x
+// 4096 16.6).  Stream against tiles, us: 20 rows, 4096 x 4096 6.8, 9.7; 40, 2080 x 2080 5.6, 7.3;
+// 100, 1040 x 8192 14.0, 10.7; 128, 4096 x 4096 19.1, 11.5.
 bool stream_rows_int8(int64_t m, int64_t n, int64_t k) {
   const int64_t passes = (m + 15) / 16;
   if (m <= 8) return true;
   if (passes > 8) return false;
-  const double bytes = (double)n * k, pass = bytes / 9e6, tiles = dense_int8_us(m, n, k), read = bytes / 4.8e6 + 3;
-  return 3 + passes * pass <= (tiles > read ? tiles : read);
+  return 1.5 + passes * ((double)n * k / 6.2e6) <= dense_int8_us(m, n, k);
 }
 
 namespace {
