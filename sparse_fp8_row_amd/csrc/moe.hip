@@ -736,7 +736,9 @@ __global__ __launch_bounds__(64 * NW) void moe_down_kernel(MoeArgs p) {
 // More tokens: a workgroup owns NW wavefronts' weight tiles of one expert and all
 // of k, and its wavefronts share the expert's activation rows, gathered: each
 // puts its own weight tiles and a share of the activation in flight, D - 1 units
-// ahead, and one barrier a unit publishes them.  The number of 16-row blocks of
+// ahead, and one barrier a unit publishes them.  The weight, read once, is loaded
+// non-temporally (a layer for 64 tokens, 2 of 8 experts, k = 4096, f = 14336, 8-bit 297 -> 256
+// us, bf16 501 -> 458; 16 tokens, 8 of 64, k = 2048, f = 1408, bf16 139 -> 127).  The number of 16-row blocks of
 // the expert's tokens picks the loop (NB), and with it how many units fit LDS.
 // The groups of NW wavefronts' tiles of all chosen experts are split evenly, in
 // order, over as many workgroups as the CUs hold, which keep units in flight
@@ -798,7 +800,7 @@ __device__ __forceinline__ void moe_tiles(const MoeArgs& p, const TileShared& sh
     const int left = K - unit_in * U::UK;  // not positive past the last unit: every lane masked
 #pragma unroll
     for (int t = 0; t < RT; ++t)
-      issue_weight<WF, false, U>(rw[t], rs[t], b + wave * U::WBYTES + t * U::TILE, unit_in, left, K, lane);
+      issue_weight<WF, true, U>(rw[t], rs[t], b + wave * U::WBYTES + t * U::TILE, unit_in, left, K, lane);
 #pragma unroll
     for (int j = 0; j < XL; ++j) {
       const int row = (wave * XL + j) * XPL + lane / XC, c = (lane % XC) ^ (row & 7);
@@ -932,9 +934,9 @@ constexpr int kLdsLeft = 160 * 1024 - (int)sizeof(ManyChoices::Shared) - (int)si
 // Whether the layer is two launches of the streaming kernels, or three of the tiled
 // ones.  Every workgroup that streams loads all tokens' activation for 16 or 32
 // weight rows, where the tiled ones share it, so it is for few tokens on few
-// experts (us, streamed against tiled: 8 tokens E8 8-bit 181, 191, bf16 308, 357; 4 tokens
-// E64 8-bit 57.4, 48.5, 4-bit 41.1, 37.6; 6 tokens E64 bf16 97.2, 99.6; 2 tokens on 2 of 16
-// experts of 1024 x 512 15.4, 19.3).
+// experts (us, streamed against tiled: 8 tokens E8 8-bit 180, 180, bf16 309, 325; 5 tokens
+// E8 4-bit 103, 112; 4 tokens on 4 of 16 experts of 1024 x 512 15.4, 19.3; but 4 tokens E64
+// bf16 82, 71; 8 tokens E64 8-bit 78, 57).
 bool streamed(int64_t m, int top) { return m <= 2 || (m <= 8 && top <= 4); }
 
 template <int WF, int RT, int R, int NW, int D>
@@ -976,12 +978,11 @@ hipError_t run_tile(const MoeArgs& p, hipStream_t stream) {
 
 // The forms, each by what it measured of those that fit LDS (us a layer in a graph;
 // E8: 2 of 8 experts, k = 4096, f = 14336, E64: 8 of 64, k = 2048, f = 1408):
-//   tiled, by tiles, wavefronts and k of a unit (one workgroup a CU; two with half the
-//     LDS are within 5%, as is a group of tiles a workgroup instead of even shares):
-//     up   bf16 2, 4, 128;  8-bit 4, 4, 128 (64 tokens E8 290, with 2, 8, 128 301, 2, 4, 256
-//          308);  4-bit 2, 8, 256 (225, with 2, 4, 128 238)
-//     down bf16 2, 4, 128;  8-bit 1, 8, 128 (285, with 2, 4, 128 287);  4-bit 1, 8, 256 (216,
-//          2, 4, 128 222)
+//   tiled, by tiles, wavefronts and k of a unit, one workgroup a CU:
+//     up   bf16 2, 4, 128 (64 tokens E8 510; 2, 2, 128 in half of LDS 518);  8-bit 4, 4, 128
+//          (264; 2, 8, 128 281; 2, 4, 256 287);  4-bit 2, 8, 256 (232; 2, 4, 256 246)
+//     down bf16 2, 4, 128 (445; 1, 8, 128 446);  8-bit 1, 8, 128 (258; 2, 4, 128 260; 1, 4, 128
+//          in half of LDS 264);  4-bit 1, 8, 256 (212; 2, 4, 256 217; 1, 8, 128 228)
 //   streamed up, by wavefronts: up to two tokens four, where each has four units of k or
 //     more, else two (E8 4-bit 42.4, two 46.7; E64 8-bit, 6 of 64, 20.9, two 20.1); up to eight
 //     three, and two for 4-bit (8 tokens E8 bf16 314, two 320; 4-bit 133, two 126)
