@@ -422,31 +422,39 @@ __device__ __forceinline__ void multiply_unit(v4f (&acc)[RT][RB], const uint8_t*
         x[rb][j] = *reinterpret_cast<const v8bf*>(xb + row * U::XROW + 16 * (c ^ (row & 7)));
       }
     }
+    // two weight tiles at a time: a product's wait for its sum is the other's turn
+    constexpr int P = RT % 2 == 0 ? 2 : 1;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      const uint8_t* wb = b + t * U::TILE + r16 * U::WROW;
-      v8bf w[4];
-      if constexpr (WF == EXPERT_BF16) {
+    for (int t0 = 0; t0 < RT; t0 += P) {
+      v8bf w[P][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const v8bf*>(wb + 16 * ((4 * j + lg) ^ sw));
-      } else if constexpr (WF == EXPERT_INT8) {
+      for (int i = 0; i < P; ++i) {
+        const uint8_t* const tile = b + (t0 + i) * U::TILE;
+        const uint8_t* const wb = tile + r16 * U::WROW;
+        if constexpr (WF == EXPERT_BF16) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const v4i q = *reinterpret_cast<const v4i*>(wb + 16 * ((8 * s + 2 * lg + h) ^ sw));
-          w[2 * h] = widen8_int8((uint32_t)q[0], (uint32_t)q[1]);
-          w[2 * h + 1] = widen8_int8((uint32_t)q[2], (uint32_t)q[3]);
+          for (int j = 0; j < 4; ++j) w[i][j] = *reinterpret_cast<const v8bf*>(wb + 16 * ((4 * j + lg) ^ sw));
+        } else if constexpr (WF == EXPERT_INT8) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const v4i q = *reinterpret_cast<const v4i*>(wb + 16 * ((8 * s + 2 * lg + h) ^ sw));
+            w[i][2 * h] = widen8_int8((uint32_t)q[0], (uint32_t)q[1]);
+            w[i][2 * h + 1] = widen8_int8((uint32_t)q[2], (uint32_t)q[3]);
+          }
+        } else {
+          const v4i q = *reinterpret_cast<const v4i*>(wb + 16 * ((4 * s + lg) ^ sw));
+          const float f = mx_scale_value(
+              *reinterpret_cast<const uint32_t*>(tile + U::WL * 1024 + 4 * (r16 * (U::UK / 32) + 4 * s + lg)));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[i][j] = __builtin_bit_cast(v8bf, mx_widen8_e2m1((uint32_t)q[j], f));
         }
-      } else {
-        const v4i q = *reinterpret_cast<const v4i*>(wb + 16 * ((4 * s + lg) ^ sw));
-        const float f = mx_scale_value(
-            *reinterpret_cast<const uint32_t*>(b + t * U::TILE + U::WL * 1024 + 4 * (r16 * (U::UK / 32) + 4 * s + lg)));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = __builtin_bit_cast(v8bf, mx_widen8_e2m1((uint32_t)q[j], f));
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) acc[t][rb] = mfma16(w[j], x[rb][j], acc[t][rb]);
+        for (int i = 0; i < P; ++i)
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb) acc[t0 + i][rb] = mfma16(w[i][j], x[rb][j], acc[t0 + i][rb]);
     }
   }
 }
