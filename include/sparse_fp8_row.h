@@ -662,7 +662,7 @@ typedef enum { SFR_EXPERT_BF16 = 0, SFR_EXPERT_INT8 = 1, SFR_EXPERT_MXFP4 = 2 } 
 
 /*
  * moe_layer -- the layer on the router's choice, in two launches up to two tokens (up
- * to eight with top <= 4), three for each further 64:
+ * to eight with top <= 4), else in three for every 64:
  *     h[t, s]  = act(x[t] Wg[e]^T) * (x[t] Wu[e]^T),  e = ids[t, s]
  *     out[t]   = sum_s weights[t, s] h[t, s] Wd[e]^T
  * Sums are binary32; h is rounded once to bf16, the type in which the second

@@ -997,8 +997,8 @@ hipError_t run_tile(const MoeArgs& p, hipStream_t stream) {
 //   streamed down: twelve wavefronts up to two tokens (E64 19.9, four 20.5), eight up to
 //     eight (8 tokens E8 4-bit 124.7, four 130.6).
 template <int WF>
-hipError_t run_layer(const MoeArgs& p, hipStream_t stream) {
-  if (!streamed(p.m, p.top)) {
+hipError_t run_layer(const MoeArgs& p, bool few, hipStream_t stream) {
+  if (!few) {
     constexpr int pool = 148 * 1024;
     hipError_t e;
     if constexpr (WF == EXPERT_BF16) {
@@ -1058,9 +1058,12 @@ int64_t moe_workspace_bytes(int64_t m, int64_t k, int64_t f, int top) {
   return align256(pairs * f * 2) + (streamed(m, top) ? 0 : pairs * k * 4);
 }
 
-// kMoeTokens tokens at a time (a lane of a wavefront each).
+// kMoeTokens tokens at a time (a lane of a wavefront each).  The last of several
+// passes takes the tiled kernels too, however short: a token's result is the same
+// wherever in the call it stands.
 hipError_t launch_moe_layer(const MoeArgs& args, int64_t m, hipStream_t stream) {
   MoeArgs p = args;
+  const bool few = streamed(m, p.top);
   p.y = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(p.h) +
                                  align256((m < kMoeTokens ? m : kMoeTokens) * p.top * p.f * 2));
   for (int64_t t = 0; t < m; t += kMoeTokens) {
@@ -1069,9 +1072,9 @@ hipError_t launch_moe_layer(const MoeArgs& args, int64_t m, hipStream_t stream) 
     p.ids = args.ids + t * p.top;
     p.weights = args.weights + t * p.top;
     p.out = args.out + t * p.k;
-    const hipError_t e = p.form == EXPERT_BF16   ? run_layer<EXPERT_BF16>(p, stream)
-                         : p.form == EXPERT_INT8 ? run_layer<EXPERT_INT8>(p, stream)
-                                                 : run_layer<EXPERT_FP4>(p, stream);
+    const hipError_t e = p.form == EXPERT_BF16   ? run_layer<EXPERT_BF16>(p, few, stream)
+                         : p.form == EXPERT_INT8 ? run_layer<EXPERT_INT8>(p, few, stream)
+                                                 : run_layer<EXPERT_FP4>(p, few, stream);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;

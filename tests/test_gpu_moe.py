@@ -274,7 +274,7 @@ def test_tokens_do_not_depend_on_the_batch(sfr, form):
     # one more than a pass: the last token in a pass of its own
     twice = [torch.cat((t, t[:1])) for t in (x, ids, weights)]
     again = sfr.moe_layer(twice[0], sfr.MoeRoute(*twice[1:]), gu, down)
-    assert torch.equal(again[:64], whole)
+    assert torch.equal(again[:64], whole) and torch.equal(again[64:], whole[:1])
 
 
 def test_layer_refusals(sfr):
