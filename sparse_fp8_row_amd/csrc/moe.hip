@@ -418,7 +418,7 @@ __device__ __forceinline__ void multiply_unit(v4f (&acc)[RT][RB], const uint8_t*
       const int row = min(16 * rb + r16, R - 1);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int c = WF == EXPERT_BF16 ? 4 * j + lg : 16 * s + 4 * lg + j;
+        const int c = 16 * s + (WF == EXPERT_BF16 ? 4 * j + lg : 4 * lg + j);
         x[rb][j] = *reinterpret_cast<const v8bf*>(xb + row * U::XROW + 16 * (c ^ (row & 7)));
       }
     }
@@ -433,7 +433,7 @@ __device__ __forceinline__ void multiply_unit(v4f (&acc)[RT][RB], const uint8_t*
         const uint8_t* const wb = tile + r16 * U::WROW;
         if constexpr (WF == EXPERT_BF16) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) w[i][j] = *reinterpret_cast<const v8bf*>(wb + 16 * ((4 * j + lg) ^ sw));
+          for (int j = 0; j < 4; ++j) w[i][j] = *reinterpret_cast<const v8bf*>(wb + 16 * ((16 * s + 4 * j + lg) ^ sw));
         } else if constexpr (WF == EXPERT_INT8) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -938,6 +938,7 @@ hipError_t allow_lds(K* kernel, int bytes) {
 
 int64_t align256(int64_t b) { return (b + 255) / 256 * 256; }
 
+constexpr int kWhole = 148 * 1024, kHalf = 74 * 1024, kLess = 50 * 1024, kThird = 48 * 1024;
 constexpr int kLdsLeft = 160 * 1024 - (int)sizeof(ManyChoices::Shared) - (int)sizeof(TileShared);
 // Whether the layer is two launches of the streaming kernels, or three of the tiled
 // ones.  Every workgroup that streams loads all tokens' activation for 16 or 32
@@ -984,33 +985,69 @@ hipError_t run_tile(const MoeArgs& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// The forms, each by what it measured of those that fit LDS (us a layer in a graph;
-// E8: 2 of 8 experts, k = 4096, f = 14336, E64: 8 of 64, k = 2048, f = 1408):
-//   tiled, by tiles, wavefronts and k of a unit, one workgroup a CU:
-//     up   bf16 2, 4, 128 (64 tokens E8 510; 2, 2, 128 in half of LDS 518);  8-bit 4, 4, 128
-//          (264; 2, 8, 128 281; 2, 4, 256 287);  4-bit 2, 8, 256 (232; 2, 4, 256 246)
-//     down bf16 2, 4, 128 (445; 1, 8, 128 446);  8-bit 1, 8, 128 (258; 2, 4, 128 260; 1, 4, 128
-//          in half of LDS 264);  4-bit 1, 8, 256 (212; 2, 4, 256 217; 1, 8, 128 228)
-//   streamed up, by wavefronts: up to two tokens four, where each has four units of k or
-//     more, else two (E8 4-bit 42.4, two 46.7; E64 8-bit, 6 of 64, 20.9, two 20.1); up to eight
-//     three, and two for 4-bit (8 tokens E8 bf16 314, two 320; 4-bit 133, two 126)
-//   streamed down: twelve wavefronts up to two tokens (E64 19.9, four 20.5), eight up to
-//     eight (8 tokens E8 4-bit 124.7, four 130.6).
+// The tiled forms, by tiles, wavefronts and k of a unit; LDS for one workgroup of a CU
+// (kWhole), two (kHalf, kLess: fewer units ahead) or three (kThird).  Where there are
+// few tiles, small workgroups: more of them, and the last round of groups wastes less;
+// where there are many, large ones, which read the tokens' rows from LDS and memory less
+// often.  `most` bounds the tiles of 16 result columns over the experts that can be
+// chosen.  Measured on 300 layers of 4 to 128 experts, k and f from 256 to 4096 and 14336, 3
+// to 64 tokens (lengths over the best of ten forms, in the mean), and on 24 large ones:
+//   up   bf16  2, 2, 256 kWhole by itself 2.8%, 2, 2, 128 kHalf 2.0%, parted at k = 1536 0.5%
+//        8-bit 2, 4, 128 kHalf 2.6%, 2, 2, 128 kLess 2.9%, parted at 640 tiles 2.1%; before,
+//              4, 4, 128 kWhole, 16% (equal for 64 tokens, 2 of 8 experts, k = 4096, f = 14336)
+//        4-bit 2, 8, 256 kWhole 7.3%, 2, 2, 128 kLess 4.0%, parted at 1700 tiles 1.0%; of 64
+//              tokens, 2 of 8 experts 220 us and 289
+//   down bf16  1, 4, 256 kWhole 2.8%, 1, 2, 128 kHalf 3.5%, parted at 700 tiles 1.6%; with many
+//              tokens 1, 8, 128 kWhole (64 tokens, 2 of 8 experts 468 us, 1, 4, 256 494; 32 401, 406)
+//        8-bit 1, 4, 128 kThird 1.9%, 1, 8, 128 kHalf 8.7%, parted at 2048 tiles 1.5%; with many
+//              tokens 1, 8, 128 kWhole (64 tokens, 2 of 8 experts 277 us, kHalf 295; 32 234, 232)
+//        4-bit 1, 4, 128 kThird 2.4%, 1, 8, 256 kWhole 8.8%, parted at 2048 tiles 2.1%; of 64
+//              tokens, 2 of 8 experts 208 us, 1, 4, 128 kHalf 228
+// All of them add a sum's terms in the same order, so the choice, which depends on the
+// number of tokens, leaves a token's bits as they are.
+template <int WF>
+hipError_t run_tiled_up(const MoeArgs& p, hipStream_t stream) {
+  const int most = min(p.experts, p.m * p.top) * (p.f / 16);
+  if constexpr (WF == EXPERT_BF16)
+    return p.k < 1536 ? run_tile<WF, false, 2, 2, 128, kHalf>(p, stream)
+                      : run_tile<WF, false, 2, 2, 256, kWhole>(p, stream);
+  else if constexpr (WF == EXPERT_INT8)
+    return most <= 640 ? run_tile<WF, false, 2, 2, 128, kLess>(p, stream)
+                       : run_tile<WF, false, 2, 4, 128, kHalf>(p, stream);
+  else
+    return most <= 1700 ? run_tile<WF, false, 2, 2, 128, kLess>(p, stream)
+                        : run_tile<WF, false, 2, 8, 256, kWhole>(p, stream);
+}
+
+template <int WF>
+hipError_t run_tiled_down(const MoeArgs& p, hipStream_t stream) {
+  const int most = min(p.experts, p.m * p.top) * (p.k / 16);
+  if constexpr (WF == EXPERT_BF16)
+    return most <= 700 ? run_tile<WF, true, 1, 2, 128, kHalf>(p, stream)
+           : p.m > 32  ? run_tile<WF, true, 1, 8, 128, kWhole>(p, stream)
+                       : run_tile<WF, true, 1, 4, 256, kWhole>(p, stream);
+  else if constexpr (WF == EXPERT_INT8)
+    return most < 2048 ? run_tile<WF, true, 1, 4, 128, kThird>(p, stream)
+           : p.m > 32  ? run_tile<WF, true, 1, 8, 128, kWhole>(p, stream)
+                       : run_tile<WF, true, 1, 8, 128, kHalf>(p, stream);
+  else
+    return most < 2048 ? run_tile<WF, true, 1, 4, 128, kThird>(p, stream)
+                       : run_tile<WF, true, 1, 8, 256, kWhole>(p, stream);
+}
+
+// The streamed forms, by wavefronts, each with what it measured (us a layer in a graph;
+// E8: 2 of 8 experts, k = 4096, f = 14336, E64: 8 of 64, k = 2048, f = 1408); three and four
+// units in LDS are slower than two (one token, E64 8-bit 19.8, 21.8, 22.2):
+//   up: up to two tokens four, where each has four units of k or more, else two (E8
+//     4-bit 42.7, two 45.6; E64 8-bit, 6 of 64, 20.6, two 20.3); up to eight three, and two for
+//     4-bit (8 tokens E8 bf16 326, two 331; 4-bit 131, two 125)
+//   down: twelve up to two tokens (E64 19.9, four 20.7), eight up to eight (8 tokens E8
+//     4-bit 125, four 130).
 template <int WF>
 hipError_t run_layer(const MoeArgs& p, bool few, hipStream_t stream) {
   if (!few) {
-    constexpr int pool = 148 * 1024;
-    hipError_t e;
-    if constexpr (WF == EXPERT_BF16) {
-      e = run_tile<WF, false, 2, 4, 128, pool>(p, stream);
-      if (e == hipSuccess) e = run_tile<WF, true, 2, 4, 128, pool>(p, stream);
-    } else if constexpr (WF == EXPERT_INT8) {
-      e = run_tile<WF, false, 4, 4, 128, pool>(p, stream);
-      if (e == hipSuccess) e = run_tile<WF, true, 1, 8, 128, pool>(p, stream);
-    } else {
-      e = run_tile<WF, false, 2, 8, 256, pool>(p, stream);
-      if (e == hipSuccess) e = run_tile<WF, true, 1, 8, 256, pool>(p, stream);
-    }
+    hipError_t e = run_tiled_up<WF>(p, stream);
+    if (e == hipSuccess) e = run_tiled_down<WF>(p, stream);
     if (e != hipSuccess) return e;
     moe_combine_kernel<<<dim3((unsigned)((p.k / 4 + 255) / 256), (unsigned)p.m), dim3(256), 0, stream>>>(p);
     return hipGetLastError();

@@ -17,6 +17,8 @@ LAYERS = [(1, 32, 32, 1, 1), (1, 4096, 64, 4, 2), (1, 96, 1408, 8, 8), (2, 288, 
           (5, 544, 96, 33, 6), (8, 160, 288, 64, 8), (9, 256, 416, 4, 2), (15, 32, 96, 130, 16), (16, 320, 224, 16, 4),
           (17, 96, 352, 8, 2), (31, 416, 160, 3, 1), (32, 128, 128, 12, 4), (33, 224, 64, 6, 3), (47, 64, 544, 64, 8),
           (64, 352, 288, 8, 2), (65, 128, 96, 9, 2), (130, 96, 160, 1000, 5), (200, 64, 32, 2, 2),
+          # the tiles of many and of large experts
+          (10, 1536, 512, 48, 4), (40, 2048, 768, 36, 3), (9, 2112, 1440, 40, 2), (33, 1024, 2080, 32, 2),
           # more groups of tiles than workgroups, of one expert and of several
           (20, 64, 16416, 5, 2), (20, 8224, 64, 5, 2), (12, 2080, 1056, 40, 3), (2, 64, 8224, 16, 16), (8, 8224, 96, 6, 4)]
 
@@ -275,6 +277,18 @@ def test_tokens_do_not_depend_on_the_batch(sfr, form):
     twice = [torch.cat((t, t[:1])) for t in (x, ids, weights)]
     again = sfr.moe_layer(twice[0], sfr.MoeRoute(*twice[1:]), gu, down)
     assert torch.equal(again[:64], whole) and torch.equal(again[64:], whole[:1])
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("k,f", [(1024, 1024), (2080, 544), (288, 4128)])
+def test_tokens_do_not_depend_on_the_kernels(sfr, form, k, f):
+    """Nine tokens on few experts and 64 on many take tiles of different sizes."""
+    x, ids, weights, gu, down = stacked(k, 64, k, f, 64, 1, form, sfr, 0.05)
+    ids[:9] = 7
+    whole = compare(sfr, x, ids, weights, gu, down)
+    for rows in (slice(0, 9), slice(5, 16), slice(10, 35), slice(0, 64, 3)):
+        part = [t[rows].contiguous() for t in (x, ids, weights)]
+        assert torch.equal(sfr.moe_layer(part[0], sfr.MoeRoute(*part[1:]), gu, down), whole[rows]), rows
 
 
 def test_layer_refusals(sfr):
