@@ -992,13 +992,15 @@ hipError_t run_tile(const MoeArgs& p, hipStream_t stream) {
 // often.  `most` bounds the tiles of 16 result columns over the experts that can be
 // chosen.  Measured on 300 layers of 4 to 128 experts, k and f from 256 to 4096 and 14336, 3
 // to 64 tokens (lengths over the best of ten forms, in the mean), and on 24 large ones:
-//   up   bf16  2, 2, 256 kWhole by itself 2.8%, 2, 2, 128 kHalf 2.0%, parted at k = 1536 0.5%
+//   up   bf16  2, 2, 128 kHalf 0.9%, 2, 4, 128 kWhole 4.8%, parted at 45 tokens 0.7%; of 64
+//              tokens, 8 of 32 experts, k = 7168, f = 2048 505 us and 465, of 24 403 and 465
 //        8-bit 2, 4, 128 kHalf 2.6%, 2, 2, 128 kLess 2.9%, parted at 640 tiles 2.1%; before,
 //              4, 4, 128 kWhole, 16% (equal for 64 tokens, 2 of 8 experts, k = 4096, f = 14336)
 //        4-bit 2, 8, 256 kWhole 7.3%, 2, 2, 128 kLess 4.0%, parted at 1700 tiles 1.0%; of 64
 //              tokens, 2 of 8 experts 220 us and 289
-//   down bf16  1, 4, 256 kWhole 2.8%, 1, 2, 128 kHalf 3.5%, parted at 700 tiles 1.6%; with many
-//              tokens 1, 8, 128 kWhole (64 tokens, 2 of 8 experts 468 us, 1, 4, 256 494; 32 401, 406)
+//   down bf16  1, 2, 128 kHalf 3.2%, 1, 4, 256 kWhole 5.1%, 2, 4, 128 kWhole 12%, parted as
+//              below 2.0%; of the large layers with up to 16 tokens 1, 4, 256 is the faster one
+//              (16 of 4096 x 4096, 16 tokens 149 us, 2, 4, 128 166), with 64 2, 4, 128 (531, 562)
 //        8-bit 1, 4, 128 kThird 1.9%, 1, 8, 128 kHalf 8.7%, parted at 2048 tiles 1.5%; with many
 //              tokens 1, 8, 128 kWhole (64 tokens, 2 of 8 experts 277 us, kHalf 295; 32 234, 232)
 //        4-bit 1, 4, 128 kThird 2.4%, 1, 8, 256 kWhole 8.8%, parted at 2048 tiles 2.1%; of 64
@@ -1009,8 +1011,8 @@ template <int WF>
 hipError_t run_tiled_up(const MoeArgs& p, hipStream_t stream) {
   const int most = min(p.experts, p.m * p.top) * (p.f / 16);
   if constexpr (WF == EXPERT_BF16)
-    return p.k < 1536 ? run_tile<WF, false, 2, 2, 128, kHalf>(p, stream)
-                      : run_tile<WF, false, 2, 2, 256, kWhole>(p, stream);
+    return p.m > 44 && most >= 500 ? run_tile<WF, false, 2, 4, 128, kWhole>(p, stream)
+                                   : run_tile<WF, false, 2, 2, 128, kHalf>(p, stream);
   else if constexpr (WF == EXPERT_INT8)
     return most <= 640 ? run_tile<WF, false, 2, 2, 128, kLess>(p, stream)
                        : run_tile<WF, false, 2, 4, 128, kHalf>(p, stream);
@@ -1023,9 +1025,10 @@ template <int WF>
 hipError_t run_tiled_down(const MoeArgs& p, hipStream_t stream) {
   const int most = min(p.experts, p.m * p.top) * (p.k / 16);
   if constexpr (WF == EXPERT_BF16)
-    return most <= 700 ? run_tile<WF, true, 1, 2, 128, kHalf>(p, stream)
-           : p.m > 32  ? run_tile<WF, true, 1, 8, 128, kWhole>(p, stream)
-                       : run_tile<WF, true, 1, 4, 256, kWhole>(p, stream);
+    return most <= 1000   ? run_tile<WF, true, 1, 2, 128, kHalf>(p, stream)
+           : most <= 2000 ? run_tile<WF, true, 1, 4, 128, kHalf>(p, stream)
+           : p.m <= 16    ? run_tile<WF, true, 1, 4, 256, kWhole>(p, stream)
+                          : run_tile<WF, true, 2, 4, 128, kWhole>(p, stream);
   else if constexpr (WF == EXPERT_INT8)
     return most < 2048 ? run_tile<WF, true, 1, 4, 128, kThird>(p, stream)
            : p.m > 32  ? run_tile<WF, true, 1, 8, 128, kWhole>(p, stream)

@@ -18,7 +18,7 @@ LAYERS = [(1, 32, 32, 1, 1), (1, 4096, 64, 4, 2), (1, 96, 1408, 8, 8), (2, 288, 
           (17, 96, 352, 8, 2), (31, 416, 160, 3, 1), (32, 128, 128, 12, 4), (33, 224, 64, 6, 3), (47, 64, 544, 64, 8),
           (64, 352, 288, 8, 2), (65, 128, 96, 9, 2), (130, 96, 160, 1000, 5), (200, 64, 32, 2, 2),
           # the tiles of many and of large experts
-          (10, 1536, 512, 48, 4), (40, 2048, 768, 36, 3), (9, 2112, 1440, 40, 2), (33, 1024, 2080, 32, 2),
+          (10, 1536, 512, 48, 4), (40, 2048, 768, 36, 3), (9, 2112, 1440, 40, 2), (33, 1024, 2080, 32, 2), (46, 544, 768, 64, 3), (16, 1056, 288, 60, 3),
           # more groups of tiles than workgroups, of one expert and of several
           (20, 64, 16416, 5, 2), (20, 8224, 64, 5, 2), (12, 2080, 1056, 40, 3), (2, 64, 8224, 16, 16), (8, 8224, 96, 6, 4)]
 
