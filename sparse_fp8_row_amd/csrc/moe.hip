@@ -748,9 +748,13 @@ __global__ __launch_bounds__(64 * NW) void moe_down_kernel(MoeArgs p) {
 // non-temporally (a layer for 64 tokens, 2 of 8 experts, k = 4096, f = 14336, 8-bit 297 -> 256
 // us, bf16 501 -> 458; 16 tokens, 8 of 64, k = 2048, f = 1408, bf16 139 -> 127).  The number of 16-row blocks of
 // the expert's tokens picks the loop (NB), and with it how many units fit LDS.
-// The groups of NW wavefronts' tiles of all chosen experts are split evenly, in
-// order, over as many workgroups as the CUs hold, which keep units in flight
-// from one group to the next.
+// The groups of NW wavefronts' tiles of all chosen experts are split evenly over as
+// many workgroups as the CUs hold.  A group of an expert with many tokens takes longer
+// where the weight has to be converted, so 8- and 4-bit groups are dealt out one by one
+// when an expert can have more than 16 tokens; else in runs, whose units stay in flight
+// from one group to the next (us, dealt against runs: 64 tokens, 2 of 8 experts, k = 4096,
+// f = 14336, 8-bit 251, 298; 8 of 64, k = 2048, f = 1408, 8-bit 102, 123, 4-bit 88, 103, bf16 179,
+// 166; 16 tokens, bf16 128, 118, 4-bit 65, 61).
 //
 // Up: RT / 2 pairs of gate and up tiles a wavefront; h as above.
 // Down: RT tiles of 16 columns; weight times the sums go to the workspace in
@@ -879,10 +883,12 @@ __global__ __launch_bounds__(64 * NW) void moe_tile_kernel(MoeArgs p) {
   const ManyChoices chosen(p, shared, lane);
   constexpr int cover = NW * (DOWN ? RT : RT / 2) * 16;
   const int groups = ((DOWN ? p.k : p.f) + cover - 1) / cover, tasks = chosen.count * groups;
-  const int share = (tasks + gridDim.x - 1) / gridDim.x, last = min((int)(blockIdx.x + 1) * share, tasks);
-  for (int task = blockIdx.x * share; task < last;) {
-    const int i = task / groups, g0 = task - i * groups, g1 = min(groups, g0 + last - task);
-    task += g1 - g0;
+  const int blocks = gridDim.x, share = (tasks + blocks - 1) / blocks;
+  const bool deal = WF != EXPERT_BF16 && p.m > 16;
+  const int last = deal ? tasks : min((int)(blockIdx.x + 1) * share, tasks);
+  for (int task = deal ? blockIdx.x : blockIdx.x * share; task < last;) {
+    const int i = task / groups, g0 = task - i * groups, g1 = deal ? g0 + 1 : min(groups, g0 + last - task);
+    task += deal ? blocks : g1 - g0;
     const int e = chosen.expert(i), slot = chosen.slot(e, lane);
     const uint64_t takers = __ballot(slot >= 0);
     __syncthreads();  // the expert before is done with its lists and the stages
