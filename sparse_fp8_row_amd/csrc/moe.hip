@@ -1007,10 +1007,12 @@ hipError_t run_tile(const MoeArgs& p, hipStream_t stream) {
 //   down bf16  1, 2, 128 kHalf 3.2%, 1, 4, 256 kWhole 5.1%, 2, 4, 128 kWhole 12%, parted as
 //              below 2.0%; of the large layers with up to 16 tokens 1, 4, 256 is the faster one
 //              (16 of 4096 x 4096, 16 tokens 149 us, 2, 4, 128 166), with 64 2, 4, 128 (531, 562)
-//        8-bit 1, 4, 128 kThird 1.9%, 1, 8, 128 kHalf 8.7%, parted at 2048 tiles 1.5%; with many
-//              tokens 1, 8, 128 kWhole (64 tokens, 2 of 8 experts 277 us, kHalf 295; 32 234, 232)
-//        4-bit 1, 4, 128 kThird 2.4%, 1, 8, 256 kWhole 8.8%, parted at 2048 tiles 2.1%; of 64
-//              tokens, 2 of 8 experts 208 us, 1, 4, 128 kHalf 228
+//        8-bit 1, 4, 128 kThird 1.9%, 1, 8, 128 kHalf 8.7%, parted at 2048 tiles 1.4%; with more
+//              than 16 tokens 1, 4, 128 kHalf 1.6%, kThird 4.0%, 1, 8, 128 kHalf 9.5% and of the
+//              large layers 2.0%, 7.9%, 1.7%, parted at 4000 tiles 1.3% and 1.5%
+//        4-bit 1, 4, 128 kThird 2.4%, 1, 8, 256 kWhole 8.8%, parted at 2048 tiles 2.1%; with more
+//              than 16 tokens 1, 4, 128 kHalf 2.0%, kThird 4.0%, 1, 8, 256 kWhole 8.3% and of the
+//              large layers 4.3%, 9.3%, 2.7%
 // All of them add a sum's terms in the same order, so the choice, which depends on the
 // number of tokens, leaves a token's bits as they are.
 template <int WF>
@@ -1036,12 +1038,13 @@ hipError_t run_tiled_down(const MoeArgs& p, hipStream_t stream) {
            : p.m <= 16    ? run_tile<WF, true, 1, 4, 256, kWhole>(p, stream)
                           : run_tile<WF, true, 2, 4, 128, kWhole>(p, stream);
   else if constexpr (WF == EXPERT_INT8)
-    return most < 2048 ? run_tile<WF, true, 1, 4, 128, kThird>(p, stream)
-           : p.m > 32  ? run_tile<WF, true, 1, 8, 128, kWhole>(p, stream)
-                       : run_tile<WF, true, 1, 8, 128, kHalf>(p, stream);
+    return most >= (p.m > 16 ? 4000 : 2048) ? run_tile<WF, true, 1, 8, 128, kHalf>(p, stream)
+           : p.m > 16                       ? run_tile<WF, true, 1, 4, 128, kHalf>(p, stream)
+                                            : run_tile<WF, true, 1, 4, 128, kThird>(p, stream);
   else
-    return most < 2048 ? run_tile<WF, true, 1, 4, 128, kThird>(p, stream)
-                       : run_tile<WF, true, 1, 8, 256, kWhole>(p, stream);
+    return most >= 2048 ? run_tile<WF, true, 1, 8, 256, kWhole>(p, stream)
+           : p.m > 16   ? run_tile<WF, true, 1, 4, 128, kHalf>(p, stream)
+                        : run_tile<WF, true, 1, 4, 128, kThird>(p, stream);
 }
 
 // The streamed forms, by wavefronts, each with what it measured (us a layer in a graph;
