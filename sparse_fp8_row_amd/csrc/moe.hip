@@ -746,8 +746,9 @@ __global__ __launch_bounds__(64 * NW) void moe_down_kernel(MoeArgs p) {
 // puts its own weight tiles and a share of the activation in flight, D - 1 units
 // ahead, and one barrier a unit publishes them.  The weight, read once, is loaded
 // non-temporally (a layer for 64 tokens, 2 of 8 experts, k = 4096, f = 14336, 8-bit 297 -> 256
-// us, bf16 501 -> 458; 16 tokens, 8 of 64, k = 2048, f = 1408, bf16 139 -> 127).  The number of 16-row blocks of
-// the expert's tokens picks the loop (NB), and with it how many units fit LDS.
+// us, bf16 501 -> 458; 16 tokens, 8 of 64, k = 2048, f = 1408, bf16 139 -> 127).  The
+// number of 16-row blocks of the expert's tokens picks the loop (NB), and with it how
+// many units fit LDS.
 // The groups of NW wavefronts' tiles of all chosen experts are split evenly over as
 // many workgroups as the CUs hold.  A group of an expert with many tokens takes longer
 // where the weight has to be converted, so 8- and 4-bit groups are dealt out one by one
@@ -949,9 +950,9 @@ constexpr int kLdsLeft = 160 * 1024 - (int)sizeof(ManyChoices::Shared) - (int)si
 // Whether the layer is two launches of the streaming kernels, or three of the tiled
 // ones.  Every workgroup that streams loads all tokens' activation for 16 or 32
 // weight rows, where the tiled ones share it, so it is for few tokens on few
-// experts (us, streamed against tiled: 8 tokens E8 8-bit 180, 180, bf16 309, 325; 5 tokens
-// E8 4-bit 103, 112; 4 tokens on 4 of 16 experts of 1024 x 512 15.4, 19.3; but 4 tokens E64
-// bf16 82, 71; 8 tokens E64 8-bit 78, 57).
+// experts (us, streamed against tiled: 8 tokens E8 8-bit 182, 208, bf16 351, 345; 5 tokens
+// E8 4-bit 105, 126; 4 tokens on 4 of 16 experts of 1024 x 512 8-bit 14.1, 16.9; but 4
+// tokens E64 bf16 89, 88, 8-bit 59, 48; 8 tokens E64 8-bit 87, 63).
 bool streamed(int64_t m, int top) { return m <= 2 || (m <= 8 && top <= 4); }
 
 template <int WF, int RT, int R, int NW, int D>
