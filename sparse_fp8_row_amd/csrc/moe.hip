@@ -16,8 +16,9 @@ namespace {
 // ---------------------------------------------------------------------------
 
 // logits[t, e] = x[t] . w[e] + bias[e], summed in binary64 and rounded once to
-// binary32: every product of two bf16 values is exact in binary32, so the sum's
-// rounding (2^-53) is all there is before the last, and which of two nearly equal
+// binary32: every product of two bf16 values is exact in binary64 (in binary32 it can
+// overflow, vanish or be rounded among the subnormals), so the sum's rounding
+// (2^-53) is all there is before the last, and which of two nearly equal
 // experts a token takes does not depend on the batch, the tiling or the order.
 //
 // Few tokens: a workgroup per expert and T tokens, its threads share k.
@@ -39,8 +40,8 @@ __global__ __launch_bounds__(256) void route_few_kernel(RouteArgs p) {
       const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        sum[t] += (double)(bf16_to_f32(aw[i] & 0xFFFFu) * bf16_to_f32(bw[i] & 0xFFFFu));
-        sum[t] += (double)(bf16_to_f32(aw[i] >> 16) * bf16_to_f32(bw[i] >> 16));
+        sum[t] += (double)bf16_to_f32(aw[i] & 0xFFFFu) * (double)bf16_to_f32(bw[i] & 0xFFFFu);
+        sum[t] += (double)bf16_to_f32(aw[i] >> 16) * (double)bf16_to_f32(bw[i] >> 16);
       }
     }
   }
