@@ -640,8 +640,8 @@ typedef enum { SFR_ROUTE_SOFTMAX = 0, SFR_ROUTE_SIGMOID = 1 } sfr_route_t;
  *                     rounded; -0 equals 0) the lowest expert comes first
  *     weights[t, s] = score of logits[t, ids[t, s]], divided by the sum of the
  *                     chosen experts' scores where renormalize is not 0
- * The sum is formed in binary64 and rounded once to binary32, so that the choice
- * does not depend on the other tokens of a call.  An expert with logit -infinity (a
+ * The sum is formed in binary64, in the same order in every call, and rounded once to
+ * binary32, so that a token's results do not depend on the other tokens of a call.  An expert with logit -infinity (a
  * bias of -infinity shuts it off) is never chosen: a slot left over has id -1 and
  * weight 0.  NaN counts as larger than everything else and makes the weights NaN.
  *

@@ -17,70 +17,122 @@ namespace {
 
 // logits[t, e] = x[t] . w[e] + bias[e], summed in binary64 and rounded once to
 // binary32: every product of two bf16 values is exact in binary64 (in binary32 it can
-// overflow, vanish or be rounded among the subnormals), so the sum's rounding
-// (2^-53) is all there is before the last, and which of two nearly equal
-// experts a token takes does not depend on the batch, the tiling or the order.
+// overflow, vanish or be rounded among the subnormals).
 //
-// Few tokens: a workgroup per expert and T tokens, its threads share k.
-constexpr int kFewTokens = 4;
-
-__global__ __launch_bounds__(256) void route_few_kernel(RouteArgs p) {
-  constexpr int T = kFewTokens;
-  __shared__ double red[4][T];
-  const int tid = threadIdx.x, e = blockIdx.x;
-  const int64_t t0 = (int64_t)blockIdx.y * T;
-  double sum[T] = {};
-  for (int c = tid; c < p.k / 8; c += 256) {
-    const uint4 b = reinterpret_cast<const uint4*>(p.w + (int64_t)e * p.k)[c];
-    const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int t = 0; t < T; ++t) {
-      if (t0 + t >= p.m) continue;
-      const uint4 a = reinterpret_cast<const uint4*>(p.x + (t0 + t) * p.k)[c];
-      const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        sum[t] += (double)bf16_to_f32(aw[i] & 0xFFFFu) * (double)bf16_to_f32(bw[i] & 0xFFFFu);
-        sum[t] += (double)bf16_to_f32(aw[i] >> 16) * (double)bf16_to_f32(bw[i] >> 16);
-      }
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < T; ++t) {
-#pragma unroll
-    for (int d = 32; d >= 1; d /= 2) sum[t] += __shfl_xor(sum[t], d);
-    if ((tid & 63) == 0) red[tid >> 6][t] = sum[t];
-  }
-  __syncthreads();
-  if (tid < T && t0 + tid < p.m) {
-    double s = ((red[0][tid] + red[1][tid]) + red[2][tid]) + red[3][tid];
-    if (p.bias) s += (double)p.bias[e];
-    p.logits[(t0 + tid) * p.experts + e] = (float)s;
-  }
-}
-
-// More tokens: on v_mfma_f64_16x16x4_f64 (lane l holds A row and B column l % 16 at
-// k l / 16, and rows 4 i + l / 16 of D's column l % 16).  A workgroup owns 16 TB tokens
-// x 16 EB experts and its eight wavefronts an eighth of k each, in steps of 32: a lane
-// loads eight values of each operand, whose j-th go into the j-th instruction (any
-// order of k serves, the same for both).  Bound by the binary64 rate (64 cycles an
-// instruction) and, at a third of that again, by the conversions of its operands.
-// One block a workgroup fills the CUs evenly; from 1024 blocks on 2 x 2, which halves
-// the conversions (k = 4096, logits and choice in a graph, us: 1000 tokens, 161
-// experts 39.6, in 2 x 2 44.0; 1024, 256 49.8, 44.8; 4096, 128 89.9, 78.9).  Up to
-// kFewLogits the form above is faster (96 x 128 16.2, 17.4; 128 x 128 19.1, 17.3; 64 x 128
-// 13.6, 17.3).
-constexpr int64_t kFewLogits = 12288;
-typedef double v4d __attribute__((ext_vector_type(4)));
+// All kernels add in the same order, so a token's logits, and which of two nearly
+// equal experts it takes, depend on nothing but its row and the experts': k is taken in
+// steps of 32; chain s % 32 adds step s's products by fused multiply-adds, in the order
+// j = 0 .. 7, lg = 0 .. 3 of k = 8 lg + j (the binary64 matrix instructions do just that
+// over their own k, lg here, in both shapes); chains w, w + 8, w + 16, w + 24 join in this
+// order to the sum of w = 0 .. 7, and these as waves_joined says.
+constexpr int kChains = 4, kRouteWaves = 8;
 
 __device__ __forceinline__ double bf16_to_f64(const uint4& v, int i) {
   const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
   return (double)(i & 1 ? __uint_as_float(w & 0xFFFF0000u) : bf16_to_f32(w & 0xFFFFu));
 }
 
-template <int TB, int EB, int NW>  // blocks of 16 tokens and experts, wavefronts
-__global__ __launch_bounds__(64 * NW) void route_many_kernel(RouteArgs p) {
-  constexpr int H = NW / 2;
+template <class F>  // of(w): the sum of w
+__device__ __forceinline__ auto waves_joined(F of) {
+  auto s = of(0) + of(4);
+#pragma unroll
+  for (int w = 1; w < kRouteWaves / 2; ++w) s += of(w) + of(w + 4);
+  return s;
+}
+
+// Few tokens: on v_mfma_f64_4x4x4_4b_f64 (lane l holds row l % 4 of both operands at k
+// l / 16, of block l / 4 % 4, and row l / 16, column l % 4 of that block of D).  The
+// blocks are the chains of one w, and its rows
+//   4 tokens and 4 experts, with a w for each of eight wavefronts, or
+//   ONE: four w of one token and one expert, in two wavefronts; of D only the diagonal
+//     counts.  That takes four times the instructions, on sixteen times the
+//     workgroups, and serves so few logits that CUs are idle (up to kOneLogits).
+// A wavefront streams four rows of each operand, a step of every chain at a time, through
+// LDS buffers of its own, kRouteDepth - 1 ahead (three and four buffers: 1 to 5% slower).  Bound
+// by the conversions to binary64 (16 cycles each, two an instruction), for one token by
+// the two launches.
+constexpr int kRouteDepth = 2;
+
+template <bool ONE>
+__global__ __launch_bounds__(ONE ? 128 : 64 * kRouteWaves) void route_few_kernel(RouteArgs p) {
+  static_assert(kChains == 4 && kRouteWaves == 8, "the blocks and rows of the instruction, the order of the joins");
+  constexpr int D = kRouteDepth, N = ONE ? 1 : 4;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t smem[];
+  __shared__ double red[kRouteWaves][N * N];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row = lane & 3, block = lane >> 2 & 3, lg = lane >> 4;
+  const int e0 = blockIdx.x * N;
+  const int64_t t0 = (int64_t)blockIdx.y * N;
+  const __amdgpu_buffer_rsrc_t rx = buf_rsrc(p.x + t0 * p.k, kPastRange);
+  const __amdgpu_buffer_rsrc_t rw = buf_rsrc(p.w + (int64_t)e0 * p.k, kPastRange);
+  uint8_t* const mine = smem + wave * (D * 2048);
+  // lane l loads row l / 16, block l / 4 % 4, lg l % 4 ^ row: what eight lanes read of LDS at
+  // once (two blocks, four rows) then lies in different banks
+  const int ahead = 8 * block + (ONE ? lg : 0);  // the lane's step, from the wavefront's first one on
+  const int from = (ONE ? 0 : lg * p.k * 2) + ahead * 64 + 16 * (row ^ lg);
+  const int at = 16 * (16 * row + 4 * block + (lg ^ row));
+  const int steps = p.k / 32;
+  const bool token = ONE || lg < p.m - t0, expert = ONE || lg < p.experts - e0;
+  auto issue = [&](int buf, int s0) __attribute__((always_inline)) {
+    const bool in = s0 + ahead < steps;  // past the ends zeros, which leave a sum as it is
+    buf_to_lds(rx, mine + buf * 2048, in && token ? from + s0 * 64 : kPastRange);
+    buf_to_lds(rw, mine + buf * 2048 + 1024, in && expert ? from + s0 * 64 : kPastRange);
+  };
+  const int first = ONE ? 4 * wave : wave;
+#pragma unroll
+  for (int i = 0; i < D - 1; ++i) issue(i, first + 32 * i);
+  double sum = 0;
+  int buf = 0;
+  for (int s0 = first; s0 < steps; s0 += 32) {
+    wait_lds();  // the buffer to be refilled has been read
+    issue(buf == 0 ? D - 1 : buf - 1, s0 + 32 * (D - 1));
+    wait_vm<2 * (D - 1)>();
+    asm volatile("" ::: "memory");
+    const uint4 a = *reinterpret_cast<const uint4*>(mine + buf * 2048 + at);
+    const uint4 b = *reinterpret_cast<const uint4*>(mine + buf * 2048 + 1024 + at);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      sum = __builtin_amdgcn_mfma_f64_4x4x4f64(bf16_to_f64(a, j), bf16_to_f64(b, j), sum, 0, 0, 0);
+    buf = buf == D - 1 ? 0 : buf + 1;
+  }
+  wait_vm<0>();  // the loads past the last step (zeros) end before the workgroup's LDS does
+  sum = ((sum + __shfl_xor(sum, 4)) + __shfl_xor(sum, 8)) + __shfl_xor(sum, 12);  // (right where block is 0)
+  if constexpr (ONE) {
+    if (block == 0 && row == lg) red[4 * wave + row][0] = sum;
+  } else {
+    if (block == 0) red[wave][4 * lg + row] = sum;
+  }
+  __syncthreads();
+  const int64_t t = t0 + threadIdx.x / N;
+  const int e = e0 + threadIdx.x % N;
+  if (threadIdx.x < N * N && t < p.m && e < p.experts) {
+    const double s = waves_joined([&](int w) { return red[w][threadIdx.x]; });
+    p.logits[t * p.experts + e] = (float)(s + (p.bias ? (double)p.bias[e] : -0.0));
+  }
+}
+
+// More tokens: on v_mfma_f64_16x16x4_f64 (lane l holds A row and B column l % 16 at
+// k l / 16, and rows 4 i + l / 16 of D's column l % 16).  A workgroup owns 16 TB tokens
+// x 16 EB experts and each of its eight wavefronts the chains of one w: a lane loads
+// eight values of each operand, whose j-th go into the j-th instruction.  Bound by the
+// binary64 rate (64 cycles an instruction) and, at a third of that again, by the
+// conversions of its operands.
+//
+// The forms, logits and choice in a graph, us:
+//   ONE and 4 x 4: 64 logits of k = 2048 5.4, 5.6; 256 of k = 4096 7.1, 7.6; 256 (4 x 64) of
+//     k = 2048 5.4, 5.6; 512 (8 x 64) 5.9, 5.9; 2048 (16 x 128) of k = 4096 8.7, 7.3;
+//   4 x 4 and one block of 16 x 16, k = 4096: 64 x 256 12.7, 17.2; 384 x 64 13.8, 15.5; 192 x 160
+//     17.8, 17.0; 128 x 256 18.2, 17.3; k = 1024: 96 x 160 8.8, 9.6; 192 x 160 10.9, 9.7;
+//   one block fills the CUs evenly, 2 x 2 halve the conversions, from 1024 blocks on, k =
+//     4096: 1000 x 161 37.6, 43.3; 1024 x 256 47.6, 44.0; 4096 x 128 86, 78; 8192 x 256 321,
+//     286; a rule of their number alone, it is wrong where 2 x 2 leave a last round nearly
+//     empty (1100 x 250 57, 78) or cover experts that are not there (16384 x 16 51, 81).
+constexpr int64_t kOneLogits = 256, kFewLogits = 24576;
+typedef double v4d __attribute__((ext_vector_type(4)));
+
+template <int TB, int EB>  // blocks of 16 tokens and experts
+__global__ __launch_bounds__(64 * kRouteWaves) void route_many_kernel(RouteArgs p) {
+  constexpr int NW = kRouteWaves, H = NW / 2;
   __shared__ v4d red[H][TB * EB][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, lg = lane >> 4;
@@ -92,11 +144,6 @@ __global__ __launch_bounds__(64 * NW) void route_many_kernel(RouteArgs p) {
   for (int i = 0; i < TB; ++i) px[i] = p.x + min(t0 + 16 * i + r16, p.m - 1) * p.k + 8 * lg;
 #pragma unroll
   for (int i = 0; i < EB; ++i) pw[i] = p.w + (int64_t)min(e0 + 16 * i + r16, p.experts - 1) * p.k + 8 * lg;
-  v4d acc[TB][EB];
-#pragma unroll
-  for (int i = 0; i < TB; ++i)
-#pragma unroll
-    for (int j = 0; j < EB; ++j) acc[i][j] = v4d{0, 0, 0, 0};
   const int steps = p.k / 32;
   uint4 x[TB], w[EB];
   auto load = [&](int s) __attribute__((always_inline)) {
@@ -106,44 +153,55 @@ __global__ __launch_bounds__(64 * NW) void route_many_kernel(RouteArgs p) {
     for (int i = 0; i < EB; ++i) w[i] = *reinterpret_cast<const uint4*>(pw[i] + s * 32);
   };
   if (wave < steps) load(wave);
-  for (int s = wave; s < steps; s += NW) {
-    uint4 a[TB], b[EB];
+  v4d sum[TB * EB];
 #pragma unroll
-    for (int i = 0; i < TB; ++i) a[i] = x[i];
-#pragma unroll
-    for (int i = 0; i < EB; ++i) b[i] = w[i];
-    if (s + NW < steps) load(s + NW);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      double xa[TB], wb[EB];
-#pragma unroll
-      for (int i = 0; i < TB; ++i) xa[i] = bf16_to_f64(a[i], k);
-#pragma unroll
-      for (int i = 0; i < EB; ++i) wb[i] = bf16_to_f64(b[i], k);
-#pragma unroll
-      for (int i = 0; i < TB; ++i)
-#pragma unroll
-        for (int j = 0; j < EB; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f64_16x16x4f64(xa[i], wb[j], acc[i][j], 0, 0, 0);
-    }
-  }
-  // the wavefronts' sums join in a fixed order: w, w + H; then 0 .. H - 1
-  if (wave >= H) {
+  for (int b = 0; b < TB * EB; ++b) sum[b] = v4d{0, 0, 0, 0};
+  // chain by chain, so that one chain's sums are all that is held beside the joined ones'
+  for (int c = 0; c < kChains; ++c) {
+    v4d acc[TB][EB];
 #pragma unroll
     for (int i = 0; i < TB; ++i)
 #pragma unroll
-      for (int j = 0; j < EB; ++j) red[wave - H][i * EB + j][lane] = acc[i][j];
+      for (int j = 0; j < EB; ++j) acc[i][j] = v4d{0, 0, 0, 0};
+    for (int s = wave + NW * c; s < steps; s += NW * kChains) {
+      uint4 a[TB], b[EB];
+#pragma unroll
+      for (int i = 0; i < TB; ++i) a[i] = x[i];
+#pragma unroll
+      for (int i = 0; i < EB; ++i) b[i] = w[i];
+      const int on = s + NW * kChains, next = on < steps ? on : wave + NW * (c + 1);
+      if (next < steps) load(next);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        double xa[TB], wb[EB];
+#pragma unroll
+        for (int i = 0; i < TB; ++i) xa[i] = bf16_to_f64(a[i], k);
+#pragma unroll
+        for (int i = 0; i < EB; ++i) wb[i] = bf16_to_f64(b[i], k);
+#pragma unroll
+        for (int i = 0; i < TB; ++i)
+#pragma unroll
+          for (int j = 0; j < EB; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f64_16x16x4f64(xa[i], wb[j], acc[i][j], 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < TB; ++i)
+#pragma unroll
+      for (int j = 0; j < EB; ++j) sum[i * EB + j] += acc[i][j];
+  }
+  if (wave >= H) {
+#pragma unroll
+    for (int b = 0; b < TB * EB; ++b) red[wave - H][b][lane] = sum[b];
   }
   __syncthreads();
   if (wave < H) {
 #pragma unroll
-    for (int i = 0; i < TB; ++i)
-#pragma unroll
-      for (int j = 0; j < EB; ++j) red[wave][i * EB + j][lane] += acc[i][j];
+    for (int b = 0; b < TB * EB; ++b) red[wave][b][lane] += sum[b];
   }
   __syncthreads();
   for (int b = wave; b < TB * EB; b += NW) {
-    v4d s = red[0][b][lane];
+    v4d s = red[0][b][lane];  // in the order of waves_joined
 #pragma unroll
     for (int h = 1; h < H; ++h) s += red[h][b][lane];
     const int e = e0 + 16 * (b % EB) + r16;
@@ -1082,7 +1140,7 @@ void run_many(const RouteArgs& a, hipStream_t stream) {
     p.m = a.m - t;
     const int64_t groups = (p.m + 16 * TB - 1) / (16 * TB);
     const dim3 grid((unsigned)((a.experts + 16 * EB - 1) / (16 * EB)), (unsigned)(groups < 65535 ? groups : 65535));
-    route_many_kernel<TB, EB, 8><<<grid, dim3(512), 0, stream>>>(p);
+    route_many_kernel<TB, EB><<<grid, dim3(64 * kRouteWaves), 0, stream>>>(p);
   }
 }
 
@@ -1090,8 +1148,11 @@ void run_many(const RouteArgs& a, hipStream_t stream) {
 
 hipError_t launch_moe_route(const RouteArgs& a, hipStream_t stream) {
   const int64_t blocks = ((a.m + 15) / 16) * ((a.experts + 15) / 16);
-  if (a.m * a.experts <= kFewLogits)
-    route_few_kernel<<<dim3(a.experts, (unsigned)((a.m + kFewTokens - 1) / kFewTokens)), dim3(256), 0, stream>>>(a);
+  if (a.m * a.experts <= kOneLogits)
+    route_few_kernel<true><<<dim3(a.experts, (unsigned)a.m), dim3(128), 2 * kRouteDepth * 2048, stream>>>(a);
+  else if (a.m * a.experts <= kFewLogits)
+    route_few_kernel<false><<<dim3((a.experts + 3) / 4, (unsigned)((a.m + 3) / 4)), dim3(64 * kRouteWaves),
+                              kRouteWaves * kRouteDepth * 2048, stream>>>(a);
   else if (blocks < 1024) run_many<1, 1>(a, stream);
   else run_many<2, 2>(a, stream);
   const dim3 grid((unsigned)((a.m + 3) / 4)), block(256);

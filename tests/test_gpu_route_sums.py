@@ -6,8 +6,8 @@ import pytest
 import torch
 
 pytestmark = pytest.mark.gpu
-# tokens of a call of ten experts, or of what a test takes
-CALLS = [1, 7, 2000, 17000]
+# tokens of a call of ten experts: each of the kernels
+CALLS = [1, 7, 40, 2000, 5000, 17000]
 
 
 @pytest.fixture(scope="module")
@@ -66,3 +66,33 @@ def test_infinities(sfr, m):
     r = sfr.moe_route(tokens(x, m), w.bfloat16().cuda(), 2)
     want = (x[:, None] * w[None]).sum(2)[torch.arange(m) % 4].float()
     assert same(r.logits.cpu(), want)
+
+
+@pytest.mark.parametrize("k", [32, 64, 288, 1024, 1056, 2080, 4096, 7200])
+def test_sums_do_not_depend_on_the_call(sfr, k):
+    """Sums that cancel until only what binary64 lost is left, so that another order of
+    their terms is another logit: the same bits for a token alone, in small and in large
+    calls, and for an expert among others."""
+    g = torch.Generator().manual_seed(k)
+    m, experts = 17000, 10
+
+    def wide(rows):  # values over 2^80, every one of them once more
+        v = torch.randn(rows, k // 2, generator=g) * torch.exp2(torch.randint(-40, 40, (rows, k // 2), generator=g).float())
+        return torch.cat((v, v), 1).bfloat16()
+    x, w = wide(40)[torch.arange(m) % 40].cuda(), wide(experts).cuda()
+    w[:, k // 2:] *= -1
+    order = torch.randperm(k, generator=g).cuda()
+    x, w = x[:, order].contiguous(), w[:, order].contiguous()
+    whole = sfr.moe_route(x, w, 3)
+    # sums that lost nothing would be 0
+    assert bool((whole.logits[:40] != 0).any()) or k < 64
+    for rows in (slice(0, 1), slice(1, 6), slice(3, 40), slice(7, 1300), slice(100, 6000), slice(10, 16900)):
+        part = sfr.moe_route(x[rows].clone(), w, 3)
+        assert torch.equal(part.logits, whole.logits[rows]) and torch.equal(part.ids, whole.ids[rows]), rows
+        assert torch.equal(part.weights, whole.weights[rows]), rows
+    among = torch.randperm(300, generator=g)[:experts].cuda()
+    many = wide(300).cuda()
+    many[among] = w
+    for rows in (slice(0, 1), slice(0, 30), slice(0, 100), slice(0, 1000)):
+        part = sfr.moe_route(x[rows].clone(), many, 3)
+        assert torch.equal(part.logits[:, among], whole.logits[rows]), rows
