@@ -1155,12 +1155,18 @@ hipError_t launch_moe_route(const RouteArgs& a, hipStream_t stream) {
                               kRouteWaves * kRouteDepth * 2048, stream>>>(a);
   else if (blocks < 1024) run_many<1, 1>(a, stream);
   else run_many<2, 2>(a, stream);
-  const dim3 grid((unsigned)((a.m + 3) / 4)), block(256);
   auto* select = a.experts <= 64    ? route_select_kernel<1>
                  : a.experts <= 128 ? route_select_kernel<2>
                  : a.experts <= 256 ? route_select_kernel<4>
                                     : route_select_kernel<kMoeExperts / 64>;
-  select<<<grid, block, 0, stream>>>(a);
+  for (int64_t t = 0; t < a.m; t += kGridRows) {
+    RouteArgs p = a;
+    p.logits = a.logits + t * a.experts;
+    p.ids = a.ids + t * a.top;
+    p.weights = a.weights + t * a.top;
+    p.m = a.m - t < kGridRows ? a.m - t : kGridRows;
+    select<<<dim3((unsigned)((p.m + 3) / 4)), dim3(256), 0, stream>>>(p);
+  }
   return hipGetLastError();
 }
 

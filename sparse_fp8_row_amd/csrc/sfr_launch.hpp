@@ -157,6 +157,9 @@ DenseKernel dense_dw_kernel(int64_t m, int64_t k, int64_t f2);
 enum { PRODUCT_GATED = 0, PRODUCT_GATED_SAVING, PRODUCT_DX, PRODUCT_DW, PRODUCT_MXFP4, PRODUCT_MXFP4_GATED };
 DenseKernel block_kernel(int product, int64_t m, int64_t k, int64_t f);
 
+// Rows of one launch with a wavefront per row: a grid has fewer than 2^32 threads.
+constexpr int64_t kGridRows = (int64_t)1 << 25;
+
 // 8-bit integers with a scale per row: the quantizer, and the product of two
 // quantized matrices (or of a bf16 x, quantized into the workspace first).
 hipError_t launch_quantize_int8(const uint16_t* x, int64_t rows, int64_t cols, int8_t* q, float* scale,

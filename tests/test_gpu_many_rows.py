@@ -1,0 +1,32 @@
+"""GPU: more rows than the wavefronts of one grid (2^26)."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+P, REPS = 1025, 65537  # 67175425 rows, the same 1025 again and again
+
+
+@pytest.fixture(scope="module")
+def sfr():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import sparse_fp8_row_amd as sfr
+    sfr.load()
+    return sfr
+
+
+def rows(cols, seed):
+    g = torch.Generator("cuda").manual_seed(seed)
+    return torch.randn(P, cols, generator=g, device="cuda").bfloat16()
+
+
+def repeats(whole, part):
+    return torch.equal(whole.view(REPS, *part.shape), part.expand(REPS, *part.shape))
+
+
+def test_router(sfr):
+    x = rows(32, 1)
+    w = rows(32, 2)[:3].contiguous()
+    part = sfr.moe_route(x, w, 2)
+    whole = sfr.moe_route(x.repeat(REPS, 1), w, 2)
+    assert whole.ids.shape[0] > 1 << 26
+    assert repeats(whole.logits, part.logits) and repeats(whole.ids, part.ids) and repeats(whole.weights, part.weights)
