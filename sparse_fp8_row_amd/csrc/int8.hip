@@ -214,10 +214,13 @@ hipError_t launch_quantize_int8(const uint16_t* x, int64_t rows, int64_t cols, i
     else quantize_int8_kernel<2, 1024, true><<<grid, dim3(1024), 0, stream>>>(x, rows, c, q, scale);
     return hipGetLastError();
   }
-  const dim3 grid((unsigned)((rows + 3) / 4)), block(256);
-  if (cols <= 2048) quantize_int8_kernel<4, 256, false><<<grid, block, 0, stream>>>(x, rows, c, q, scale);
-  else if (cols <= 4096) quantize_int8_kernel<8, 256, false><<<grid, block, 0, stream>>>(x, rows, c, q, scale);
-  else quantize_int8_kernel<16, 256, false><<<grid, block, 0, stream>>>(x, rows, c, q, scale);
+  auto* kernel = cols <= 2048   ? quantize_int8_kernel<4, 256, false>
+                 : cols <= 4096 ? quantize_int8_kernel<8, 256, false>
+                                : quantize_int8_kernel<16, 256, false>;
+  for (int64_t r = 0; r < rows; r += kGridRows) {
+    const int64_t n = rows - r < kGridRows ? rows - r : kGridRows;
+    kernel<<<dim3((unsigned)((n + 3) / 4)), dim3(256), 0, stream>>>(x + r * cols, n, c, q + r * cols, scale + r);
+  }
   return hipGetLastError();
 }
 

@@ -30,3 +30,15 @@ def test_router(sfr):
     whole = sfr.moe_route(x.repeat(REPS, 1), w, 2)
     assert whole.ids.shape[0] > 1 << 26
     assert repeats(whole.logits, part.logits) and repeats(whole.ids, part.ids) and repeats(whole.weights, part.weights)
+
+
+def test_int8(sfr):
+    """The quantizer, by itself and within the layer."""
+    x = rows(16, 3)
+    w = sfr.quantize_rowwise_int8(rows(16, 4)[:16].contiguous())
+    part, y = sfr.quantize_rowwise_int8(x), sfr.int8_linear(x, w)
+    x = x.repeat(REPS, 1)
+    whole = sfr.quantize_rowwise_int8(x)
+    assert repeats(whole.codes, part.codes) and repeats(whole.scale, part.scale)
+    del whole
+    assert repeats(sfr.int8_linear(x, w), y)
