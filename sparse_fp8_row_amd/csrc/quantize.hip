@@ -153,19 +153,21 @@ hipError_t launch_fmt(const uint16_t* x, int64_t rows, int64_t cols, uint8_t* q,
     return hipGetLastError();
   }
   const int64_t per_lane = ((cols >> 3) + 63) / 64;
-  const dim3 grid((unsigned)((rows + kRowsPerBlock - 1) / kRowsPerBlock)), block(256);
-#define SFR_Q(R) hipLaunchKernelGGL((quantize_rows_kernel<FMT, R>), grid, block, 0, stream, x, rows, cols, q, scale)
+  auto* kernel = quantize_rows_kernel<FMT, 0>;
   // R = chunks per lane; rows of exactly 64 * R chunks (K = 4096 -> 8, K = 14336
   // -> 28) take the unconditional-load path
-  if (per_lane <= 1) SFR_Q(1);
-  else if (per_lane <= 2) SFR_Q(2);
-  else if (per_lane <= 4) SFR_Q(4);
-  else if (per_lane <= 8) SFR_Q(8);
-  else if (per_lane <= 16) SFR_Q(16);
-  else if (per_lane <= 28) SFR_Q(28);
-  else if (per_lane <= 32) SFR_Q(32);
-  else SFR_Q(0);
-#undef SFR_Q
+  if (per_lane <= 1) kernel = quantize_rows_kernel<FMT, 1>;
+  else if (per_lane <= 2) kernel = quantize_rows_kernel<FMT, 2>;
+  else if (per_lane <= 4) kernel = quantize_rows_kernel<FMT, 4>;
+  else if (per_lane <= 8) kernel = quantize_rows_kernel<FMT, 8>;
+  else if (per_lane <= 16) kernel = quantize_rows_kernel<FMT, 16>;
+  else if (per_lane <= 28) kernel = quantize_rows_kernel<FMT, 28>;
+  else if (per_lane <= 32) kernel = quantize_rows_kernel<FMT, 32>;
+  for (int64_t r = 0; r < rows; r += kGridRows) {
+    const int64_t n = rows - r < kGridRows ? rows - r : kGridRows;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((n + kRowsPerBlock - 1) / kRowsPerBlock)), dim3(256), 0, stream,
+                       x + r * cols, n, cols, q + r * cols, scale + r);
+  }
   return hipGetLastError();
 }
 

@@ -42,3 +42,11 @@ def test_int8(sfr):
     assert repeats(whole.codes, part.codes) and repeats(whole.scale, part.scale)
     del whole
     assert repeats(sfr.int8_linear(x, w), y)
+
+
+@pytest.mark.parametrize("fmt", [torch.float8_e4m3fn, torch.float8_e5m2])
+def test_fp8(sfr, fmt):
+    x = rows(8, 5)
+    codes, scale = sfr.quantize_rowwise_fp8(x, fmt)
+    many, scales = sfr.quantize_rowwise_fp8(x.repeat(REPS, 1), fmt)
+    assert repeats(many.view(torch.uint8), codes.view(torch.uint8)) and repeats(scales, scale)
