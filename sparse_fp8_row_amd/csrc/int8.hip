@@ -174,10 +174,24 @@ __global__ __launch_bounds__(kFusedThreads) void int8_fused_kernel(Int8Args p) {
 // Whether a bf16 x of m rows is quantized in the product's own launch.
 bool fused(int64_t m, int64_t k) { return m * ((k / 8 + kFusedThreads - 1) / kFusedThreads) <= kFusedChunks; }
 
+// Bytes of LDS of m rows of k, and the most of any call that fused() admits: the
+// kernel's limit is shared by all host threads, so every call sets it to the same.
+constexpr int fused_bytes(int m, int k) { return kFusedWaves * kFusedDepth * 16 * kFusedUnit + m * codes_stride(k); }
+constexpr int most_fused_bytes() {
+  int most = 0;
+  for (int m = 1; m <= kFusedChunks; ++m) {
+    const int bytes = fused_bytes(m, kFusedChunks / m * kFusedThreads * 8);
+    if (bytes > most) most = bytes;
+  }
+  return most;
+}
+
 hipError_t launch_fused(const Int8Args& a, hipStream_t stream) {
-  const int bytes = kFusedWaves * kFusedDepth * 16 * kFusedUnit + (int)a.m * codes_stride((int)a.k);
+  constexpr int limit = most_fused_bytes();
+  static_assert(limit + 5 * 1024 <= 160 * 1024, "LDS of a CU");
+  const int bytes = fused_bytes((int)a.m, (int)a.k);
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(int8_fused_kernel),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, limit);
   if (e != hipSuccess) return e;
   // as many workgroups as the CUs hold, each the same number of tiles, or one fewer
   const int tiles = (int)(a.n / 16), most = 256 * (160 * 1024 / (bytes + 5 * 1024)), each = (tiles + most - 1) / most;
