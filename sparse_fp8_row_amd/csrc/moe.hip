@@ -433,15 +433,15 @@ __device__ __forceinline__ int row_bytes(int k) {
 }
 
 // Puts a unit's 16 weight rows and (4-bit) scales in flight: k from u UK on, of
-// which `left` exist (zeros past them; none for left <= 0).
-template <int WF, bool NT, class U>
+// which `left` exist (zeros past them; none for left <= 0).  Non-temporal: the weight is read once.
+template <int WF, class U>
 __device__ __forceinline__ void issue_weight(__amdgpu_buffer_rsrc_t rw, __amdgpu_buffer_rsrc_t rs, uint8_t* b, int u,
                                              int left, int k, int lane) {
   constexpr int WC = U::WROW / 16, WPL = 64 / WC, PER = U::UK / WC;  // chunks per row, rows per load, k per chunk
 #pragma unroll
   for (int j = 0; j < U::WL; ++j) {
     const int row = j * WPL + lane / WC, c = (lane % WC) ^ U::swizzle(row);
-    buf_to_lds<NT>(rw, b + j * 1024, c * PER < left ? row * row_bytes<WF>(k) + u * U::WROW + c * 16 : kPastRange);
+    buf_to_lds<true>(rw, b + j * 1024, c * PER < left ? row * row_bytes<WF>(k) + u * U::WROW + c * 16 : kPastRange);
   }
 #pragma unroll
   for (int j = 0; j < U::SL; ++j) {
@@ -611,7 +611,7 @@ __global__ __launch_bounds__(64 * NW) void moe_up_kernel(MoeArgs p) {
     uint8_t* b = mine + at * L::BYTES;
     const int left = K - u * U::UK;  // may be negative: every lane masked
 #pragma unroll
-    for (int t = 0; t < RT; ++t) issue_weight<WF, true, U>(rw[t], rs[t], b + t * U::TILE, u, left, K, lane);
+    for (int t = 0; t < RT; ++t) issue_weight<WF, U>(rw[t], rs[t], b + t * U::TILE, u, left, K, lane);
 #pragma unroll
     for (int j = 0; j < U::XL; ++j) {
       const int c = (lane % XC) ^ ((j * XPL + lane / XC) & 7);
@@ -721,7 +721,7 @@ __global__ __launch_bounds__(64 * NW) void moe_down_kernel(MoeArgs p) {
     }
     const int left = next < last ? F - unit_in * U::UK : 0;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) issue_weight<WF, true, U>(rw[t], rs[t], b + t * U::TILE, unit_in, left, F, lane);
+    for (int t = 0; t < RT; ++t) issue_weight<WF, U>(rw[t], rs[t], b + t * U::TILE, unit_in, left, F, lane);
 #pragma unroll
     for (int j = 0; j < U::XL; ++j) {
       const int c = (lane % XC) ^ ((j * XPL + lane / XC) & 7);
@@ -872,7 +872,7 @@ __device__ __forceinline__ void moe_tiles(const MoeArgs& p, const TileShared& sh
     const int left = K - unit_in * U::UK;  // not positive past the last unit: every lane masked
 #pragma unroll
     for (int t = 0; t < RT; ++t)
-      issue_weight<WF, true, U>(rw[t], rs[t], b + wave * U::WBYTES + t * U::TILE, unit_in, left, K, lane);
+      issue_weight<WF, U>(rw[t], rs[t], b + wave * U::WBYTES + t * U::TILE, unit_in, left, K, lane);
 #pragma unroll
     for (int j = 0; j < XL; ++j) {
       const int row = (wave * XL + j) * XPL + lane / XC, c = (lane % XC) ^ (row & 7);
