@@ -641,9 +641,11 @@ typedef enum { SFR_ROUTE_SOFTMAX = 0, SFR_ROUTE_SIGMOID = 1 } sfr_route_t;
  *     weights[t, s] = score of logits[t, ids[t, s]], divided by the sum of the
  *                     chosen experts' scores where renormalize is not 0
  * The sum is formed in binary64, in the same order in every call, and rounded once to
- * binary32, so that a token's results do not depend on the other tokens of a call.  An expert with logit -infinity (a
- * bias of -infinity shuts it off) is never chosen: a slot left over has id -1 and
- * weight 0.  NaN counts as larger than everything else and makes the weights NaN.
+ * binary32, so that a token's results do not depend on the other tokens of a call.
+ * An expert with logit -infinity (a bias of -infinity shuts it off) is never chosen:
+ * a slot left over has id -1 and weight 0.  NaN counts as larger than everything else.
+ * It makes a token's weights NaN, and so does +infinity for the softmax; in the
+ * sigmoid without renormalize NaN is the weight of that expert alone.
  *
  *   x [m, k], w [experts, k]: bf16 bits;  bias [experts] binary32 or NULL.
  *   logits [m, experts] binary32, ids [m, top] int32, weights [m, top] binary32: written.
@@ -665,7 +667,8 @@ typedef enum { SFR_EXPERT_BF16 = 0, SFR_EXPERT_INT8 = 1, SFR_EXPERT_MXFP4 = 2 } 
  * to eight with top <= 4), else in three for every 64:
  *     h[t, s]  = act(x[t] Wg[e]^T) * (x[t] Wu[e]^T),  e = ids[t, s]
  *     out[t]   = sum_s weights[t, s] h[t, s] Wd[e]^T
- * Sums are binary32; h is rounded once to bf16, the type in which the second
+ * Sums are binary32 (of 8-bit experts the sums of the codes, which the rows' scales
+ * multiply); h is rounded once to bf16, the type in which the second
  * product reads it, and out once to bf16.  ids outside [0, experts) are no choice
  * (padding, or experts held elsewhere: out is then this device's share); a token
  * without a choice gets zeros.  An expert named twice counts with the sum of its

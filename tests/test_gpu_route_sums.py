@@ -96,3 +96,25 @@ def test_sums_do_not_depend_on_the_call(sfr, k):
     for rows in (slice(0, 1), slice(0, 30), slice(0, 100), slice(0, 1000)):
         part = sfr.moe_route(x[rows].clone(), many, 3)
         assert torch.equal(part.logits[:, among], whole.logits[rows]), rows
+
+
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("m", [1, 40, 6000])
+def test_weights_of_logits_that_are_not_finite(sfr, score, renormalize, m):
+    x, w = torch.zeros(m, 32, device="cuda").bfloat16(), torch.zeros(10, 32, device="cuda").bfloat16()
+    bias = torch.tensor([0.5, -1.0, 2.0, 0.0, 1.0, -math.inf, 3.0, -2.0, 0.25, -0.5], device="cuda")
+    for value in (math.nan, math.inf):
+        bias[4] = value
+        r = sfr.moe_route(x, w, 3, bias, score, renormalize)
+        assert bool((r.ids.cpu() == torch.tensor([4, 6, 2])).all())
+        l = torch.tensor([value, 3.0, 2.0], dtype=torch.float64)
+        if score == "softmax":
+            want = torch.full((3,), math.nan, dtype=torch.float64)
+        else:
+            want = torch.sigmoid(l)
+            want = want / want.sum() if renormalize else want
+        got = r.weights.double().cpu()
+        assert torch.equal(got.isnan(), want.isnan().expand(m, 3))
+        # exponentials and logarithms good to two steps, a quotient, sums of three: under 16 roundings
+        assert bool(((got - want).abs()[~got.isnan()] <= 16 * 2.0 ** -24).all())
